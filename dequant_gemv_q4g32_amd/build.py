@@ -25,7 +25,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqgemv.so")
 
 HOST_SOURCES = ["host.cpp"]
-DEVICE_SOURCES = ["gemv.hip", "prefill.hip", "skinny.hip", "kvcache.hip"] + sorted(
+DEVICE_SOURCES = ["gemv.hip", "prefill.hip", "skinny.hip", "kvcache.hip", "paged_kv.hip", "paged_attn.hip"] + sorted(
     f for f in os.listdir(CSRC) if f.startswith("mv_") and f.endswith(".hip"))   # streaming launchers per format
 ARCH = "gfx950"
 

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "../../include/qgemv.h"
+#include "kv_pages.h"
 #include "layout.h"
 
 namespace qg {
@@ -703,8 +704,17 @@ const char *qg_strerror(int status) {
     case QG_ERR_FORMAT: return "unknown format or bit width";
     case QG_ERR_LAUNCH: return "the HIP runtime refused a kernel launch";
     case QG_ERR_DEVICE: return "no usable gfx950 device or HIP runtime error";
+    case QG_ERR_WORKSPACE: return "the workspace is smaller than the call needs";
     default: return "unknown status";
   }
+}
+
+int qg_kv_page_bytes(int kind, int64_t kv_heads, int64_t head_dim, int64_t page_tokens, int64_t *bytes) {
+  if (!bytes) return QG_ERR_NULL;
+  KvLayout L;
+  if (int st = kv_layout(kind, kv_heads, head_dim, page_tokens, &L)) return st;
+  *bytes = L.page_bytes;
+  return QG_OK;
 }
 
 int qg_canonical_bytes(int fmt, int64_t n, int64_t k, int64_t *bytes) {

@@ -125,7 +125,8 @@ typedef enum qg_status {
   QG_ERR_RANGE = -5,     /* d or dmin does not fit fp16 (section 2.3's overflow warning)     */
   QG_ERR_FORMAT = -6,    /* unknown format or bit width                                     */
   QG_ERR_LAUNCH = -7,    /* the HIP runtime refused a launch                                 */
-  QG_ERR_DEVICE = -8     /* no usable gfx950 device / HIP runtime error                       */
+  QG_ERR_DEVICE = -8,    /* no usable gfx950 device / HIP runtime error                       */
+  QG_ERR_WORKSPACE = -9  /* the workspace is smaller than the call needs                      */
 } qg_status;
 
 #define QG_MAX_PLANES 4
@@ -359,6 +360,132 @@ int qg_kv_quantize(const uint16_t *src, int64_t ld_src, int64_t rows, int64_t co
                    void *stream);
 int qg_kv_dequantize(const int8_t *codes, const uint16_t *scales, int64_t rows, int64_t cols, uint16_t *dst,
                      int64_t ld_dst, void *stream);
+
+/* ---- paged KV cache (device) ---------------------------------------------------------------
+ * A cache of many sequences in pages of page_tokens tokens each, which grow, branch and end
+ * without moving each other ("二三五六位量化" page section 4.1 sizes the cache that these pages
+ * hold: one K and one V entry of head_dim elements for every token, KV head and layer).
+ *
+ * A pool is [layers][num_pages] page records, layer l at pages + l * layer_stride bytes (records
+ * are dense, layer_stride is read only when layers > 1). A record (qg_kv_page_bytes) holds, for
+ * each KV head in turn, page_tokens (T) consecutive tokens of D = head_dim elements:
+ *   QG_KV_Q8   K codes int8 [T][D], V codes int8 [T][D], K scales fp16 [T][D/32], V scales fp16
+ *              [D/32][T]: the groups of 32, codes and scales of qg_kv_quantize. A cached value is
+ *              what qg_kv_dequantize gives: d * q rounded once to fp16, saturated at +-65504.
+ *   QG_KV_F16  K fp16 [T][D], V fp16 [T][D].
+ * pages and layer_stride are 16-byte aligned; head_dim is 64, 128 or 256; page_tokens is a power
+ * of two from 16 to 256; kv_heads is 1 to 1024, layers 1 to 65535, num_pages 1 to 2^31 - 1.
+ *
+ * Sequences are rows of a page table, int32 [table_rows][ld_table] on the device, of which the
+ * first table_pages entries are used: token j of row s lies in page table[s][j / T] at place
+ * j % T. An entry outside [0, num_pages) names no page (-1 by convention): nothing is read or
+ * written there. lens, int32 [table_rows], holds the sequences' lengths in tokens (below 0
+ * counts as 0, past table_pages * T as that), refs, int32 [num_pages], how many rows hold a
+ * page (0: the page is free). All of them are device memory, so that every call below can be
+ * captured into a graph and replayed while the cache changes. One table serves all layers.
+ * Calls that read what another call writes are ordered by the caller (one stream, or events).
+ *
+ * Errors of all these calls: QG_ERR_NULL, QG_ERR_FORMAT (kind), QG_ERR_SHAPE, QG_ERR_ALIGN,
+ * QG_ERR_LAUNCH. A call with nothing to do (count, batch or table_rows 0) is a no-op. */
+typedef enum qg_kv_kind { QG_KV_Q8 = 1, QG_KV_F16 = 2 } qg_kv_kind;
+
+typedef struct qg_kv_pool {
+  void *pages;
+  int64_t num_pages;
+  int64_t layers;
+  int64_t layer_stride;
+  int32_t kind;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t page_tokens;
+} qg_kv_pool;
+
+/* Bytes of one page record (host). Errors: QG_ERR_NULL, QG_ERR_FORMAT, QG_ERR_SHAPE. */
+int qg_kv_page_bytes(int kind, int64_t kv_heads, int64_t head_dim, int64_t page_tokens, int64_t *bytes);
+
+/* Append: for i < count, K row k + i * ldk and V row v + i * ldv (fp16 [kv_heads * head_dim],
+ * finite) are quantized (QG_KV_Q8) or copied (QG_KV_F16) into `layer` of the pool as token
+ * positions[i] of table row seqs[i] (seqs NULL: row i). A row that names no place (a row outside
+ * the table, a position below 0 or past table_pages * T, an entry that is no page) is skipped,
+ * which is how a padded batch marks its empty rows. The count rows must name distinct places:
+ * two rows written to one place leave a mix of both there. Nothing else of a page changes.
+ * k, v: 16-byte aligned, ldk and ldv multiples of 8 and at least kv_heads * head_dim when
+ * count > 1. count * kv_heads * head_dim / 8 must be below 2^31. */
+int qg_kv_append(const qg_kv_pool *pool, int64_t layer, const int32_t *table, int64_t ld_table, int64_t table_rows,
+                 int64_t table_pages, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                 const int32_t *seqs, const int32_t *positions, int64_t count, void *stream);
+
+/* The way back: row i of k and v becomes the cached K and V of token positions[i] of row
+ * seqs[i], zeros where that names no place. Rows may repeat. This gives a cached prefix as the
+ * dense matrices that a prefill over it multiplies. Sizes and alignment as qg_kv_append. */
+int qg_kv_gather(const qg_kv_pool *pool, int64_t layer, const int32_t *table, int64_t ld_table, int64_t table_rows,
+                 int64_t table_pages, uint16_t *k, int64_t ldk, uint16_t *v, int64_t ldv, const int32_t *seqs,
+                 const int32_t *positions, int64_t count, void *stream);
+
+/* Attention of one new token a sequence over its cache: for b < batch, h < heads, with
+ * g = h / (heads / kv_heads) and n = lens[b] clamped to [0, max_len],
+ *   s_j = scale * <q[b][h], K[g][j]>   for the tokens max(0, n - window) <= j < n (all j < n
+ *                                      when window is 0) that lie in a page of the pool,
+ *   out[b][h] = sum_j e^(s_j) V[g][j] / sum_j e^(s_j),   lse[b][h] = ln sum_j e^(s_j).
+ * A sequence without such a token gets out = 0 and lse = -inf. q: fp16, row b at q + b * ldq,
+ * heads dense; out: fp16, or fp32 with out_f32 != 0, row b at out + b * ldo, heads dense; lse:
+ * fp32 [batch][heads], or NULL. The new token's own K and V are in the cache before the call
+ * (qg_kv_append) and counted by lens. Products, the softmax and its sums are fp32; the weights
+ * e^(s_j - max) meet V as a pair of fp16 numbers (their rounding and its remainder, 22 bits),
+ * so that fp32 out is good to about 1e-6 and fp16 out to its one rounding.
+ *
+ * The cache's length is split over the workgroups, whose partial results go through
+ * `workspace` (device, 16-byte aligned, at least qg_paged_attention_bytes; its contents need no
+ * preparation, and calls that may run at the same time each need their own). The split follows
+ * lens on the device, so a captured call follows lens as it changes; the result depends on the
+ * split only by rounding, and equal inputs give equal bits. max_len bounds the lengths (a graph
+ * that is replayed while sequences grow passes the longest it will see); the table has at least
+ * ceil(max_len / T) entries a row. q and out: 16-byte aligned, ldq a multiple of 8 (ldo of 8, of
+ * 4 for fp32) and at least heads * head_dim when batch > 1. heads is a multiple of kv_heads;
+ * batch * heads is at most 2^24, max_len at most 2^30, window >= 0, scale finite.
+ * Errors: also QG_ERR_WORKSPACE, and QG_ERR_RANGE for a scale that is not finite. */
+int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_len, int64_t *bytes);
+int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q, int64_t ldq, const int32_t *table,
+                       int64_t ld_table, const int32_t *lens, int64_t batch, int64_t heads, int64_t max_len,
+                       int64_t window, float scale, void *out, int64_t ldo, int out_f32, float *lse, void *workspace,
+                       int64_t workspace_bytes, void *stream);
+
+/* Copy whole pages in every layer: page src[i] to page dst[i] for i < count (device arrays). A
+ * pair with an index outside [0, num_pages) is skipped. No page may be a destination twice, or
+ * both a source and a destination of different pairs. count is at most 2^23 (also of forks and
+ * freed rows below). */
+int qg_kv_copy_pages(const qg_kv_pool *pool, const int32_t *src, const int32_t *dst, int64_t count, void *stream);
+
+/* Fork: for i < count, table row dst_rows[i] becomes a second holder of row src_rows[i]'s
+ * tokens. Its whole pages are shared (refs + 1 each); a last page that is only partly filled is
+ * copied in every layer to page new_pages[i], whose refs become 1, so that the two rows grow
+ * apart. Further entries of the row become -1 and lens[dst] = lens[src]. What the row held
+ * before is overwritten, not released (qg_kv_free releases it). new_pages[i] is read only when
+ * a last page is copied. A fork is skipped, its row left as it was, when a row is outside the
+ * table, when dst_rows[i] is also a source row or an earlier destination row of the call, or
+ * when a copy is needed and new_pages[i] is outside the pool or named earlier in the call. */
+int qg_kv_fork(const qg_kv_pool *pool, int32_t *table, int64_t ld_table, int64_t table_rows, int64_t table_pages,
+               int32_t *lens, int32_t *refs, const int32_t *src_rows, const int32_t *dst_rows,
+               const int32_t *new_pages, int64_t count, void *stream);
+
+/* Free: for i < count, table row rows[i] gives up its pages (refs - 1 for each page of its
+ * lens tokens), its table_pages entries become -1 and its length 0. A row outside the table, or
+ * one that is empty already (named twice, for instance), is left as it is. */
+int qg_kv_free(const qg_kv_pool *pool, int32_t *table, int64_t ld_table, int64_t table_rows, int64_t table_pages,
+               int32_t *lens, int32_t *refs, const int32_t *rows, int64_t count, void *stream);
+
+/* Compact: with L pages held (refs > 0), the held pages at index L and above move, in every
+ * layer, to the free pages below L (both in ascending order), after which the pages from L on
+ * are free and that end of the pool can be given back. remap, int32 [num_pages], receives each
+ * page's new index (-1 for a free page), live, int32 [1], receives L, refs_out the moved counts
+ * and table_out the table with its entries replaced (-1 where the page was free or no page).
+ * table_out and refs_out may be table and refs themselves; else they must not overlap them.
+ * workspace (4-byte aligned): at least qg_kv_compact_bytes, as for qg_paged_attention.
+ * num_pages is at most 2^24 here. Errors: also QG_ERR_WORKSPACE. */
+int qg_kv_compact_bytes(const qg_kv_pool *pool, int64_t *bytes);
+int qg_kv_compact(const qg_kv_pool *pool, const int32_t *table, int64_t ld_table, int32_t *table_out, int64_t ld_out,
+                  int64_t table_rows, int64_t table_pages, const int32_t *refs, int32_t *refs_out, int32_t *remap,
+                  int32_t *live, void *workspace, int64_t workspace_bytes, void *stream);
 
 /* ---- decode to memory (device; for verification, not for inference) ----------------------
  * Writes W_hat as fp32 [n][k] to w_out (if non-NULL) and the integer codes as uint8 [n][k]
