@@ -366,7 +366,6 @@ class KVPool:
         self._c = _Pool(pages.data_ptr(), self.num_pages, self.layers, pages.stride(0) if self.layers > 1 else 0,
                         KV_KINDS[kind], kv_heads, head_dim, page_tokens)
         self._ref = ctypes.addressof(self._c)
-        self._workspaces = {}
 
     @classmethod
     def zeros(cls, kind: str, kv_heads: int, head_dim: int, page_tokens: int, num_pages: int, layers: int = 1,
@@ -481,10 +480,6 @@ def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: 
     if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != pool.device
                                   or not workspace.is_contiguous()):
         raise ValueError(f"workspace must be dense uint8 on {pool.device}")
-    key = (batch, heads, max_len)
-    need = pool._workspaces.get(key)
-    if need is None:
-        need = pool._workspaces[key] = paged_attention_bytes(pool, batch, heads, max_len)
 
     def call(st):
         nonlocal out, lse
@@ -498,7 +493,9 @@ def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: 
         elif lse is not None and (lse.shape != (batch, heads) or lse.dtype != torch.float32 or lse.device != pool.device
                                   or not lse.is_contiguous()):
             raise ValueError(f"lse must be dense fp32 [{batch}, {heads}] on {pool.device}")
-        ws = torch.empty(need, dtype=torch.uint8, device=pool.device) if workspace is None else workspace
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(paged_attention_bytes(pool, batch, heads, max_len), dtype=torch.uint8, device=pool.device)
         _check(_lib.qg_paged_attention(pool._ref, layer, q.data_ptr(), q.stride(0), at, ld, lens_at, batch, heads, max_len,
                                        window, scale, out.data_ptr(), out.stride(0), int(out.dtype == torch.float32),
                                        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), st),

@@ -5,7 +5,6 @@
 
 #include "../../include/qgemv.h"
 #include "device_common.h"
-#include "kv_codec.h"
 #include "kv_pages.h"
 #include "launch.h"
 
@@ -22,110 +21,528 @@ struct AttnArgs {
   int64_t ld_table;
   const int32_t *lens;
   int32_t batch, heads, group;   // group = heads / kv_heads
+  int32_t tiles_per_kv, head_tiles;   // 16-head tiles of a KV head, and of all of them
+  int32_t rows;                  // heads of a tile that a partial result has room for
   int32_t max_len, window;
-  float scale;
+  float scale_log2;              // scale * log2(e)
   void *out;
   int64_t ldo;
   int32_t out_f32;
   float *lse;
+  float *slots;                  // workspace: two partial results a workgroup
 };
 
-// Eight elements of token `at` of a page, K (which = 0) or V, as fp32.
-template <int D, bool Q8>
-__device__ __forceinline__ void load8(const AttnArgs &a, const uint8_t *head, int which, int at, int e, float *f) {
-  u32x4 w;
-  if constexpr (Q8) {
-    const uint8_t *c = head + (which ? a.v_off : 0) + at * D + e;
-    const uint8_t *s = head + (which ? a.vs_off + 2 * (((e / 32) << a.tok_shift) + at) : a.ks_off + 2 * (at * (D / 32) + e / 32));
-    w = kv_decode8(ld2(c), half_bits(ldh(s)));
-  } else {
-    w = ld4(head + (which ? a.v_off : 0) + 2 * (at * D + e));
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 4;                          // waves of a workgroup
+constexpr int kTile = 32;                          // tokens of a wave's step: two 16-token blocks
+constexpr int kUnit = kWaves * kTile;              // tokens of a workgroup's step, the grain of the split
+constexpr int kThreads = 64 * kWaves;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+// Weights are 2^(s - ref) with ref moved to (largest s) - 7 once a score passes ref + 15: they
+// stay below fp16's 65504, and numbers down to 2^-31 of the largest keep their bits.
+constexpr float kLow = 7.0f, kHigh = 15.0f;
+
+template <typename T>
+__device__ __forceinline__ T uniform(T v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Read-only memory at a uniform address, through the scalar cache.
+__device__ __forceinline__ int32_t scalar_load(const int32_t *p) {
+  return *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)p;
+}
+
+// What of sequence b is seen: tokens [first, len), in tiles from base = first rounded down.
+struct Seen {
+  int32_t first, len, base, tiles, units;
+};
+__device__ __forceinline__ Seen seen_of(const AttnArgs &a, int32_t raw) {
+  Seen s;
+  s.len = min(max(raw, 0), a.max_len);
+  s.first = a.window ? max(0, s.len - a.window) : 0;
+  s.base = s.first & ~(kTile - 1);
+  s.tiles = (s.len - s.base + kTile - 1) / kTile;
+  s.units = max(1, (s.tiles + kWaves - 1) / kWaves);      // an empty sequence still gets its zeros written
+  return s;
+}
+
+// The split. All units of all sequences and head tiles, sequence by sequence and head tile by head
+// tile, are one line of `total` units; workgroup w of W takes [total * w / W, total * (w + 1) / W).
+// Every workgroup finds its place on the line from lens alone.
+struct Line {
+  int64_t total;
+  int32_t groups;            // workgroups that share it
+};
+__device__ __forceinline__ int64_t line_start(const Line &l, int32_t w) { return l.total * w / l.groups; }
+
+// Sum of `v` over the threads before this one; total: over all. lds: kWaves + 1 values.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *lds, int64_t &total) {
+  int64_t scan = v;
+  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t up = __shfl_up(scan, o);
+    scan += lane >= o ? up : 0;
   }
-  for (int j = 0; j < 4; ++j) {
-    f[2 * j] = half_lo(w[j]);
-    f[2 * j + 1] = half_hi(w[j]);
+  if (lane == 63) lds[threadIdx.x >> 6] = scan;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+  for (int w = 0; w < waves; ++w) {
+    const int64_t t = lds[w];
+    before += w < (int)(threadIdx.x >> 6) ? t : 0;
+    total += t;
+  }
+  return before + scan - v;
+}
+
+// 16 codes of one group to 16 fp16 values: code + 128 under the exponent of 1024 (a byte permute
+// and an exact subtraction for two), times the scale, rounded to fp16 as qg_kv_dequantize does.
+// MODE.FP16_OVFL (set at the start of the kernel) saturates the product at +-65504.
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t magic_pair, uint32_t scale) {
+  const h2_t off = __builtin_bit_cast(h2_t, 0x64806480u);       // 1152 = 1024 + 128
+  return __builtin_bit_cast(uint32_t, (__builtin_bit_cast(h2_t, magic_pair) - off) * __builtin_bit_cast(h2_t, scale));
+}
+constexpr uint32_t kMagicBytes = 0x64646464u;
+constexpr uint32_t kSelLow = 0x04010400u, kSelHigh = 0x04030402u;   // bytes 0, 1 and 2, 3 of the second operand under 0x64
+
+template <int D, bool Q8>
+struct Tile {
+  static constexpr int KD = D / 32;                 // matrix steps along the head
+  static constexpr int VJ = D / 16;                 // elements of one token's V a lane holds
+  static constexpr int KR = Q8 ? D / 64 : D / 32;   // 16-byte loads of a K row a lane takes part in
+  static constexpr int VW = Q8 ? VJ / 4 : VJ / 2;   // dwords of a V row a lane holds
+  u32x4 k[2][KR];
+  uint32_t ks[2][Q8 ? D / 64 : 1];
+  uint32_t v[8][VW];
+  u32x2 vs[2];
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
+  if constexpr (N == 1) {
+    w[0] = ld1(p);
+  } else if constexpr (N == 2) {
+    const u32x2 t = ld2(p);
+    w[0] = t.x;
+    w[1] = t.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const u32x4 t = ld4(p + 16 * i);
+      w[4 * i] = t.x;
+      w[4 * i + 1] = t.y;
+      w[4 * i + 2] = t.z;
+      w[4 * i + 3] = t.w;
+    }
   }
 }
 
-// One wave per (sequence, head): 64 tokens at a time, a lane scores one token, then holds
-// D / 64 elements of the output.
+// K of a tile: lane (c = lane % 16, g = lane / 16) takes token c of each 16-token block; of every 64
+// elements of its row the 16 at 16 g, eight for each of two matrix steps. head[st]: the KV head's part of the page of block st, at[st] the
+// block's first place in the page.
 template <int D, bool Q8>
-__global__ __launch_bounds__(64) void attn_kernel(AttnArgs a) {
-  __shared__ float qs[D], p[64], v[64][8];
-  const int b = blockIdx.x / a.heads, h = blockIdx.x - b * a.heads, lane = threadIdx.x;
-  const int len = min(max(a.lens[b], 0), a.max_len);
-  const int first = a.window ? max(0, len - a.window) : 0;
-  for (int e = lane; e < D; e += 64) qs[e] = half_bits(a.q[b * a.ldq + (int64_t)h * D + e]);
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, acc[D / 64] = {};
-  for (int t0 = first; t0 < len; t0 += 64) {
-    const int t = t0 + lane;
-    const uint8_t *head = nullptr;
-    if (t < len) {
-      const int page = a.table[b * a.ld_table + (t >> a.tok_shift)];
-      if (page >= 0 && page < a.num_pages) head = a.pool + page * a.page_bytes + (h / a.group) * a.head_bytes;
+__device__ __forceinline__ void load_k(const AttnArgs &a, const uint8_t *const *head, const int32_t *at, Tile<D, Q8> &t) {
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int st = 0; st < 2; ++st) {
+    const int row = at[st] + c;
+#pragma unroll
+    for (int i = 0; i < Tile<D, Q8>::KR; ++i)
+      t.k[st][i] = ld4(head[st] + (Q8 ? row * D + 64 * i + 16 * g : row * 2 * D + 128 * (i >> 1) + 32 * g + 16 * (i & 1)));
+    if constexpr (Q8) load_words<D / 64>(head[st] + a.ks_off + row * (D / 16), t.ks[st]);
+  }
+}
+
+// V of a tile: a lane takes the VJ elements at VJ * c of the tokens 4 g .. 4 g + 3 of each block.
+template <int D, bool Q8>
+__device__ __forceinline__ void load_v(const AttnArgs &a, const uint8_t *const *head, const int32_t *at, Tile<D, Q8> &t) {
+  constexpr int VJ = Tile<D, Q8>::VJ, VW = Tile<D, Q8>::VW;
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int st = 0; st < 2; ++st) {
+    const int row = at[st] + 4 * g;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_words<VW>(head[st] + a.v_off + ((row + i) * D + VJ * c) * (Q8 ? 1 : 2), t.v[4 * st + i]);
+    if constexpr (Q8) t.vs[st] = ld2(head[st] + a.vs_off + 2 * ((((VJ * c) / 32) << a.tok_shift) + row));
+  }
+}
+
+// Scores of a block: S^T [16 tokens x 16 heads] = K Q^T. Lane: head c, tokens 4 g + i.
+template <int D, bool Q8>
+__device__ __forceinline__ f32x4 scores(const Tile<D, Q8> &t, int st, const half8_t *q) {
+  f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+  if constexpr (Q8) {
+    const uint32_t pick = (threadIdx.x & 32) ? 0x03020302u : 0x01000100u;   // the group of the lane's 16 elements
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const uint32_t d = __builtin_amdgcn_perm(t.ks[st][i], t.ks[st][i], pick);
+      u32x4 w[2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t x = t.k[st][i][j] ^ 0x80808080u;
+        w[j >> 1][2 * (j & 1)] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, x, kSelLow), d);
+        w[j >> 1][2 * (j & 1) + 1] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, x, kSelHigh), d);
+      }
+      s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w[0]), q[2 * i], s, 0, 0, 0);
+      s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w[1]), q[2 * i + 1], s, 0, 0, 0);
     }
-    const int at = t & ((1 << a.tok_shift) - 1);
-    float s = 0.f;
-    if (head)
-      for (int e = 0; e < D; e += 8) {
-        float f[8];
-        load8<D, Q8>(a, head, 0, at, e, f);
-        for (int j = 0; j < 8; ++j) s = fmaf(qs[e + j], f[j], s);
+  } else {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, t.k[st][i]), q[i], s, 0, 0, 0);
+  }
+  return s;
+}
+
+// O^T += V^T P^T with the weights as hi + lo fp16 pairs. Column c of V^T's block j is element
+// VJ * c + j, so O^T's lane holds head c and elements VJ * (4 g + i) + j.
+template <int D, bool Q8>
+__device__ __forceinline__ void accumulate(const Tile<D, Q8> &t, half8_t hi, half8_t lo, f32x4 *o) {
+  constexpr int VW = Tile<D, Q8>::VW;
+#pragma unroll
+  for (int w = 0; w < VW; ++w) {
+    if constexpr (Q8) {
+      // two tokens' dwords interleave to bytes (t0 d, t1 d, t0 d+1, t1 d+1), then to fp16 pairs
+      u32x4 e[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t x0 = t.v[2 * p][w] ^ 0x80808080u, x1 = t.v[2 * p + 1][w] ^ 0x80808080u;
+        const uint32_t d = t.vs[p >> 1][p & 1];
+        const uint32_t a = __builtin_amdgcn_perm(x1, x0, 0x05010400u), b = __builtin_amdgcn_perm(x1, x0, 0x07030602u);
+        e[0][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, a, kSelLow), d);
+        e[1][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, a, kSelHigh), d);
+        e[2][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, b, kSelLow), d);
+        e[3][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, b, kSelHigh), d);
       }
-    s = head ? s * a.scale : -INFINITY;
-    float top = s;
-    for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    const float now = fmaxf(m, top);
-    const float base = now == -INFINITY ? 0.f : now;
-    const float w = head ? expf(s - base) : 0.f;
-    const float keep = expf(m - base);
-    m = now;
-    float sum = w;
-    for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
-    l = l * keep + sum;
-    for (int i = 0; i < D / 64; ++i) acc[i] *= keep;
-    p[lane] = w;
-    for (int e = 0; e < D; e += 8) {
-      float f[8] = {};
-      if (head) load8<D, Q8>(a, head, 1, at, e, f);
-      __syncthreads();
-      for (int j = 0; j < 8; ++j) v[lane][j] = head ? f[j] : 0.f;
-      __syncthreads();
-      // element e + j belongs to lane (e + j) % 64
-      const int j = lane - (e & 63);
-      if (j >= 0 && j < 8) {
-        float add = 0.f;
-        for (int k = 0; k < 64; ++k) add = fmaf(p[k], v[k][j], add);
-        for (int i = 0; i < D / 64; ++i)
-          if (i == e / 64) acc[i] += add;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        o[4 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), hi, o[4 * w + j], 0, 0, 0);
+        o[4 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), lo, o[4 * w + j], 0, 0, 0);
       }
+    } else {
+      u32x4 e[2];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        e[0][p] = __builtin_amdgcn_perm(t.v[2 * p + 1][w], t.v[2 * p][w], 0x05040100u);
+        e[1][p] = __builtin_amdgcn_perm(t.v[2 * p + 1][w], t.v[2 * p][w], 0x07060302u);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        o[2 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), hi, o[2 * w + j], 0, 0, 0);
+        o[2 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), lo, o[2 * w + j], 0, 0, 0);
+      }
+    }
+  }
+}
+
+// The pages of a tile's two blocks.
+struct Pages {
+  int32_t p[2];
+};
+__device__ __forceinline__ Pages tile_pages(const AttnArgs &a, const int32_t *row, const Seen &s, int32_t tile) {
+  Pages r;
+  for (int st = 0; st < 2; ++st) {
+    const int32_t t = s.base + tile * kTile + 16 * st;
+    const int32_t p = t < s.len ? scalar_load(row + (t >> a.tok_shift)) : -1;
+    r.p[st] = p >= 0 && p < a.num_pages ? p : -1;
+  }
+  return r;
+}
+
+// One partial result: the sums of a head tile over one workgroup's part of a sequence.
+__device__ __forceinline__ float *slot_of(const AttnArgs &a, int64_t slot, int D) {
+  return a.slots + slot * ((int64_t)a.rows * (D + 2));
+}
+
+template <int D>
+__device__ __forceinline__ void store_out(const AttnArgs &a, int32_t b, int32_t h, int d, float o, float l) {
+  const float y = l > 0.f ? o / l : l * o;          // no token: 0; NaN sums stay NaN
+  const int64_t at = b * a.ldo + (int64_t)h * D + d;
+  if (a.out_f32) static_cast<float *>(a.out)[at] = y;
+  else static_cast<uint16_t *>(a.out)[at] = __builtin_bit_cast(uint16_t, (_Float16)y);
+}
+
+template <int D, bool Q8>
+__global__ __launch_bounds__(kThreads) void attn_kernel(AttnArgs a) {
+  using T = Tile<D, Q8>;
+  constexpr int VJ = T::VJ;
+  extern __shared__ float sums[];                    // [kWaves][rows][D], rows = heads of a tile
+  __shared__ int64_t scan[kWaves + 1];
+  __shared__ int32_t found[1];
+  __shared__ int64_t found_at[1];
+  __shared__ float wave_m[kWaves][16], wave_l[kWaves][16];
+  const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
+  if constexpr (Q8) __builtin_amdgcn_s_setreg(1 | (23 << 6) | (0 << 11), 1);   // hwreg(MODE, 23, 1): FP16_OVFL
+
+  // this workgroup's part of the line
+  const int32_t per = (a.batch + kThreads - 1) / kThreads;
+  int64_t mine = 0;
+  for (int32_t i = 0; i < per; ++i) {
+    const int32_t b = (int32_t)threadIdx.x * per + i;
+    if (b < a.batch) mine += (int64_t)seen_of(a, a.lens[b]).units * a.head_tiles;
+  }
+  Line line;
+  const int64_t before = block_scan(mine, scan, line.total);
+  line.groups = (int32_t)(line.total < (int64_t)gridDim.x ? line.total : gridDim.x);
+  const int32_t w = blockIdx.x;
+  if (w >= line.groups) return;
+  int64_t at = line_start(line, w);
+  const int64_t end = line_start(line, w + 1);
+  if (at >= before && at < before + mine) {
+    int64_t u = before;
+    int32_t b = (int32_t)threadIdx.x * per;
+    for (;; ++b) {
+      const int64_t n = (int64_t)seen_of(a, a.lens[b]).units * a.head_tiles;
+      if (at < u + n) break;
+      u += n;
+    }
+    found[0] = b;
+    found_at[0] = u;
+  }
+  __syncthreads();
+  int32_t b = uniform(found[0]);
+  int64_t u0 = found_at[0];                          // the line's unit where sequence b starts
+  u0 = ((int64_t)uniform((int32_t)(u0 >> 32)) << 32) | (uint32_t)uniform((int32_t)u0);
+  at = ((int64_t)uniform((int32_t)(at >> 32)) << 32) | (uint32_t)uniform((int32_t)at);
+
+  const int64_t start = at;
+  while (at < end) {
+    Seen s = seen_of(a, scalar_load(a.lens + b));
+    int64_t rel = at - u0;
+    if (rel >= (int64_t)s.units * a.head_tiles) {
+      u0 += (int64_t)s.units * a.head_tiles;
+      ++b;
+      continue;
+    }
+    const int32_t ht = (int32_t)(rel / s.units);
+    const int32_t unit0 = (int32_t)(rel - (int64_t)ht * s.units);
+    const int64_t left = end - at;
+    const int32_t unit1 = (int32_t)(left < s.units - unit0 ? unit0 + left : s.units);
+    const int32_t kvh = ht / a.tiles_per_kv, first_head = (ht - kvh * a.tiles_per_kv) * 16;
+    const int32_t h0 = kvh * a.group + first_head, rows = min(16, a.group - first_head);
+    const int32_t *row = a.table + b * a.ld_table;
+    const uint8_t *kv = a.pool + kvh * a.head_bytes;
+
+    half8_t q[T::KD];
+#pragma unroll
+    for (int i = 0; i < T::KD; ++i) {
+      const int e = 64 * (i >> 1) + 16 * g + 8 * (i & 1);
+      u32x4 x = u32x4{0, 0, 0, 0};
+      if (c < rows) x = ld4(reinterpret_cast<const uint8_t *>(a.q + b * a.ldq + (int64_t)(h0 + c) * D + e));
+      q[i] = __builtin_bit_cast(half8_t, x);
+    }
+    f32x4 o[VJ];
+#pragma unroll
+    for (int j = 0; j < VJ; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float ref = -INFINITY, l = 0.f;
+
+    const int32_t last = min(unit1 * kWaves, s.tiles);
+    int32_t tile = unit0 * kWaves + wave;
+    T t;
+    const uint8_t *head[2];
+    int32_t place[2];
+    Pages pg, next;
+    auto locate = [&](const Pages &p, int32_t tl) {
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        head[st] = kv + (int64_t)max(p.p[st], 0) * a.page_bytes;
+        place[st] = p.p[st] < 0 ? 0 : (s.base + tl * kTile + 16 * st) & ((1 << a.tok_shift) - 1);
+      }
+    };
+    if (tile < last) {
+      pg = tile_pages(a, row, s, tile);
+      locate(pg, tile);
+      load_k<D, Q8>(a, head, place, t);
+      load_v<D, Q8>(a, head, place, t);
+      next = tile_pages(a, row, s, tile + kWaves);
+    }
+    while (tile < last) {
+      f32x4 x[2];
+#pragma unroll
+      for (int st = 0; st < 2; ++st) x[st] = scores<D, Q8>(t, st, q);
+      const int32_t t0 = s.base + tile * kTile;
+      const bool full = t0 >= s.first && t0 + kTile <= s.len && pg.p[0] >= 0 && pg.p[1] >= 0;
+      const int32_t after = tile + kWaves;
+      if (after < last) {
+        locate(next, after);
+        load_k<D, Q8>(a, head, place, t);
+      }
+      uint32_t valid = 0xFF;                         // of the lane's eight tokens
+      if (!full) {
+        valid = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int32_t tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+          valid |= (uint32_t)(tok >= s.first && tok < s.len && pg.p[i >> 2] >= 0) << i;
+        }
+      }
+      float y[8], top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y[i] = x[i >> 2][i & 3] * a.scale_log2;
+        if (!full && !(valid >> i & 1)) y[i] = -INFINITY;
+        top = fmaxf(top, y[i]);
+      }
+      if (__any(top > ref + kHigh)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float now = fmaxf(ref, top - kLow);
+        const float keep = now == ref ? 1.0f : __builtin_amdgcn_exp2f(ref - now);
+        ref = now;
+        l *= keep;
+#pragma unroll
+        for (int j = 0; j < VJ; ++j) o[j] *= keep;
+      }
+      half8_t hi, lo;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float p = __builtin_amdgcn_exp2f(y[i] - ref);
+        if (!full && !(valid >> i & 1)) p = 0.f;
+        l += p;
+        hi[i] = (_Float16)p;
+        lo[i] = (_Float16)(p - (float)hi[i]);
+      }
+      if (!full) {                                   // masked places may hold anything: zero times NaN is NaN
+        if constexpr (Q8) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t m = (valid >> i & 1) ? 0u : (i & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+            t.vs[i >> 2][(i & 3) >> 1] &= ~m;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < T::VW; ++k) t.v[i][k] = (valid >> i & 1) ? t.v[i][k] : 0u;
+        }
+      }
+      accumulate<D, Q8>(t, hi, lo, o);
+      if (after < last) {
+        load_v<D, Q8>(a, head, place, t);
+        pg = next;
+        next = tile_pages(a, row, s, after + kWaves);
+      }
+      tile = after;
+    }
+
+    // join the four waves
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    __syncthreads();
+    if (g == 0) {
+      wave_m[wave][c] = ref;
+      wave_l[wave][c] = l;
     }
     __syncthreads();
+    if (c < rows) {
+      float m = wave_m[0][c];
+      for (int k = 1; k < kWaves; ++k) m = fmaxf(m, wave_m[k][c]);
+      const float f = ref == m ? 1.0f : __builtin_amdgcn_exp2f(ref - m);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < VJ; j += 4)
+          *reinterpret_cast<f32x4 *>(sums + ((wave * rows + c) * D + VJ * (4 * g + i) + j)) =
+              f32x4{o[j][i] * f, o[j + 1][i] * f, o[j + 2][i] * f, o[j + 3][i] * f};
+    }
+    __syncthreads();
+    const bool whole = unit0 == 0 && unit1 == s.units;
+    float *slot = slot_of(a, 2 * (int64_t)w + (at == start ? 0 : 1), D);
+    for (int i = threadIdx.x; i < rows * D; i += kThreads) {
+      const int r = i / D, d = i - r * D;
+      float m = wave_m[0][r], sum = 0.f, den = 0.f;
+      for (int k = 1; k < kWaves; ++k) m = fmaxf(m, wave_m[k][r]);
+      for (int k = 0; k < kWaves; ++k) {
+        sum += sums[(k * rows + r) * D + d];
+        den += wave_l[k][r] * (wave_m[k][r] == m ? 1.0f : __builtin_amdgcn_exp2f(wave_m[k][r] - m));
+      }
+      if (whole) {
+        store_out<D>(a, b, h0 + r, d, sum, den);
+        if (d == 0 && a.lse) a.lse[(int64_t)b * a.heads + h0 + r] = (m + __log2f(den)) * kLn2;
+      } else {
+        slot[r * D + d] = sum;
+        if (d == 0) {
+          slot[a.rows * D + 2 * r] = m;
+          slot[a.rows * D + 2 * r + 1] = den;
+        }
+      }
+    }
+    at += unit1 - unit0;
   }
-  const float inv = l > 0.f ? 1.0f / l : l;     // a NaN stays one
-  for (int i = 0; i < D / 64; ++i) {
-    const int64_t o = b * a.ldo + (int64_t)h * D + 64 * i + lane;
-    const float y = acc[i] * inv;
-    if (a.out_f32) static_cast<float *>(a.out)[o] = y;
-    else static_cast<uint16_t *>(a.out)[o] = __builtin_bit_cast(uint16_t, (_Float16)y);
+}
+
+// Joins the parts of the head tiles that several workgroups shared: one workgroup for each sequence,
+// head tile and head.
+template <int D>
+__global__ __launch_bounds__(D) void attn_join_kernel(AttnArgs a, int32_t grid) {
+  __shared__ int64_t scan[kWaves + 1];
+  const int32_t b = blockIdx.x / a.head_tiles, ht = blockIdx.x - b * a.head_tiles, r = blockIdx.y;
+  const int32_t kvh = ht / a.tiles_per_kv, first_head = (ht - kvh * a.tiles_per_kv) * 16;
+  if (r >= a.group - first_head) return;
+  int64_t all = 0, before = 0;
+  for (int32_t k = threadIdx.x; k < a.batch; k += D) {
+    const int64_t n = (int64_t)seen_of(a, a.lens[k]).units * a.head_tiles;
+    all += n;
+    before += k < b ? n : 0;
   }
-  if (a.lse && lane == 0) a.lse[(int64_t)b * a.heads + h] = m + logf(l);
+  Line line;
+  block_scan(all, scan, line.total);
+  __syncthreads();
+  int64_t u0;
+  block_scan(before, scan, u0);
+  line.groups = (int32_t)(line.total < (int64_t)grid ? line.total : grid);
+  const Seen s = seen_of(a, scalar_load(a.lens + b));
+  u0 += (int64_t)ht * s.units;
+  const int64_t u1 = u0 + s.units;
+  // the workgroup that holds unit u is the last w with line_start(w) <= u
+  auto holder = [&](int64_t u) { return (int32_t)(((u + 1) * line.groups - 1) / line.total); };
+  const int32_t w0 = holder(u0), w1 = holder(u1 - 1);
+  if (w0 == w1) return;
+  auto slot = [&](int32_t w) { return slot_of(a, 2 * (int64_t)w + (line_start(line, w) < u0 ? 1 : 0), D); };
+  const int d = threadIdx.x;
+  float m = -INFINITY;
+  for (int32_t w = w0; w <= w1; ++w) m = fmaxf(m, slot(w)[a.rows * D + 2 * r]);
+  float sum = 0.f, den = 0.f;
+  for (int32_t w = w0; w <= w1; ++w) {
+    const float *p = slot(w);
+    const float mw = p[a.rows * D + 2 * r];
+    const float f = mw == m ? 1.0f : __builtin_amdgcn_exp2f(mw - m);
+    sum += p[r * D + d] * f;
+    den += p[a.rows * D + 2 * r + 1] * f;
+  }
+  const int32_t h = kvh * a.group + first_head + r;
+  store_out<D>(a, b, h, d, sum, den);
+  if (d == 0 && a.lse) a.lse[(int64_t)b * a.heads + h] = (m + __log2f(den)) * kLn2;
 }
 
 namespace {
 
 bool attn_misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
+// Workgroups: as many as the longest case has units for, at most kGrid.
+constexpr int64_t kGrid = 768;
+
+int32_t attn_grid(int64_t batch, int64_t head_tiles, int64_t max_len) {
+  const int64_t units = batch * head_tiles * ((max_len + kTile + kUnit - 1) / kUnit + 1);
+  return (int32_t)(units < kGrid ? units : kGrid);
+}
+
+template <int D, bool Q8>
+int launch_attn(const AttnArgs &a, int32_t grid, hipStream_t s) {
+  const size_t lds = sizeof(float) * kWaves * a.rows * D;
+  if (int st = launch(attn_kernel<D, Q8>, dim3(grid), dim3(kThreads), lds, s, a)) return st;
+  return launch(attn_join_kernel<D>, dim3((unsigned)(a.batch * a.head_tiles), (unsigned)a.rows), dim3(D), 0, s, a, grid);
+}
+
 template <int D>
-int launch_dim(const AttnArgs &a, bool q8, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)a.batch * a.heads)), block(64);
-  return q8 ? launch(attn_kernel<D, true>, grid, block, 0, s, a) : launch(attn_kernel<D, false>, grid, block, 0, s, a);
+int launch_dim(const AttnArgs &a, int32_t grid, bool q8, hipStream_t s) {
+  return q8 ? launch_attn<D, true>(a, grid, s) : launch_attn<D, false>(a, grid, s);
 }
 
 int attn_shape(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_len, KvLayout *L) {
   if (int st = kv_pool_layout(pool, L)) return st;
-  if (batch < 0 || heads < 1 || heads % pool->kv_heads || heads > (1 << 24) || batch > (1 << 24) / heads) return QG_ERR_SHAPE;
+  if (batch < 0 || heads < 1 || heads % pool->kv_heads || heads > (1 << 22) || batch > (1 << 22) / heads) return QG_ERR_SHAPE;
   if (max_len < 0 || max_len > (1 << 30)) return QG_ERR_SHAPE;
   return QG_OK;
 }
@@ -142,7 +559,10 @@ int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t head
   if (!bytes) return QG_ERR_NULL;
   KvLayout L;
   if (int st = attn_shape(pool, batch, heads, max_len, &L)) return st;
-  *bytes = 16;
+  const int64_t group = heads / pool->kv_heads, rows = group < 16 ? group : 16;
+  const int64_t slots = 2 * attn_grid(batch, (group + 15) / 16 * pool->kv_heads, max_len);
+  *bytes = 4 * slots * rows * (pool->head_dim + 2);
+  if (*bytes < 16) *bytes = 16;
   return QG_OK;
 }
 
@@ -182,19 +602,24 @@ int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q,
   a.batch = (int32_t)batch;
   a.heads = (int32_t)heads;
   a.group = (int32_t)(heads / pool->kv_heads);
+  a.tiles_per_kv = (a.group + 15) / 16;
+  a.head_tiles = a.tiles_per_kv * pool->kv_heads;
+  a.rows = a.group < 16 ? a.group : 16;
   a.max_len = (int32_t)max_len;
   a.window = (int32_t)(window > max_len ? 0 : window);
-  a.scale = scale;
+  a.scale_log2 = scale * kLog2e;
   a.out = out;
   a.ldo = batch > 1 ? ldo : cols;
   a.out_f32 = out_f32 != 0;
   a.lse = lse;
+  a.slots = static_cast<float *>(workspace);
+  const int32_t grid = attn_grid(batch, a.head_tiles, max_len);
   const bool q8 = pool->kind == QG_KV_Q8;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   switch (pool->head_dim) {
-    case 64: return launch_dim<64>(a, q8, s);
-    case 128: return launch_dim<128>(a, q8, s);
-    default: return launch_dim<256>(a, q8, s);
+    case 64: return launch_dim<64>(a, grid, q8, s);
+    case 128: return launch_dim<128>(a, grid, q8, s);
+    default: return launch_dim<256>(a, grid, q8, s);
   }
 }
 
