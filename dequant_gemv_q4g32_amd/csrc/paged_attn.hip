@@ -68,31 +68,44 @@ __device__ __forceinline__ Seen seen_of(const AttnArgs &a, int32_t raw) {
 }
 
 // The split. All units of all sequences and head tiles, sequence by sequence and head tile by head
-// tile, are one line of `total` units; workgroup w of W takes [total * w / W, total * (w + 1) / W).
-// Every workgroup finds its place on the line from lens alone.
+// tile, are one line of `total` units (below 2^31), of which workgroup w of `groups` takes the
+// w-th part: quota units, and one more if w < extra. Every workgroup finds its place on the line
+// from lens alone.
 struct Line {
-  int64_t total;
-  int32_t groups;            // workgroups that share it
+  uint32_t total, groups, quota, extra;
+  __device__ __forceinline__ uint32_t start(uint32_t w) const { return w * quota + min(w, extra); }
+  // the workgroup that holds unit u
+  __device__ __forceinline__ uint32_t holder(uint32_t u) const {
+    const uint32_t big = extra * (quota + 1);
+    return u < big ? u / (quota + 1) : extra + (u - big) / quota;
+  }
 };
-__device__ __forceinline__ int64_t line_start(const Line &l, int32_t w) { return l.total * w / l.groups; }
+__device__ __forceinline__ Line make_line(uint32_t total, uint32_t grid) {
+  Line l;
+  l.total = total;
+  l.groups = min(total, grid);
+  l.quota = total / l.groups;
+  l.extra = total - l.quota * l.groups;
+  return l;
+}
 
-// Sum of `v` over the threads before this one; total: over all. lds: kWaves + 1 values.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *lds, int64_t &total) {
-  int64_t scan = v;
+// Sum of `v` over the threads before this one; total: over all. lds: a value for each wave.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *lds, uint32_t &total) {
+  uint32_t scan = v;
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   for (int o = 1; o < 64; o <<= 1) {
-    const int64_t up = __shfl_up(scan, o);
+    const uint32_t up = __shfl_up(scan, o);
     scan += lane >= o ? up : 0;
   }
   if (lane == 63) lds[threadIdx.x >> 6] = scan;
   __syncthreads();
-  int64_t before = 0;
-  total = 0;
+  uint32_t before = 0, all = 0;
   for (int w = 0; w < waves; ++w) {
-    const int64_t t = lds[w];
+    const uint32_t t = lds[w];
     before += w < (int)(threadIdx.x >> 6) ? t : 0;
-    total += t;
+    all += t;
   }
+  total = uniform(all);
   return before + scan - v;
 }
 
@@ -118,53 +131,61 @@ struct Tile {
   u32x2 vs[2];
 };
 
+// A 16-token block in memory: its KV head's part of a page as a buffer resource, and the block's
+// first place in the page. A block without a page has an empty range, whose loads give zeros.
+struct Block {
+  rsrc_t r;
+  uint32_t place;
+};
+
+constexpr int kCache = 0;                            // cache policy of the loads
+
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
+__device__ __forceinline__ void load_words(rsrc_t r, uint32_t voff, uint32_t soff, uint32_t *w) {
   if constexpr (N == 1) {
-    w[0] = ld1(p);
+    w[0] = bldx1<kCache>(r, voff, soff);
   } else if constexpr (N == 2) {
-    const u32x2 t = ld2(p);
+    const u32x2 t = bldx2<kCache>(r, voff, soff);
     w[0] = t.x;
     w[1] = t.y;
   } else {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const u32x4 t = ld4(p + 16 * i);
-      w[4 * i] = t.x;
-      w[4 * i + 1] = t.y;
-      w[4 * i + 2] = t.z;
-      w[4 * i + 3] = t.w;
+      const u32x4 t = bldx4<kCache>(r, voff + 16 * i, soff);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[4 * i + j] = t[j];
     }
   }
 }
 
 // K of a tile: lane (c = lane % 16, g = lane / 16) takes token c of each 16-token block; of every 64
-// elements of its row the 16 at 16 g, eight for each of two matrix steps. head[st]: the KV head's part of the page of block st, at[st] the
-// block's first place in the page.
+// elements of its row the 16 at 16 g, eight for each of two matrix steps. The lane's part of an
+// address never changes: what does (page, place) is scalar.
 template <int D, bool Q8>
-__device__ __forceinline__ void load_k(const AttnArgs &a, const uint8_t *const *head, const int32_t *at, Tile<D, Q8> &t) {
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void load_k(const AttnArgs &a, const Block *blk, Tile<D, Q8> &t) {
+  const uint32_t lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int st = 0; st < 2; ++st) {
-    const int row = at[st] + c;
 #pragma unroll
     for (int i = 0; i < Tile<D, Q8>::KR; ++i)
-      t.k[st][i] = ld4(head[st] + (Q8 ? row * D + 64 * i + 16 * g : row * 2 * D + 128 * (i >> 1) + 32 * g + 16 * (i & 1)));
-    if constexpr (Q8) load_words<D / 64>(head[st] + a.ks_off + row * (D / 16), t.ks[st]);
+      t.k[st][i] = Q8 ? bldx4<kCache>(blk[st].r, c * D + 16 * g + 64 * i, blk[st].place * D)
+                      : bldx4<kCache>(blk[st].r, c * 2 * D + 32 * g + 128 * (i >> 1) + 16 * (i & 1), blk[st].place * 2 * D);
+    if constexpr (Q8) load_words<D / 64>(blk[st].r, c * (D / 16), a.ks_off + blk[st].place * (D / 16), t.ks[st]);
   }
 }
 
 // V of a tile: a lane takes the VJ elements at VJ * c of the tokens 4 g .. 4 g + 3 of each block.
 template <int D, bool Q8>
-__device__ __forceinline__ void load_v(const AttnArgs &a, const uint8_t *const *head, const int32_t *at, Tile<D, Q8> &t) {
-  constexpr int VJ = Tile<D, Q8>::VJ, VW = Tile<D, Q8>::VW;
-  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+__device__ __forceinline__ void load_v(const AttnArgs &a, const Block *blk, uint32_t vs_lane, Tile<D, Q8> &t) {
+  constexpr uint32_t VJ = Tile<D, Q8>::VJ, VW = Tile<D, Q8>::VW, kElem = Q8 ? 1 : 2;
+  const uint32_t lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int st = 0; st < 2; ++st) {
-    const int row = at[st] + 4 * g;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_words<VW>(head[st] + a.v_off + ((row + i) * D + VJ * c) * (Q8 ? 1 : 2), t.v[4 * st + i]);
-    if constexpr (Q8) t.vs[st] = ld2(head[st] + a.vs_off + 2 * ((((VJ * c) / 32) << a.tok_shift) + row));
+    for (int i = 0; i < 4; ++i)
+      load_words<VW>(blk[st].r, (4 * g * D + VJ * c) * kElem + i * D * kElem, a.v_off + blk[st].place * (D * kElem),
+                     t.v[4 * st + i]);
+    if constexpr (Q8) t.vs[st] = bldx2<kCache>(blk[st].r, vs_lane, a.vs_off + 2 * blk[st].place);
   }
 }
 
@@ -236,20 +257,6 @@ __device__ __forceinline__ void accumulate(const Tile<D, Q8> &t, half8_t hi, hal
   }
 }
 
-// The pages of a tile's two blocks.
-struct Pages {
-  int32_t p[2];
-};
-__device__ __forceinline__ Pages tile_pages(const AttnArgs &a, const int32_t *row, const Seen &s, int32_t tile) {
-  Pages r;
-  for (int st = 0; st < 2; ++st) {
-    const int32_t t = s.base + tile * kTile + 16 * st;
-    const int32_t p = t < s.len ? scalar_load(row + (t >> a.tok_shift)) : -1;
-    r.p[st] = p >= 0 && p < a.num_pages ? p : -1;
-  }
-  return r;
-}
-
 // One partial result: the sums of a head tile over one workgroup's part of a sequence.
 __device__ __forceinline__ float *slot_of(const AttnArgs &a, int64_t slot, int D) {
   return a.slots + slot * ((int64_t)a.rows * (D + 2));
@@ -263,127 +270,164 @@ __device__ __forceinline__ void store_out(const AttnArgs &a, int32_t b, int32_t 
   else static_cast<uint16_t *>(a.out)[at] = __builtin_bit_cast(uint16_t, (_Float16)y);
 }
 
+// A workgroup's part of one head tile of one sequence, and a wave's tiles of it.
+struct Segment {
+  uint32_t at, n;            // its units on the line
+  int32_t b;
+  uint32_t seq_at;           // where sequence b starts on the line
+  int32_t first, len, base;  // what of the sequence is seen
+  int32_t kvh, h0, rows;     // KV head, first head, heads
+  int32_t tile, last;        // this wave's tiles: tile, tile + kWaves, ... below last
+  bool whole;                // all units of the head tile
+};
+
+// The segment at unit `at` < end, at or after sequence b, which starts at seq_at.
+__device__ __forceinline__ Segment segment_at(const AttnArgs &a, uint32_t at, uint32_t end, int32_t b, uint32_t seq_at,
+                                             int32_t wave) {
+  Segment g;
+  Seen s = seen_of(a, scalar_load(a.lens + b));
+  while (at - seq_at >= (uint32_t)s.units * a.head_tiles) {
+    seq_at += (uint32_t)s.units * a.head_tiles;
+    ++b;
+    s = seen_of(a, scalar_load(a.lens + b));
+  }
+  const uint32_t rel = at - seq_at, ht = rel / (uint32_t)s.units, unit0 = rel - ht * (uint32_t)s.units;
+  g.at = at;
+  g.n = min(end - at, (uint32_t)s.units - unit0);
+  g.b = b;
+  g.seq_at = seq_at;
+  g.first = s.first;
+  g.len = s.len;
+  g.base = s.base;
+  g.kvh = (int32_t)ht / a.tiles_per_kv;
+  const int32_t first_head = ((int32_t)ht - g.kvh * a.tiles_per_kv) * 16;
+  g.h0 = g.kvh * a.group + first_head;
+  g.rows = min(16, a.group - first_head);
+  g.tile = (int32_t)unit0 * kWaves + wave;
+  g.last = min((int32_t)(unit0 + g.n) * kWaves, s.tiles);
+  g.whole = g.n == (uint32_t)s.units;
+  return g;
+}
+
 template <int D, bool Q8>
-__global__ __launch_bounds__(kThreads) void attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnArgs a) {
   using T = Tile<D, Q8>;
   constexpr int VJ = T::VJ;
   extern __shared__ float sums[];                    // [kWaves][rows][D], rows = heads of a tile
-  __shared__ int64_t scan[kWaves + 1];
-  __shared__ int32_t found[1];
-  __shared__ int64_t found_at[1];
+  __shared__ uint32_t scan[kWaves], found[2];
   __shared__ float wave_m[kWaves][16], wave_l[kWaves][16];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
   if constexpr (Q8) __builtin_amdgcn_s_setreg(1 | (23 << 6) | (0 << 11), 1);   // hwreg(MODE, 23, 1): FP16_OVFL
+  const uint32_t vs_lane = 2 * ((((VJ * (uint32_t)c) / 32) << a.tok_shift) + 4 * g);   // the lane's V scales
 
   // this workgroup's part of the line
-  const int32_t per = (a.batch + kThreads - 1) / kThreads;
-  int64_t mine = 0;
-  for (int32_t i = 0; i < per; ++i) {
-    const int32_t b = (int32_t)threadIdx.x * per + i;
-    if (b < a.batch) mine += (int64_t)seen_of(a, a.lens[b]).units * a.head_tiles;
-  }
-  Line line;
-  const int64_t before = block_scan(mine, scan, line.total);
-  line.groups = (int32_t)(line.total < (int64_t)gridDim.x ? line.total : gridDim.x);
-  const int32_t w = blockIdx.x;
+  const int32_t per = (a.batch + kThreads - 1) / kThreads, my_b = (int32_t)threadIdx.x * per;
+  uint32_t mine = 0;
+  for (int32_t i = 0; i < per; ++i)
+    if (my_b + i < a.batch) mine += (uint32_t)seen_of(a, a.lens[my_b + i]).units * a.head_tiles;
+  uint32_t total;
+  const uint32_t before = block_scan(mine, scan, total);
+  const Line line = make_line(total, gridDim.x);
+  const uint32_t w = blockIdx.x;
   if (w >= line.groups) return;
-  int64_t at = line_start(line, w);
-  const int64_t end = line_start(line, w + 1);
-  if (at >= before && at < before + mine) {
-    int64_t u = before;
-    int32_t b = (int32_t)threadIdx.x * per;
-    for (;; ++b) {
-      const int64_t n = (int64_t)seen_of(a, a.lens[b]).units * a.head_tiles;
-      if (at < u + n) break;
-      u += n;
-    }
-    found[0] = b;
-    found_at[0] = u;
+  const uint32_t start = line.start(w), end = line.start(w + 1);
+  if (start >= before && start - before < mine) {
+    found[0] = (uint32_t)my_b;
+    found[1] = before;
   }
   __syncthreads();
-  int32_t b = uniform(found[0]);
-  int64_t u0 = found_at[0];                          // the line's unit where sequence b starts
-  u0 = ((int64_t)uniform((int32_t)(u0 >> 32)) << 32) | (uint32_t)uniform((int32_t)u0);
-  at = ((int64_t)uniform((int32_t)(at >> 32)) << 32) | (uint32_t)uniform((int32_t)at);
 
-  const int64_t start = at;
-  while (at < end) {
-    Seen s = seen_of(a, scalar_load(a.lens + b));
-    int64_t rel = at - u0;
-    if (rel >= (int64_t)s.units * a.head_tiles) {
-      u0 += (int64_t)s.units * a.head_tiles;
-      ++b;
-      continue;
+  T t;
+  half8_t q[T::KD];
+  Block blk[2];
+  int32_t page[2] = {-1, -1};                        // of the tile in t; below 0: none
+  Segment cur = segment_at(a, start, end, (int32_t)uniform(found[0]), uniform(found[1]), wave);
+  Segment fetch = cur;                               // the segment of the tile in t, fetch.tile that tile
+  bool loaded = true;                                // whether t holds a tile
+
+  // moves fetch to the wave's next tile from fetch.tile on; false: there is none
+  auto settle = [&]() {
+    while (fetch.tile >= fetch.last) {
+      if (fetch.at + fetch.n >= end) return false;
+      fetch = segment_at(a, fetch.at + fetch.n, end, fetch.b, fetch.seq_at, wave);
     }
-    const int32_t ht = (int32_t)(rel / s.units);
-    const int32_t unit0 = (int32_t)(rel - (int64_t)ht * s.units);
-    const int64_t left = end - at;
-    const int32_t unit1 = (int32_t)(left < s.units - unit0 ? unit0 + left : s.units);
-    const int32_t kvh = ht / a.tiles_per_kv, first_head = (ht - kvh * a.tiles_per_kv) * 16;
-    const int32_t h0 = kvh * a.group + first_head, rows = min(16, a.group - first_head);
-    const int32_t *row = a.table + b * a.ld_table;
-    const uint8_t *kv = a.pool + kvh * a.head_bytes;
-
-    half8_t q[T::KD];
+    return true;
+  };
+  auto tile_page = [&](int st) {
+    const int32_t tok = fetch.base + fetch.tile * kTile + 16 * st;
+    const int32_t p = tok < fetch.len ? scalar_load(a.table + fetch.b * a.ld_table + (tok >> a.tok_shift)) : -1;
+    return p >= 0 && p < a.num_pages ? p : -1;
+  };
+  auto locate = [&]() {
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      blk[st].r = make_rsrc(a.pool + fetch.kvh * a.head_bytes + (int64_t)max(page[st], 0) * a.page_bytes,
+                            page[st] < 0 ? 0u : (uint32_t)a.head_bytes);
+      blk[st].place = (uint32_t)(fetch.base + fetch.tile * kTile + 16 * st) & ((1u << a.tok_shift) - 1);
+    }
+  };
+  auto load_q = [&]() {
 #pragma unroll
     for (int i = 0; i < T::KD; ++i) {
-      const int e = 64 * (i >> 1) + 16 * g + 8 * (i & 1);
       u32x4 x = u32x4{0, 0, 0, 0};
-      if (c < rows) x = ld4(reinterpret_cast<const uint8_t *>(a.q + b * a.ldq + (int64_t)(h0 + c) * D + e));
+      if (c < fetch.rows)
+        x = ld4(reinterpret_cast<const uint8_t *>(a.q + fetch.b * a.ldq + (int64_t)(fetch.h0 + c) * D + 64 * (i >> 1) + 16 * g +
+                                                  8 * (i & 1)));
       q[i] = __builtin_bit_cast(half8_t, x);
     }
+  };
+
+  loaded = settle();
+  if (loaded) {
+    page[0] = tile_page(0);
+    page[1] = tile_page(1);
+    locate();
+    load_q();
+    load_k<D, Q8>(a, blk, t);
+    load_v<D, Q8>(a, blk, vs_lane, t);
+  }
+  for (;;) {
     f32x4 o[VJ];
 #pragma unroll
     for (int j = 0; j < VJ; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     float ref = -INFINITY, l = 0.f;
-
-    const int32_t last = min(unit1 * kWaves, s.tiles);
-    int32_t tile = unit0 * kWaves + wave;
-    T t;
-    const uint8_t *head[2];
-    int32_t place[2];
-    Pages pg, next;
-    auto locate = [&](const Pages &p, int32_t tl) {
-#pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        head[st] = kv + (int64_t)max(p.p[st], 0) * a.page_bytes;
-        place[st] = p.p[st] < 0 ? 0 : (s.base + tl * kTile + 16 * st) & ((1 << a.tok_shift) - 1);
-      }
-    };
-    if (tile < last) {
-      pg = tile_pages(a, row, s, tile);
-      locate(pg, tile);
-      load_k<D, Q8>(a, head, place, t);
-      load_v<D, Q8>(a, head, place, t);
-      next = tile_pages(a, row, s, tile + kWaves);
-    }
-    while (tile < last) {
-      f32x4 x[2];
-#pragma unroll
-      for (int st = 0; st < 2; ++st) x[st] = scores<D, Q8>(t, st, q);
-      const int32_t t0 = s.base + tile * kTile;
-      const bool full = t0 >= s.first && t0 + kTile <= s.len && pg.p[0] >= 0 && pg.p[1] >= 0;
-      const int32_t after = tile + kWaves;
-      if (after < last) {
-        locate(next, after);
-        load_k<D, Q8>(a, head, place, t);
-      }
+    while (loaded && fetch.at == cur.at) {
+      const int32_t t0 = cur.base + fetch.tile * kTile;
+      const bool full = t0 >= cur.first && t0 + kTile <= cur.len && page[0] >= 0 && page[1] >= 0;
       uint32_t valid = 0xFF;                         // of the lane's eight tokens
       if (!full) {
         valid = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int32_t tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
-          valid |= (uint32_t)(tok >= s.first && tok < s.len && pg.p[i >> 2] >= 0) << i;
+          valid |= (uint32_t)(tok >= cur.first && tok < cur.len && page[i >> 2] >= 0) << i;
         }
+      }
+      // the next tile's pages are on their way while this one's scores are made, its K while the
+      // softmax and the products with V are, its V from then on: also across segments
+      fetch.tile += kWaves;
+      loaded = settle();
+      if (loaded) {
+        page[0] = tile_page(0);
+        page[1] = tile_page(1);
+      }
+      f32x4 x[2];
+#pragma unroll
+      for (int st = 0; st < 2; ++st) x[st] = scores<D, Q8>(t, st, q);
+      if (loaded) {
+        locate();
+        load_k<D, Q8>(a, blk, t);
+        if (fetch.at != cur.at) load_q();
       }
       float y[8], top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        y[i] = x[i >> 2][i & 3] * a.scale_log2;
-        if (!full && !(valid >> i & 1)) y[i] = -INFINITY;
-        top = fmaxf(top, y[i]);
+      for (int i = 0; i < 8; ++i) y[i] = x[i >> 2][i & 3] * a.scale_log2;
+      if (!full) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = (valid >> i & 1) ? y[i] : -INFINITY;
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
       if (__any(top > ref + kHigh)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -394,16 +438,12 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnArgs a) {
 #pragma unroll
         for (int j = 0; j < VJ; ++j) o[j] *= keep;
       }
-      half8_t hi, lo;
+      float p[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float p = __builtin_amdgcn_exp2f(y[i] - ref);
-        if (!full && !(valid >> i & 1)) p = 0.f;
-        l += p;
-        hi[i] = (_Float16)p;
-        lo[i] = (_Float16)(p - (float)hi[i]);
-      }
+      for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(y[i] - ref);
       if (!full) {                                   // masked places may hold anything: zero times NaN is NaN
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = (valid >> i & 1) ? p[i] : 0.f;
         if constexpr (Q8) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -417,13 +457,15 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnArgs a) {
             for (int k = 0; k < T::VW; ++k) t.v[i][k] = (valid >> i & 1) ? t.v[i][k] : 0u;
         }
       }
-      accumulate<D, Q8>(t, hi, lo, o);
-      if (after < last) {
-        load_v<D, Q8>(a, head, place, t);
-        pg = next;
-        next = tile_pages(a, row, s, after + kWaves);
+      half8_t hi, lo;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        l += p[i];
+        hi[i] = (_Float16)p[i];
+        lo[i] = (_Float16)(p[i] - (float)hi[i]);
       }
-      tile = after;
+      accumulate<D, Q8>(t, hi, lo, o);
+      if (loaded) load_v<D, Q8>(a, blk, vs_lane, t);
     }
 
     // join the four waves
@@ -435,6 +477,7 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnArgs a) {
       wave_l[wave][c] = l;
     }
     __syncthreads();
+    const int32_t rows = cur.rows;
     if (c < rows) {
       float m = wave_m[0][c];
       for (int k = 1; k < kWaves; ++k) m = fmaxf(m, wave_m[k][c]);
@@ -447,8 +490,7 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnArgs a) {
               f32x4{o[j][i] * f, o[j + 1][i] * f, o[j + 2][i] * f, o[j + 3][i] * f};
     }
     __syncthreads();
-    const bool whole = unit0 == 0 && unit1 == s.units;
-    float *slot = slot_of(a, 2 * (int64_t)w + (at == start ? 0 : 1), D);
+    float *slot = slot_of(a, 2 * (int64_t)w + (cur.at == start ? 0 : 1), D);
     for (int i = threadIdx.x; i < rows * D; i += kThreads) {
       const int r = i / D, d = i - r * D;
       float m = wave_m[0][r], sum = 0.f, den = 0.f;
@@ -457,9 +499,9 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnArgs a) {
         sum += sums[(k * rows + r) * D + d];
         den += wave_l[k][r] * (wave_m[k][r] == m ? 1.0f : __builtin_amdgcn_exp2f(wave_m[k][r] - m));
       }
-      if (whole) {
-        store_out<D>(a, b, h0 + r, d, sum, den);
-        if (d == 0 && a.lse) a.lse[(int64_t)b * a.heads + h0 + r] = (m + __log2f(den)) * kLn2;
+      if (cur.whole) {
+        store_out<D>(a, cur.b, cur.h0 + r, d, sum, den);
+        if (d == 0 && a.lse) a.lse[(int64_t)cur.b * a.heads + cur.h0 + r] = (m + __log2f(den)) * kLn2;
       } else {
         slot[r * D + d] = sum;
         if (d == 0) {
@@ -468,48 +510,74 @@ __global__ __launch_bounds__(kThreads) void attn_kernel(AttnArgs a) {
         }
       }
     }
-    at += unit1 - unit0;
+    if (cur.at + cur.n >= end) break;
+    cur = segment_at(a, cur.at + cur.n, end, cur.b, cur.seq_at, wave);
   }
 }
 
 // Joins the parts of the head tiles that several workgroups shared: one workgroup for each sequence,
-// head tile and head.
+// head tile and head. The parts' largest scores and sums are read at once, then the threads share
+// out the parts, each holding one element of the output.
+constexpr int kGrid = 512;                           // workgroups of attn_kernel at most
+
 template <int D>
-__global__ __launch_bounds__(D) void attn_join_kernel(AttnArgs a, int32_t grid) {
-  __shared__ int64_t scan[kWaves + 1];
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_t grid) {
+  constexpr int kSplit = kThreads / D;               // threads of an element
+  __shared__ uint32_t scan[kWaves];
+  __shared__ float red[kWaves], factor[kGrid], sums[kThreads];
+  __shared__ uint32_t slots[kGrid];
   const int32_t b = blockIdx.x / a.head_tiles, ht = blockIdx.x - b * a.head_tiles, r = blockIdx.y;
   const int32_t kvh = ht / a.tiles_per_kv, first_head = (ht - kvh * a.tiles_per_kv) * 16;
   if (r >= a.group - first_head) return;
-  int64_t all = 0, before = 0;
-  for (int32_t k = threadIdx.x; k < a.batch; k += D) {
-    const int64_t n = (int64_t)seen_of(a, a.lens[k]).units * a.head_tiles;
+  uint32_t all = 0, before = 0;
+  for (int32_t k = threadIdx.x; k < a.batch; k += kThreads) {
+    const uint32_t n = (uint32_t)seen_of(a, a.lens[k]).units * a.head_tiles;
     all += n;
     before += k < b ? n : 0;
   }
-  Line line;
-  block_scan(all, scan, line.total);
+  uint32_t total, u0;
+  block_scan(all, scan, total);
   __syncthreads();
-  int64_t u0;
   block_scan(before, scan, u0);
-  line.groups = (int32_t)(line.total < (int64_t)grid ? line.total : grid);
+  const Line line = make_line(total, grid);
   const Seen s = seen_of(a, scalar_load(a.lens + b));
-  u0 += (int64_t)ht * s.units;
-  const int64_t u1 = u0 + s.units;
-  // the workgroup that holds unit u is the last w with line_start(w) <= u
-  auto holder = [&](int64_t u) { return (int32_t)(((u + 1) * line.groups - 1) / line.total); };
-  const int32_t w0 = holder(u0), w1 = holder(u1 - 1);
-  if (w0 == w1) return;
-  auto slot = [&](int32_t w) { return slot_of(a, 2 * (int64_t)w + (line_start(line, w) < u0 ? 1 : 0), D); };
-  const int d = threadIdx.x;
+  u0 += (uint32_t)ht * (uint32_t)s.units;
+  const uint32_t w0 = line.holder(u0), w1 = line.holder(u0 + s.units - 1), n = w1 - w0 + 1;
+  if (n == 1) return;
+  // a workgroup's part is its second result if it starts before the head tile does
   float m = -INFINITY;
-  for (int32_t w = w0; w <= w1; ++w) m = fmaxf(m, slot(w)[a.rows * D + 2 * r]);
-  float sum = 0.f, den = 0.f;
-  for (int32_t w = w0; w <= w1; ++w) {
-    const float *p = slot(w);
-    const float mw = p[a.rows * D + 2 * r];
-    const float f = mw == m ? 1.0f : __builtin_amdgcn_exp2f(mw - m);
-    sum += p[r * D + d] * f;
-    den += p[a.rows * D + 2 * r + 1] * f;
+  for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+    const uint32_t slot = 2 * (w0 + i) + (line.start(w0 + i) < u0 ? 1 : 0);
+    slots[i] = slot;
+    factor[i] = slot_of(a, slot, D)[a.rows * D + 2 * r];
+    m = fmaxf(m, factor[i]);
+  }
+  for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  float den = 0.f;
+  for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+    const float f = factor[i] == m ? 1.0f : __builtin_amdgcn_exp2f(factor[i] - m);
+    factor[i] = f;
+    den += slot_of(a, slots[i], D)[a.rows * D + 2 * r + 1] * f;
+  }
+  for (int o = 32; o; o >>= 1) den += __shfl_xor(den, o);
+  __syncthreads();                                   // red is read, factor written
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = den;
+  __syncthreads();
+  den = (red[0] + red[1]) + (red[2] + red[3]);
+  const int d = threadIdx.x & (D - 1), part = threadIdx.x / D;
+  const float *p = a.slots + r * D + d;
+  const int64_t stride = (int64_t)a.rows * (D + 2);
+  float sum = 0.f;
+#pragma unroll 8
+  for (uint32_t i = part; i < n; i += kSplit) sum += p[slots[i] * stride] * factor[i];
+  if constexpr (kSplit > 1) {
+    sums[threadIdx.x] = sum;
+    __syncthreads();
+    if (part) return;
+    for (int k = 1; k < kSplit; ++k) sum += sums[k * D + d];
   }
   const int32_t h = kvh * a.group + first_head + r;
   store_out<D>(a, b, h, d, sum, den);
@@ -520,30 +588,43 @@ namespace {
 
 bool attn_misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
-// Workgroups: as many as the longest case has units for, at most kGrid.
-constexpr int64_t kGrid = 768;
+// Units of a head tile of the longest sequence: of max_len tokens, or of a window that starts
+// anywhere in a tile.
+int64_t attn_units(int64_t max_len, int64_t window) {
+  int64_t tiles = (max_len + kTile - 1) / kTile;
+  if (window > 0 && window < max_len) {
+    const int64_t seen = (window + kTile - 2) / kTile + 1;
+    tiles = seen < tiles ? seen : tiles;
+  }
+  const int64_t units = (tiles + kWaves - 1) / kWaves;
+  return units > 1 ? units : 1;
+}
 
-int32_t attn_grid(int64_t batch, int64_t head_tiles, int64_t max_len) {
-  const int64_t units = batch * head_tiles * ((max_len + kTile + kUnit - 1) / kUnit + 1);
-  return (int32_t)(units < kGrid ? units : kGrid);
+int32_t attn_grid(int64_t batch, int64_t head_tiles, int64_t units) {
+  const int64_t all = batch * head_tiles * units;
+  return (int32_t)(all < kGrid ? all : kGrid);
 }
 
 template <int D, bool Q8>
-int launch_attn(const AttnArgs &a, int32_t grid, hipStream_t s) {
+int launch_attn(const AttnArgs &a, int64_t units, hipStream_t s) {
+  const int32_t grid = attn_grid(a.batch, a.head_tiles, units);
   const size_t lds = sizeof(float) * kWaves * a.rows * D;
   if (int st = launch(attn_kernel<D, Q8>, dim3(grid), dim3(kThreads), lds, s, a)) return st;
-  return launch(attn_join_kernel<D>, dim3((unsigned)(a.batch * a.head_tiles), (unsigned)a.rows), dim3(D), 0, s, a, grid);
+  if (units == 1) return QG_OK;                      // every head tile is one workgroup's
+  return launch(attn_join_kernel<D>, dim3((unsigned)(a.batch * a.head_tiles), (unsigned)a.rows), dim3(kThreads), 0, s, a,
+                (uint32_t)grid);
 }
 
 template <int D>
-int launch_dim(const AttnArgs &a, int32_t grid, bool q8, hipStream_t s) {
-  return q8 ? launch_attn<D, true>(a, grid, s) : launch_attn<D, false>(a, grid, s);
+int launch_dim(const AttnArgs &a, int64_t units, bool q8, hipStream_t s) {
+  return q8 ? launch_attn<D, true>(a, units, s) : launch_attn<D, false>(a, units, s);
 }
 
 int attn_shape(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_len, KvLayout *L) {
   if (int st = kv_pool_layout(pool, L)) return st;
   if (batch < 0 || heads < 1 || heads % pool->kv_heads || heads > (1 << 22) || batch > (1 << 22) / heads) return QG_ERR_SHAPE;
   if (max_len < 0 || max_len > (1 << 30)) return QG_ERR_SHAPE;
+  if (batch * heads * attn_units(max_len, 0) > 0x7FFFFFFF) return QG_ERR_SHAPE;   // the line's units fit 31 bits
   return QG_OK;
 }
 
@@ -560,7 +641,7 @@ int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t head
   KvLayout L;
   if (int st = attn_shape(pool, batch, heads, max_len, &L)) return st;
   const int64_t group = heads / pool->kv_heads, rows = group < 16 ? group : 16;
-  const int64_t slots = 2 * attn_grid(batch, (group + 15) / 16 * pool->kv_heads, max_len);
+  const int64_t slots = 2 * attn_grid(batch, (group + 15) / 16 * pool->kv_heads, attn_units(max_len, 0));
   *bytes = 4 * slots * rows * (pool->head_dim + 2);
   if (*bytes < 16) *bytes = 16;
   return QG_OK;
@@ -613,13 +694,13 @@ int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q,
   a.out_f32 = out_f32 != 0;
   a.lse = lse;
   a.slots = static_cast<float *>(workspace);
-  const int32_t grid = attn_grid(batch, a.head_tiles, max_len);
+  const int64_t units = attn_units(max_len, a.window);
   const bool q8 = pool->kind == QG_KV_Q8;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   switch (pool->head_dim) {
-    case 64: return launch_dim<64>(a, grid, q8, s);
-    case 128: return launch_dim<128>(a, grid, q8, s);
-    default: return launch_dim<256>(a, grid, q8, s);
+    case 64: return launch_dim<64>(a, units, q8, s);
+    case 128: return launch_dim<128>(a, units, q8, s);
+    default: return launch_dim<256>(a, units, q8, s);
   }
 }
 
