@@ -33,11 +33,12 @@ struct AttnArgs {
 };
 
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;                          // waves of a workgroup
-constexpr int kTile = 32;                          // tokens of a wave's step: two 16-token blocks
-constexpr int kUnit = kWaves * kTile;              // tokens of a workgroup's step, the grain of the split
+constexpr int kTile = 32;                          // tokens of a wave's step, the grain of the split: two 16-token blocks
 constexpr int kThreads = 64 * kWaves;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -55,26 +56,29 @@ __device__ __forceinline__ int32_t scalar_load(const int32_t *p) {
 
 // What of sequence b is seen: tokens [first, len), in tiles from base = first rounded down.
 struct Seen {
-  int32_t first, len, base, tiles, units;
+  int32_t first, len, base, tiles;
 };
 __device__ __forceinline__ Seen seen_of(const AttnArgs &a, int32_t raw) {
   Seen s;
   s.len = min(max(raw, 0), a.max_len);
   s.first = a.window ? max(0, s.len - a.window) : 0;
   s.base = s.first & ~(kTile - 1);
-  s.tiles = (s.len - s.base + kTile - 1) / kTile;
-  s.units = max(1, (s.tiles + kWaves - 1) / kWaves);      // an empty sequence still gets its zeros written
+  s.tiles = max(1, (s.len - s.base + kTile - 1) / kTile);      // an empty sequence still gets its zeros written
   return s;
 }
 
-// The split. All units of all sequences and head tiles, sequence by sequence and head tile by head
-// tile, are one line of `total` units (below 2^31), of which workgroup w of `groups` takes the
-// w-th part: quota units, and one more if w < extra. Every workgroup finds its place on the line
-// from lens alone.
+// The split. All tiles of all sequences and head tiles, sequence by sequence and head tile by head
+// tile, are one line of `total` tiles (below 2^31), of which wave v of `waves` takes the v-th part:
+// quota tiles, and one more if v < extra. Every wave finds its place on the line from lens alone.
+// A head tile [u0, u1) of the line is thus covered by neighbouring waves. A wave that goes on
+// past u1 (its range ends beyond) has left the head tile behind as a part of its own; the waves whose
+// range ends within the head tile end on it, and those of one workgroup join their parts. So the
+// parts of a head tile are: one for each workgroup with such waves (named by the first of them,
+// the leader), and one for a wave that goes on past u1.
 struct Line {
-  uint32_t total, groups, quota, extra;
-  __device__ __forceinline__ uint32_t start(uint32_t w) const { return w * quota + min(w, extra); }
-  // the workgroup that holds unit u
+  uint32_t total, waves, quota, extra;
+  __device__ __forceinline__ uint32_t start(uint32_t v) const { return v * quota + min(v, extra); }
+  // the wave that holds tile u
   __device__ __forceinline__ uint32_t holder(uint32_t u) const {
     const uint32_t big = extra * (quota + 1);
     return u < big ? u / (quota + 1) : extra + (u - big) / quota;
@@ -83,9 +87,9 @@ struct Line {
 __device__ __forceinline__ Line make_line(uint32_t total, uint32_t grid) {
   Line l;
   l.total = total;
-  l.groups = min(total, grid);
-  l.quota = total / l.groups;
-  l.extra = total - l.quota * l.groups;
+  l.waves = min(total, grid * kWaves);
+  l.quota = total / l.waves;
+  l.extra = total - l.quota * l.waves;
   return l;
 }
 
@@ -257,9 +261,10 @@ __device__ __forceinline__ void accumulate(const Tile<D, Q8> &t, half8_t hi, hal
   }
 }
 
-// One partial result: the sums of a head tile over one workgroup's part of a sequence.
-__device__ __forceinline__ float *slot_of(const AttnArgs &a, int64_t slot, int D) {
-  return a.slots + slot * ((int64_t)a.rows * (D + 2));
+// A part in the workspace: [rows][D] sums, then each row's largest score and denominator. Slot 2 v:
+// what wave v left behind; slot 2 v + 1: what the waves of its workgroup from v on ended on.
+__device__ __forceinline__ float *slot_of(const AttnArgs &a, uint32_t slot, int D) {
+  return a.slots + (int64_t)slot * (a.rows * (D + 2));
 }
 
 template <int D>
@@ -270,268 +275,299 @@ __device__ __forceinline__ void store_out(const AttnArgs &a, int32_t b, int32_t 
   else static_cast<uint16_t *>(a.out)[at] = __builtin_bit_cast(uint16_t, (_Float16)y);
 }
 
-// A workgroup's part of one head tile of one sequence, and a wave's tiles of it.
+// A wave's part of one head tile of one sequence.
 struct Segment {
-  uint32_t at, n;            // its units on the line
+  uint32_t u0, u1;           // the head tile on the line
+  uint32_t at, end;          // the wave's part of it
   int32_t b;
-  uint32_t seq_at;           // where sequence b starts on the line
   int32_t first, len, base;  // what of the sequence is seen
-  int32_t kvh, h0, rows;     // KV head, first head, heads
-  int32_t tile, last;        // this wave's tiles: tile, tile + kWaves, ... below last
-  bool whole;                // all units of the head tile
+  int32_t ht, h0, rows;      // head tile of the sequence, its first head, heads
 };
 
-// The segment at unit `at` < end, at or after sequence b, which starts at seq_at.
-__device__ __forceinline__ Segment segment_at(const AttnArgs &a, uint32_t at, uint32_t end, int32_t b, uint32_t seq_at,
-                                             int32_t wave) {
+// The segment at tile `at` < end of the line, at or after sequence b, which starts at seq_at.
+__device__ __forceinline__ Segment segment_at(const AttnArgs &a, uint32_t at, uint32_t end, int32_t b, uint32_t seq_at) {
   Segment g;
   Seen s = seen_of(a, scalar_load(a.lens + b));
-  while (at - seq_at >= (uint32_t)s.units * a.head_tiles) {
-    seq_at += (uint32_t)s.units * a.head_tiles;
+  while (at - seq_at >= (uint32_t)s.tiles * a.head_tiles) {
+    seq_at += (uint32_t)s.tiles * a.head_tiles;
     ++b;
     s = seen_of(a, scalar_load(a.lens + b));
   }
-  const uint32_t rel = at - seq_at, ht = rel / (uint32_t)s.units, unit0 = rel - ht * (uint32_t)s.units;
+  g.ht = (int32_t)((at - seq_at) / (uint32_t)s.tiles);
+  g.u0 = seq_at + (uint32_t)g.ht * s.tiles;
+  g.u1 = g.u0 + s.tiles;
   g.at = at;
-  g.n = min(end - at, (uint32_t)s.units - unit0);
+  g.end = min(end, g.u1);
   g.b = b;
-  g.seq_at = seq_at;
   g.first = s.first;
   g.len = s.len;
   g.base = s.base;
-  g.kvh = (int32_t)ht / a.tiles_per_kv;
-  const int32_t first_head = ((int32_t)ht - g.kvh * a.tiles_per_kv) * 16;
-  g.h0 = g.kvh * a.group + first_head;
+  const int32_t kvh = g.ht / a.tiles_per_kv, first_head = (g.ht - kvh * a.tiles_per_kv) * 16;
+  g.h0 = kvh * a.group + first_head;
   g.rows = min(16, a.group - first_head);
-  g.tile = (int32_t)unit0 * kWaves + wave;
-  g.last = min((int32_t)(unit0 + g.n) * kWaves, s.tiles);
-  g.whole = g.n == (uint32_t)s.units;
   return g;
 }
 
+// Output rows of a whole head tile, or a part of one: 4 elements at d of row r.
+template <int D>
+__device__ __forceinline__ void store_result(const AttnArgs &a, const Segment &s, float *slot, int r, int d, f32x4 o, float m,
+                                             float l) {
+  if (slot) {
+    *reinterpret_cast<f32x2 *>(slot + r * D + d) = f32x2{o[0], o[1]};
+    *reinterpret_cast<f32x2 *>(slot + r * D + d + 2) = f32x2{o[2], o[3]};
+    if (d == 0) *reinterpret_cast<f32x2 *>(slot + a.rows * D + 2 * r) = f32x2{m, l};
+    return;
+  }
+  const int32_t h = s.h0 + r;
+  const int64_t at = s.b * a.ldo + (int64_t)h * D + d;
+  const float inv = l > 0.f ? 1.0f / l : l;          // no token: 0; NaN sums stay NaN
+  o *= inv;
+  if (a.out_f32) {
+    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = o;
+  } else {
+    half4_t y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = (_Float16)o[i];
+    *reinterpret_cast<half4_t *>(static_cast<uint16_t *>(a.out) + at) = y;
+  }
+  if (d == 0 && a.lse) a.lse[(int64_t)s.b * a.heads + h] = (m + __log2f(l)) * kLn2;
+}
+
 template <int D, bool Q8>
-__global__ __launch_bounds__(kThreads, 2) void attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_kernel(AttnArgs a) {
   using T = Tile<D, Q8>;
   constexpr int VJ = T::VJ;
-  extern __shared__ float sums[];                    // [kWaves][rows][D], rows = heads of a tile
-  __shared__ uint32_t scan[kWaves], found[2];
+  constexpr int kPad = D + 4;                        // LDS rows of neighbouring heads start in other banks
+  extern __shared__ float sums[];                    // [kWaves][rows][kPad], rows = heads of a tile
+  __shared__ uint32_t scan[kWaves], found[2][kWaves];
   __shared__ float wave_m[kWaves][16], wave_l[kWaves][16];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
   if constexpr (Q8) __builtin_amdgcn_s_setreg(1 | (23 << 6) | (0 << 11), 1);   // hwreg(MODE, 23, 1): FP16_OVFL
   const uint32_t vs_lane = 2 * ((((VJ * (uint32_t)c) / 32) << a.tok_shift) + 4 * g);   // the lane's V scales
 
-  // this workgroup's part of the line
+  // this workgroup's waves on the line
   const int32_t per = (a.batch + kThreads - 1) / kThreads, my_b = (int32_t)threadIdx.x * per;
   uint32_t mine = 0;
   for (int32_t i = 0; i < per; ++i)
-    if (my_b + i < a.batch) mine += (uint32_t)seen_of(a, a.lens[my_b + i]).units * a.head_tiles;
+    if (my_b + i < a.batch) mine += (uint32_t)seen_of(a, a.lens[my_b + i]).tiles * a.head_tiles;
   uint32_t total;
   const uint32_t before = block_scan(mine, scan, total);
   const Line line = make_line(total, gridDim.x);
-  const uint32_t w = blockIdx.x;
-  if (w >= line.groups) return;
-  const uint32_t start = line.start(w), end = line.start(w + 1);
-  if (start >= before && start - before < mine) {
-    found[0] = (uint32_t)my_b;
-    found[1] = before;
+  const uint32_t v0 = blockIdx.x * kWaves, v = v0 + wave;
+  if (v0 >= line.waves) return;
+  const uint32_t live = min((uint32_t)kWaves, line.waves - v0);   // waves with a part of the line
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) {
+    const uint32_t at = line.start(v0 + k);
+    if (at >= before && at - before < mine) {
+      found[0][k] = (uint32_t)my_b;
+      found[1][k] = before;
+    }
   }
   __syncthreads();
 
-  T t;
-  half8_t q[T::KD];
-  Block blk[2];
-  int32_t page[2] = {-1, -1};                        // of the tile in t; below 0: none
-  Segment cur = segment_at(a, start, end, (int32_t)uniform(found[0]), uniform(found[1]), wave);
-  Segment fetch = cur;                               // the segment of the tile in t, fetch.tile that tile
-  bool loaded = true;                                // whether t holds a tile
-
-  // moves fetch to the wave's next tile from fetch.tile on; false: there is none
-  auto settle = [&]() {
-    while (fetch.tile >= fetch.last) {
-      if (fetch.at + fetch.n >= end) return false;
-      fetch = segment_at(a, fetch.at + fetch.n, end, fetch.b, fetch.seq_at, wave);
-    }
-    return true;
-  };
-  auto tile_page = [&](int st) {
-    const int32_t tok = fetch.base + fetch.tile * kTile + 16 * st;
-    const int32_t p = tok < fetch.len ? scalar_load(a.table + fetch.b * a.ld_table + (tok >> a.tok_shift)) : -1;
-    return p >= 0 && p < a.num_pages ? p : -1;
-  };
-  auto locate = [&]() {
+  f32x4 o[VJ];
+  float ref = -INFINITY, l = 0.f;
+  Segment cur;
+  if ((uint32_t)wave < live) {
+    const uint32_t end = line.start(v + 1);
+    T t;
+    half8_t q[T::KD];
+    Block blk[2];
+    int32_t page[2];                                 // of the tile in t; below 0: none
+    cur = segment_at(a, line.start(v), end, (int32_t)uniform(found[0][wave]), uniform(found[1][wave]));
+    Segment fetch = cur;                             // the segment of the tile in t, fetch.at that tile
+    auto tile_page = [&](int st) {
+      const int32_t tok = fetch.base + (int32_t)(fetch.at - fetch.u0) * kTile + 16 * st;
+      const int32_t p = tok < fetch.len ? scalar_load(a.table + fetch.b * a.ld_table + (tok >> a.tok_shift)) : -1;
+      return p >= 0 && p < a.num_pages ? p : -1;
+    };
+    auto locate = [&]() {
 #pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      blk[st].r = make_rsrc(a.pool + fetch.kvh * a.head_bytes + (int64_t)max(page[st], 0) * a.page_bytes,
-                            page[st] < 0 ? 0u : (uint32_t)a.head_bytes);
-      blk[st].place = (uint32_t)(fetch.base + fetch.tile * kTile + 16 * st) & ((1u << a.tok_shift) - 1);
-    }
-  };
-  auto load_q = [&]() {
+      for (int st = 0; st < 2; ++st) {
+        blk[st].r = make_rsrc(a.pool + (fetch.ht / a.tiles_per_kv) * a.head_bytes + (int64_t)max(page[st], 0) * a.page_bytes,
+                              page[st] < 0 ? 0u : (uint32_t)a.head_bytes);
+        blk[st].place = (uint32_t)(fetch.base + (int32_t)(fetch.at - fetch.u0) * kTile + 16 * st) & ((1u << a.tok_shift) - 1);
+      }
+    };
+    auto load_q = [&]() {
 #pragma unroll
-    for (int i = 0; i < T::KD; ++i) {
-      u32x4 x = u32x4{0, 0, 0, 0};
-      if (c < fetch.rows)
-        x = ld4(reinterpret_cast<const uint8_t *>(a.q + fetch.b * a.ldq + (int64_t)(fetch.h0 + c) * D + 64 * (i >> 1) + 16 * g +
-                                                  8 * (i & 1)));
-      q[i] = __builtin_bit_cast(half8_t, x);
-    }
-  };
-
-  loaded = settle();
-  if (loaded) {
+      for (int i = 0; i < T::KD; ++i) {
+        u32x4 x = u32x4{0, 0, 0, 0};
+        if (c < fetch.rows)
+          x = ld4(reinterpret_cast<const uint8_t *>(a.q + fetch.b * a.ldq + (int64_t)(fetch.h0 + c) * D + 64 * (i >> 1) + 16 * g +
+                                                    8 * (i & 1)));
+        q[i] = __builtin_bit_cast(half8_t, x);
+      }
+    };
     page[0] = tile_page(0);
     page[1] = tile_page(1);
     locate();
     load_q();
     load_k<D, Q8>(a, blk, t);
     load_v<D, Q8>(a, blk, vs_lane, t);
-  }
-  for (;;) {
-    f32x4 o[VJ];
+    bool more = true;
+    while (more) {
 #pragma unroll
-    for (int j = 0; j < VJ; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float ref = -INFINITY, l = 0.f;
-    while (loaded && fetch.at == cur.at) {
-      const int32_t t0 = cur.base + fetch.tile * kTile;
-      const bool full = t0 >= cur.first && t0 + kTile <= cur.len && page[0] >= 0 && page[1] >= 0;
-      uint32_t valid = 0xFF;                         // of the lane's eight tokens
-      if (!full) {
-        valid = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int32_t tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
-          valid |= (uint32_t)(tok >= cur.first && tok < cur.len && page[i >> 2] >= 0) << i;
-        }
-      }
-      // the next tile's pages are on their way while this one's scores are made, its K while the
-      // softmax and the products with V are, its V from then on: also across segments
-      fetch.tile += kWaves;
-      loaded = settle();
-      if (loaded) {
-        page[0] = tile_page(0);
-        page[1] = tile_page(1);
-      }
-      f32x4 x[2];
-#pragma unroll
-      for (int st = 0; st < 2; ++st) x[st] = scores<D, Q8>(t, st, q);
-      if (loaded) {
-        locate();
-        load_k<D, Q8>(a, blk, t);
-        if (fetch.at != cur.at) load_q();
-      }
-      float y[8], top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = x[i >> 2][i & 3] * a.scale_log2;
-      if (!full) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = (valid >> i & 1) ? y[i] : -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
-      if (__any(top > ref + kHigh)) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float now = fmaxf(ref, top - kLow);
-        const float keep = now == ref ? 1.0f : __builtin_amdgcn_exp2f(ref - now);
-        ref = now;
-        l *= keep;
-#pragma unroll
-        for (int j = 0; j < VJ; ++j) o[j] *= keep;
-      }
-      float p[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(y[i] - ref);
-      if (!full) {                                   // masked places may hold anything: zero times NaN is NaN
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = (valid >> i & 1) ? p[i] : 0.f;
-        if constexpr (Q8) {
+      for (int j = 0; j < VJ; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      ref = -INFINITY;
+      l = 0.f;
+      bool inside = true;                            // the tile in t is of segment cur
+      while (inside) {
+        const int32_t t0 = cur.base + (int32_t)(fetch.at - cur.u0) * kTile;
+        const bool full = t0 >= cur.first && t0 + kTile <= cur.len && page[0] >= 0 && page[1] >= 0;
+        uint32_t valid = 0xFF;                       // of the lane's eight tokens
+        if (!full) {
+          valid = 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint32_t m = (valid >> i & 1) ? 0u : (i & 1) ? 0xFFFF0000u : 0x0000FFFFu;
-            t.vs[i >> 2][(i & 3) >> 1] &= ~m;
+            const int32_t tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+            valid |= (uint32_t)(tok >= cur.first && tok < cur.len && page[i >> 2] >= 0) << i;
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int k = 0; k < T::VW; ++k) t.v[i][k] = (valid >> i & 1) ? t.v[i][k] : 0u;
         }
-      }
-      half8_t hi, lo;
+        // the next tile's pages are on their way while this one's scores are made, its K while the
+        // softmax and the products with V are, its V from then on: also across segments
+        more = fetch.at + 1 < end;
+        if (++fetch.at == fetch.end) {
+          inside = false;
+          if (more) fetch = segment_at(a, fetch.at, end, fetch.b, fetch.u0 - (fetch.u1 - fetch.u0) * fetch.ht);
+        }
+        if (more) {
+          page[0] = tile_page(0);
+          page[1] = tile_page(1);
+        }
+        f32x4 x[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        l += p[i];
-        hi[i] = (_Float16)p[i];
-        lo[i] = (_Float16)(p[i] - (float)hi[i]);
+        for (int st = 0; st < 2; ++st) x[st] = scores<D, Q8>(t, st, q);
+        if (more) {
+          locate();
+          load_k<D, Q8>(a, blk, t);
+          if (!inside) load_q();
+        }
+        float y[8], top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[i >> 2][i & 3] * a.scale_log2;
+        if (!full) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = (valid >> i & 1) ? y[i] : -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
+        if (__any(top > ref + kHigh)) {
+          top = fmaxf(top, __shfl_xor(top, 16));
+          top = fmaxf(top, __shfl_xor(top, 32));
+          const float now = fmaxf(ref, top - kLow);
+          const float keep = now == ref ? 1.0f : __builtin_amdgcn_exp2f(ref - now);
+          ref = now;
+          l *= keep;
+#pragma unroll
+          for (int j = 0; j < VJ; ++j) o[j] *= keep;
+        }
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(y[i] - ref);
+        if (!full) {                                 // masked places may hold anything: zero times NaN is NaN
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[i] = (valid >> i & 1) ? p[i] : 0.f;
+          if constexpr (Q8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t m = (valid >> i & 1) ? 0u : (i & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+              t.vs[i >> 2][(i & 3) >> 1] &= ~m;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int k = 0; k < T::VW; ++k) t.v[i][k] = (valid >> i & 1) ? t.v[i][k] : 0u;
+          }
+        }
+        half8_t hi, lo;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          l += p[i];
+          hi[i] = (_Float16)p[i];
+          lo[i] = (_Float16)(p[i] - (float)hi[i]);
+        }
+        accumulate<D, Q8>(t, hi, lo, o);
+        if (more) load_v<D, Q8>(a, blk, vs_lane, t);
       }
-      accumulate<D, Q8>(t, hi, lo, o);
-      if (loaded) load_v<D, Q8>(a, blk, vs_lane, t);
+      l += __shfl_xor(l, 16);
+      l += __shfl_xor(l, 32);
+      if (more) {
+        // going on past this head tile: its result if the wave had all of it, else a part
+        float *slot = cur.at == cur.u0 ? nullptr : slot_of(a, 2 * v, D);
+        if (c < cur.rows) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < VJ; j += 4)
+              store_result<D>(a, cur, slot, c, VJ * (4 * g + i) + j, f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]}, ref,
+                              l);
+        }
+        cur = fetch;
+      }
     }
+  }
 
-    // join the four waves
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    __syncthreads();
-    if (g == 0) {
-      wave_m[wave][c] = ref;
-      wave_l[wave][c] = l;
-    }
-    __syncthreads();
-    const int32_t rows = cur.rows;
-    if (c < rows) {
-      float m = wave_m[0][c];
-      for (int k = 1; k < kWaves; ++k) m = fmaxf(m, wave_m[k][c]);
-      const float f = ref == m ? 1.0f : __builtin_amdgcn_exp2f(ref - m);
+  // the waves that ended on one head tile join their parts; the leader stores the sum
+  if ((uint32_t)wave < live && g == 0) {
+    wave_m[wave][c] = ref;
+    wave_l[wave][c] = l;
+  }
+  __syncthreads();
+  uint32_t lead = 0, tail = 0;                       // first and last wave that end on this wave's head tile
+  if ((uint32_t)wave < live) {
+    lead = tail = wave;
+    while (lead > 0 && line.start(v0 + lead) > cur.u0) --lead;
+    while (tail + 1 < live && line.start(v0 + tail + 2) <= cur.u1) ++tail;
+    float m = ref;
+    for (uint32_t k = lead; k <= tail; ++k) m = fmaxf(m, wave_m[k][c]);
+    const float f = ref == m ? 1.0f : __builtin_amdgcn_exp2f(ref - m);
+    if (c < cur.rows) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < VJ; j += 4)
-          *reinterpret_cast<f32x4 *>(sums + ((wave * rows + c) * D + VJ * (4 * g + i) + j)) =
+          *reinterpret_cast<f32x4 *>(sums + (wave * a.rows + c) * kPad + VJ * (4 * g + i) + j) =
               f32x4{o[j][i] * f, o[j + 1][i] * f, o[j + 2][i] * f, o[j + 3][i] * f};
     }
-    __syncthreads();
-    float *slot = slot_of(a, 2 * (int64_t)w + (cur.at == start ? 0 : 1), D);
-    for (int i = threadIdx.x; i < rows * D; i += kThreads) {
-      const int r = i / D, d = i - r * D;
-      float m = wave_m[0][r], sum = 0.f, den = 0.f;
-      for (int k = 1; k < kWaves; ++k) m = fmaxf(m, wave_m[k][r]);
-      for (int k = 0; k < kWaves; ++k) {
-        sum += sums[(k * rows + r) * D + d];
-        den += wave_l[k][r] * (wave_m[k][r] == m ? 1.0f : __builtin_amdgcn_exp2f(wave_m[k][r] - m));
-      }
-      if (cur.whole) {
-        store_out<D>(a, cur.b, cur.h0 + r, d, sum, den);
-        if (d == 0 && a.lse) a.lse[(int64_t)cur.b * a.heads + cur.h0 + r] = (m + __log2f(den)) * kLn2;
-      } else {
-        slot[r * D + d] = sum;
-        if (d == 0) {
-          slot[a.rows * D + 2 * r] = m;
-          slot[a.rows * D + 2 * r + 1] = den;
-        }
-      }
+  }
+  __syncthreads();
+  if ((uint32_t)wave >= live) return;
+  // every wave of the run sums its share of the elements
+  float *slot = line.start(v0 + lead) <= cur.u0 && line.start(v0 + tail + 1) >= cur.u1 ? nullptr
+                                                                                    : slot_of(a, 2 * (v0 + lead) + 1, D);
+  for (int i = 4 * (64 * (wave - (int)lead) + lane); i < cur.rows * D; i += 256 * (int)(tail - lead + 1)) {
+    const int r = i / D, d = i & (D - 1);
+    float m = wave_m[lead][r];
+    for (uint32_t k = lead + 1; k <= tail; ++k) m = fmaxf(m, wave_m[k][r]);
+    f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+    float den = 0.f;
+    for (uint32_t k = lead; k <= tail; ++k) {
+      sum += *reinterpret_cast<const f32x4 *>(sums + (k * a.rows + r) * kPad + d);
+      den += wave_l[k][r] * (wave_m[k][r] == m ? 1.0f : __builtin_amdgcn_exp2f(wave_m[k][r] - m));
     }
-    if (cur.at + cur.n >= end) break;
-    cur = segment_at(a, cur.at + cur.n, end, cur.b, cur.seq_at, wave);
+    store_result<D>(a, cur, slot, r, d, sum, m, den);
   }
 }
 
-// Joins the parts of the head tiles that several workgroups shared: one workgroup for each sequence,
-// head tile and head. The parts' largest scores and sums are read at once, then the threads share
-// out the parts, each holding one element of the output.
-constexpr int kGrid = 512;                           // workgroups of attn_kernel at most
+// Joins the parts of the head tiles that several workgroups (or a wave that went on) hold. Workgroup
+// (sequence and head tile, y) takes the heads y, y + gridDim.y, ...: the parts' largest scores and
+// sums are read at once, then the threads share out the parts, each holding one element of the
+// output.
+constexpr int kGrid = 1024;                          // workgroups of attn_kernel at most
 
 template <int D>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_t grid) {
   constexpr int kSplit = kThreads / D;               // threads of an element
-  __shared__ uint32_t scan[kWaves];
-  __shared__ float red[kWaves], factor[kGrid], sums[kThreads];
-  __shared__ uint32_t slots[kGrid];
-  const int32_t b = blockIdx.x / a.head_tiles, ht = blockIdx.x - b * a.head_tiles, r = blockIdx.y;
-  const int32_t kvh = ht / a.tiles_per_kv, first_head = (ht - kvh * a.tiles_per_kv) * 16;
-  if (r >= a.group - first_head) return;
+  constexpr int kParts = kGrid + 1;                  // of a head tile at most: one a workgroup, and one left behind
+  __shared__ uint32_t scan[kWaves], slots[kParts];
+  __shared__ float red[kWaves], factor[kParts], sums[kThreads];
+  const int32_t b = blockIdx.x / a.head_tiles, ht = blockIdx.x - b * a.head_tiles;
   uint32_t all = 0, before = 0;
   for (int32_t k = threadIdx.x; k < a.batch; k += kThreads) {
-    const uint32_t n = (uint32_t)seen_of(a, a.lens[k]).units * a.head_tiles;
+    const uint32_t n = (uint32_t)seen_of(a, a.lens[k]).tiles * a.head_tiles;
     all += n;
     before += k < b ? n : 0;
   }
@@ -541,90 +577,106 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_
   block_scan(before, scan, u0);
   const Line line = make_line(total, grid);
   const Seen s = seen_of(a, scalar_load(a.lens + b));
-  u0 += (uint32_t)ht * (uint32_t)s.units;
-  const uint32_t w0 = line.holder(u0), w1 = line.holder(u0 + s.units - 1), n = w1 - w0 + 1;
+  u0 += (uint32_t)ht * (uint32_t)s.tiles;
+  const uint32_t u1 = u0 + s.tiles, w0 = line.holder(u0), w1 = line.holder(u1 - 1);
+  // parts in order: those of workgroups, then the one of the last wave if it went on
+  const bool left = line.start(w1 + 1) > u1;
+  if (w0 == w1) return;
+  const uint32_t e1 = left ? w1 - 1 : w1;            // the last wave that ends on the head tile
+  // wave w0 ends on it unless w0 == w1, so there is a run of workgroups from its own to e1's
+  const uint32_t n_groups = e1 / kWaves - w0 / kWaves + 1, n = n_groups + (left ? 1 : 0);
   if (n == 1) return;
-  // a workgroup's part is its second result if it starts before the head tile does
-  float m = -INFINITY;
   for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-    const uint32_t slot = 2 * (w0 + i) + (line.start(w0 + i) < u0 ? 1 : 0);
-    slots[i] = slot;
-    factor[i] = slot_of(a, slot, D)[a.rows * D + 2 * r];
-    m = fmaxf(m, factor[i]);
+    const uint32_t lead = i == 0 ? w0 : (w0 / kWaves + i) * kWaves;
+    slots[i] = i < n_groups ? 2 * lead + 1 : 2 * w1;
   }
-  for (int o = 32; o; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  float den = 0.f;
-  for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-    const float f = factor[i] == m ? 1.0f : __builtin_amdgcn_exp2f(factor[i] - m);
-    factor[i] = f;
-    den += slot_of(a, slots[i], D)[a.rows * D + 2 * r + 1] * f;
-  }
-  for (int o = 32; o; o >>= 1) den += __shfl_xor(den, o);
-  __syncthreads();                                   // red is read, factor written
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = den;
-  __syncthreads();
-  den = (red[0] + red[1]) + (red[2] + red[3]);
+  const int32_t kvh = ht / a.tiles_per_kv, first_head = (ht - kvh * a.tiles_per_kv) * 16;
+  const int32_t rows = min(16, a.group - first_head);
   const int d = threadIdx.x & (D - 1), part = threadIdx.x / D;
-  const float *p = a.slots + r * D + d;
   const int64_t stride = (int64_t)a.rows * (D + 2);
-  float sum = 0.f;
-#pragma unroll 8
-  for (uint32_t i = part; i < n; i += kSplit) sum += p[slots[i] * stride] * factor[i];
-  if constexpr (kSplit > 1) {
-    sums[threadIdx.x] = sum;
+  for (int32_t r = blockIdx.y; r < rows; r += gridDim.y) {
     __syncthreads();
-    if (part) return;
-    for (int k = 1; k < kSplit; ++k) sum += sums[k * D + d];
+    float m = -INFINITY;
+    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+      factor[i] = a.slots[slots[i] * stride + a.rows * D + 2 * r];
+      m = fmaxf(m, factor[i]);
+    }
+    for (int k = 32; k; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    float den = 0.f;
+    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+      const float f = factor[i] == m ? 1.0f : __builtin_amdgcn_exp2f(factor[i] - m);
+      den += a.slots[slots[i] * stride + a.rows * D + 2 * r + 1] * f;
+      factor[i] = f;
+    }
+    for (int k = 32; k; k >>= 1) den += __shfl_xor(den, k);
+    __syncthreads();                                 // red is read, factor written
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = den;
+    __syncthreads();
+    den = (red[0] + red[1]) + (red[2] + red[3]);
+    const float *p = a.slots + r * D + d;
+    float sum = 0.f;
+#pragma unroll 8
+    for (uint32_t i = part; i < n; i += kSplit) sum += p[slots[i] * stride] * factor[i];
+    if constexpr (kSplit > 1) {
+      sums[threadIdx.x] = sum;
+      __syncthreads();
+      if (part == 0)
+        for (int k = 1; k < kSplit; ++k) sum += sums[k * D + d];
+    }
+    if (part == 0) {
+      const int32_t h = kvh * a.group + first_head + r;
+      store_out<D>(a, b, h, d, sum, den);
+      if (d == 0 && a.lse) a.lse[(int64_t)b * a.heads + h] = (m + __log2f(den)) * kLn2;
+    }
   }
-  const int32_t h = kvh * a.group + first_head + r;
-  store_out<D>(a, b, h, d, sum, den);
-  if (d == 0 && a.lse) a.lse[(int64_t)b * a.heads + h] = (m + __log2f(den)) * kLn2;
 }
 
 namespace {
 
 bool attn_misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
-// Units of a head tile of the longest sequence: of max_len tokens, or of a window that starts
+// Tiles of a head tile of the longest sequence: of max_len tokens, or of a window that starts
 // anywhere in a tile.
-int64_t attn_units(int64_t max_len, int64_t window) {
+int64_t attn_tiles(int64_t max_len, int64_t window) {
   int64_t tiles = (max_len + kTile - 1) / kTile;
   if (window > 0 && window < max_len) {
     const int64_t seen = (window + kTile - 2) / kTile + 1;
     tiles = seen < tiles ? seen : tiles;
   }
-  const int64_t units = (tiles + kWaves - 1) / kWaves;
-  return units > 1 ? units : 1;
+  return tiles > 1 ? tiles : 1;
 }
 
-int32_t attn_grid(int64_t batch, int64_t head_tiles, int64_t units) {
-  const int64_t all = batch * head_tiles * units;
-  return (int32_t)(all < kGrid ? all : kGrid);
+// Workgroups: as many as are resident at once (two of four waves a SIMD's registers hold; four for
+// heads of 64), or as there are tiles for.
+int32_t attn_grid(int64_t batch, int64_t head_tiles, int64_t tiles, int64_t dim) {
+  const int64_t all = (batch * head_tiles * tiles + kWaves - 1) / kWaves, most = dim == 64 ? 1024 : 512;
+  return (int32_t)(all < most ? all : most);
 }
 
 template <int D, bool Q8>
-int launch_attn(const AttnArgs &a, int64_t units, hipStream_t s) {
-  const int32_t grid = attn_grid(a.batch, a.head_tiles, units);
-  const size_t lds = sizeof(float) * kWaves * a.rows * D;
+int launch_attn(const AttnArgs &a, int64_t tiles, hipStream_t s) {
+  const int32_t grid = attn_grid(a.batch, a.head_tiles, tiles, D);
+  const size_t lds = sizeof(float) * kWaves * a.rows * (D + 4);
   if (int st = launch(attn_kernel<D, Q8>, dim3(grid), dim3(kThreads), lds, s, a)) return st;
-  if (units == 1) return QG_OK;                      // every head tile is one workgroup's
-  return launch(attn_join_kernel<D>, dim3((unsigned)(a.batch * a.head_tiles), (unsigned)a.rows), dim3(kThreads), 0, s, a,
-                (uint32_t)grid);
+  if (tiles == 1) return QG_OK;                      // every head tile is one wave's
+  const int64_t all = (int64_t)a.batch * a.head_tiles, share = 1024 / all;
+  const unsigned split = (unsigned)(share < 1 ? 1 : share < a.rows ? share : a.rows);
+  return launch(attn_join_kernel<D>, dim3((unsigned)all, split), dim3(kThreads), 0, s, a, (uint32_t)grid);
 }
 
 template <int D>
-int launch_dim(const AttnArgs &a, int64_t units, bool q8, hipStream_t s) {
-  return q8 ? launch_attn<D, true>(a, units, s) : launch_attn<D, false>(a, units, s);
+int launch_dim(const AttnArgs &a, int64_t tiles, bool q8, hipStream_t s) {
+  return q8 ? launch_attn<D, true>(a, tiles, s) : launch_attn<D, false>(a, tiles, s);
 }
 
 int attn_shape(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_len, KvLayout *L) {
   if (int st = kv_pool_layout(pool, L)) return st;
   if (batch < 0 || heads < 1 || heads % pool->kv_heads || heads > (1 << 22) || batch > (1 << 22) / heads) return QG_ERR_SHAPE;
   if (max_len < 0 || max_len > (1 << 30)) return QG_ERR_SHAPE;
-  if (batch * heads * attn_units(max_len, 0) > 0x7FFFFFFF) return QG_ERR_SHAPE;   // the line's units fit 31 bits
+  if (batch * heads * attn_tiles(max_len, 0) > 0x7FFFFFFF) return QG_ERR_SHAPE;   // the line fits 31 bits
   return QG_OK;
 }
 
@@ -641,7 +693,7 @@ int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t head
   KvLayout L;
   if (int st = attn_shape(pool, batch, heads, max_len, &L)) return st;
   const int64_t group = heads / pool->kv_heads, rows = group < 16 ? group : 16;
-  const int64_t slots = 2 * attn_grid(batch, (group + 15) / 16 * pool->kv_heads, attn_units(max_len, 0));
+  const int64_t slots = 2 * kWaves * attn_grid(batch, (group + 15) / 16 * pool->kv_heads, attn_tiles(max_len, 0), pool->head_dim);
   *bytes = 4 * slots * rows * (pool->head_dim + 2);
   if (*bytes < 16) *bytes = 16;
   return QG_OK;
@@ -694,13 +746,13 @@ int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q,
   a.out_f32 = out_f32 != 0;
   a.lse = lse;
   a.slots = static_cast<float *>(workspace);
-  const int64_t units = attn_units(max_len, a.window);
+  const int64_t tiles = attn_tiles(max_len, a.window);
   const bool q8 = pool->kind == QG_KV_Q8;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   switch (pool->head_dim) {
-    case 64: return launch_dim<64>(a, units, q8, s);
-    case 128: return launch_dim<128>(a, units, q8, s);
-    default: return launch_dim<256>(a, units, q8, s);
+    case 64: return launch_dim<64>(a, tiles, q8, s);
+    case 128: return launch_dim<128>(a, tiles, q8, s);
+    default: return launch_dim<256>(a, tiles, q8, s);
   }
 }
 

@@ -442,7 +442,7 @@ int qg_kv_gather(const qg_kv_pool *pool, int64_t layer, const int32_t *table, in
  * that is replayed while sequences grow passes the longest it will see); the table has at least
  * ceil(max_len / T) entries a row. q and out: 16-byte aligned, ldq a multiple of 8 (ldo of 8, of
  * 4 for fp32) and at least heads * head_dim when batch > 1. heads is a multiple of kv_heads;
- * batch * heads is at most 2^22, max_len at most 2^30, batch * heads * ceil(max_len / 128) below
+ * batch * heads is at most 2^22, max_len at most 2^30, batch * heads * ceil(max_len / 32) below
  * 2^31, window >= 0, scale finite.
  * Errors: also QG_ERR_WORKSPACE, and QG_ERR_RANGE for a scale that is not finite. */
 int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_len, int64_t *bytes);
