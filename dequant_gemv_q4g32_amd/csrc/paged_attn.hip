@@ -29,7 +29,9 @@ struct AttnArgs {
   int64_t ldo;
   int32_t out_f32;
   float *lse;
-  float *slots;                  // workspace: two partial results a workgroup
+  uint32_t *starts;              // workspace: where each sequence starts on the line, and its end;
+  const int32_t *starts_in;      // the same for reading
+  float *slots;                  // workspace: two parts a wave
 };
 
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
@@ -37,7 +39,7 @@ typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 4;                          // waves of a workgroup
+constexpr int kWaves = 4;                          // waves of a workgroup that takes a part of the line
 constexpr int kTile = 32;                          // tokens of a wave's step, the grain of the split: two 16-token blocks
 constexpr int kThreads = 64 * kWaves;
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -76,18 +78,19 @@ __device__ __forceinline__ Seen seen_of(const AttnArgs &a, int32_t raw) {
 // parts of a head tile are: one for each workgroup with such waves (named by the first of them,
 // the leader), and one for a wave that goes on past u1.
 struct Line {
-  uint32_t total, waves, quota, extra;
-  __device__ __forceinline__ uint32_t start(uint32_t v) const { return v * quota + min(v, extra); }
+  uint32_t total, waves, quota, extra, first;
+  __device__ __forceinline__ uint32_t start(uint32_t v) const { return first + v * quota + min(v, extra); }
   // the wave that holds tile u
   __device__ __forceinline__ uint32_t holder(uint32_t u) const {
     const uint32_t big = extra * (quota + 1);
     return u < big ? u / (quota + 1) : extra + (u - big) / quota;
   }
 };
-__device__ __forceinline__ Line make_line(uint32_t total, uint32_t grid) {
+__device__ __forceinline__ Line make_line(uint32_t total, uint32_t waves) {
   Line l;
   l.total = total;
-  l.waves = min(total, grid * kWaves);
+  l.first = 0;
+  l.waves = min(total, waves);
   l.quota = total / l.waves;
   l.extra = total - l.quota * l.waves;
   return l;
@@ -142,20 +145,19 @@ struct Block {
   uint32_t place;
 };
 
-constexpr int kCache = 0;                            // cache policy of the loads
 
-template <int N>
+template <int N, int AUX>
 __device__ __forceinline__ void load_words(rsrc_t r, uint32_t voff, uint32_t soff, uint32_t *w) {
   if constexpr (N == 1) {
-    w[0] = bldx1<kCache>(r, voff, soff);
+    w[0] = bldx1<AUX>(r, voff, soff);
   } else if constexpr (N == 2) {
-    const u32x2 t = bldx2<kCache>(r, voff, soff);
+    const u32x2 t = bldx2<AUX>(r, voff, soff);
     w[0] = t.x;
     w[1] = t.y;
   } else {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const u32x4 t = bldx4<kCache>(r, voff + 16 * i, soff);
+      const u32x4 t = bldx4<AUX>(r, voff + 16 * i, soff);
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[4 * i + j] = t[j];
     }
@@ -172,9 +174,9 @@ __device__ __forceinline__ void load_k(const AttnArgs &a, const Block *blk, Tile
   for (int st = 0; st < 2; ++st) {
 #pragma unroll
     for (int i = 0; i < Tile<D, Q8>::KR; ++i)
-      t.k[st][i] = Q8 ? bldx4<kCache>(blk[st].r, c * D + 16 * g + 64 * i, blk[st].place * D)
-                      : bldx4<kCache>(blk[st].r, c * 2 * D + 32 * g + 128 * (i >> 1) + 16 * (i & 1), blk[st].place * 2 * D);
-    if constexpr (Q8) load_words<D / 64>(blk[st].r, c * (D / 16), a.ks_off + blk[st].place * (D / 16), t.ks[st]);
+      t.k[st][i] = Q8 ? bldx4<0>(blk[st].r, c * D + 16 * g + 64 * i, blk[st].place * D)
+                      : bldx4<0>(blk[st].r, c * 2 * D + 32 * g + 128 * (i >> 1) + 16 * (i & 1), blk[st].place * 2 * D);
+    if constexpr (Q8) load_words<D / 64, 0>(blk[st].r, c * (D / 16), a.ks_off + blk[st].place * (D / 16), t.ks[st]);
   }
 }
 
@@ -187,9 +189,9 @@ __device__ __forceinline__ void load_v(const AttnArgs &a, const Block *blk, uint
   for (int st = 0; st < 2; ++st) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      load_words<VW>(blk[st].r, (4 * g * D + VJ * c) * kElem + i * D * kElem, a.v_off + blk[st].place * (D * kElem),
+      load_words<VW, kNT>(blk[st].r, (4 * g * D + VJ * c) * kElem + i * D * kElem, a.v_off + blk[st].place * (D * kElem),
                      t.v[4 * st + i]);
-    if constexpr (Q8) t.vs[st] = bldx2<kCache>(blk[st].r, vs_lane, a.vs_off + 2 * blk[st].place);
+    if constexpr (Q8) t.vs[st] = bldx2<0>(blk[st].r, vs_lane, a.vs_off + 2 * blk[st].place);
   }
 }
 
@@ -333,38 +335,63 @@ __device__ __forceinline__ void store_result(const AttnArgs &a, const Segment &s
   if (d == 0 && a.lse) a.lse[(int64_t)s.b * a.heads + h] = (m + __log2f(l)) * kLn2;
 }
 
-template <int D, bool Q8>
+// WHOLE: workgroup (sequence, head tile) takes that head tile, its waves a share each, and there is
+// nothing to join afterwards. Else the workgroups' waves take the parts of the line.
+template <int D, bool Q8, bool WHOLE>
 __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_kernel(AttnArgs a) {
+  constexpr int NW = kWaves;
   using T = Tile<D, Q8>;
   constexpr int VJ = T::VJ;
   constexpr int kPad = D + 4;                        // LDS rows of neighbouring heads start in other banks
-  extern __shared__ float sums[];                    // [kWaves][rows][kPad], rows = heads of a tile
-  __shared__ uint32_t scan[kWaves], found[2][kWaves];
-  __shared__ float wave_m[kWaves][16], wave_l[kWaves][16];
+  extern __shared__ float sums[];                    // [NW][rows][kPad], rows = heads of a tile
+  __shared__ uint32_t scan[NW], found[2][NW];
+  __shared__ float wave_m[NW][16], wave_l[NW][16];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
   if constexpr (Q8) __builtin_amdgcn_s_setreg(1 | (23 << 6) | (0 << 11), 1);   // hwreg(MODE, 23, 1): FP16_OVFL
   const uint32_t vs_lane = 2 * ((((VJ * (uint32_t)c) / 32) << a.tok_shift) + 4 * g);   // the lane's V scales
 
   // this workgroup's waves on the line
-  const int32_t per = (a.batch + kThreads - 1) / kThreads, my_b = (int32_t)threadIdx.x * per;
-  uint32_t mine = 0;
-  for (int32_t i = 0; i < per; ++i)
-    if (my_b + i < a.batch) mine += (uint32_t)seen_of(a, a.lens[my_b + i]).tiles * a.head_tiles;
-  uint32_t total;
-  const uint32_t before = block_scan(mine, scan, total);
-  const Line line = make_line(total, gridDim.x);
-  const uint32_t v0 = blockIdx.x * kWaves, v = v0 + wave;
-  if (v0 >= line.waves) return;
-  const uint32_t live = min((uint32_t)kWaves, line.waves - v0);   // waves with a part of the line
-#pragma unroll
-  for (int k = 0; k < kWaves; ++k) {
-    const uint32_t at = line.start(v0 + k);
-    if (at >= before && at - before < mine) {
-      found[0][k] = (uint32_t)my_b;
-      found[1][k] = before;
+  Line line;
+  uint32_t v0, from_b, from_at;                      // first wave; a sequence at or before this wave's part, and its start
+  if constexpr (WHOLE) {
+    from_b = blockIdx.x / a.head_tiles;
+    from_at = 0;
+    const uint32_t tiles = seen_of(a, scalar_load(a.lens + from_b)).tiles;
+    line = make_line(tiles, NW);
+    line.first = (blockIdx.x - from_b * a.head_tiles) * tiles;
+    v0 = 0;
+  } else {
+    const int32_t per = (a.batch + kThreads - 1) / kThreads, my_b = (int32_t)threadIdx.x * per;
+    uint32_t mine = 0;
+    for (int32_t i = 0; i < per; ++i)
+      if (my_b + i < a.batch) mine += (uint32_t)seen_of(a, a.lens[my_b + i]).tiles * a.head_tiles;
+    uint32_t total;
+    const uint32_t before = block_scan(mine, scan, total);
+    if (blockIdx.x == 0) {                           // for the join
+      uint32_t at = before;
+      for (int32_t i = 0; i < per; ++i)
+        if (my_b + i < a.batch) {
+          a.starts[my_b + i] = at;
+          at += (uint32_t)seen_of(a, a.lens[my_b + i]).tiles * a.head_tiles;
+        }
+      if (threadIdx.x == 0) a.starts[a.batch] = total;
     }
+    line = make_line(total, gridDim.x * NW);
+    v0 = blockIdx.x * NW;
+    if (v0 >= line.waves) return;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const uint32_t at = line.start(v0 + k);
+      if (at >= before && at - before < mine) {
+        found[0][k] = (uint32_t)my_b;
+        found[1][k] = before;
+      }
+    }
+    __syncthreads();
+    from_b = uniform(found[0][wave]);
+    from_at = uniform(found[1][wave]);
   }
-  __syncthreads();
+  const uint32_t v = v0 + wave, live = min((uint32_t)NW, line.waves - v0);   // waves with a part of the line
 
   f32x4 o[VJ];
   float ref = -INFINITY, l = 0.f;
@@ -375,19 +402,23 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_kernel(AttnArg
     half8_t q[T::KD];
     Block blk[2];
     int32_t page[2];                                 // of the tile in t; below 0: none
-    cur = segment_at(a, line.start(v), end, (int32_t)uniform(found[0][wave]), uniform(found[1][wave]));
+    cur = segment_at(a, line.start(v), end, (int32_t)from_b, from_at);
     Segment fetch = cur;                             // the segment of the tile in t, fetch.at that tile
-    auto tile_page = [&](int st) {
-      const int32_t tok = fetch.base + (int32_t)(fetch.at - fetch.u0) * kTile + 16 * st;
-      const int32_t p = tok < fetch.len ? scalar_load(a.table + fetch.b * a.ld_table + (tok >> a.tok_shift)) : -1;
-      return p >= 0 && p < a.num_pages ? p : -1;
+    auto token = [&](int st) { return fetch.base + (int32_t)(fetch.at - fetch.u0) * kTile + 16 * st; };
+    auto look_up = [&]() {
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        const int32_t tok = token(st);
+        const int32_t p = fetch.at < end && tok < fetch.len ? scalar_load(a.table + fetch.b * a.ld_table + (tok >> a.tok_shift)) : -1;
+        page[st] = p >= 0 && p < a.num_pages ? p : -1;
+      }
     };
     auto locate = [&]() {
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
         blk[st].r = make_rsrc(a.pool + (fetch.ht / a.tiles_per_kv) * a.head_bytes + (int64_t)max(page[st], 0) * a.page_bytes,
                               page[st] < 0 ? 0u : (uint32_t)a.head_bytes);
-        blk[st].place = (uint32_t)(fetch.base + (int32_t)(fetch.at - fetch.u0) * kTile + 16 * st) & ((1u << a.tok_shift) - 1);
+        blk[st].place = (uint32_t)token(st) & ((1u << a.tok_shift) - 1);
       }
     };
     auto load_q = [&]() {
@@ -400,12 +431,17 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_kernel(AttnArg
         q[i] = __builtin_bit_cast(half8_t, x);
       }
     };
-    page[0] = tile_page(0);
-    page[1] = tile_page(1);
+    // The loads are issued in one order everywhere (q where it changes, K, V), and after the last tile
+    // from empty ranges instead of not at all: only so the wait for a tile's K or V leaves the
+    // younger loads in flight.
+    look_up();
     locate();
     load_q();
+    __builtin_amdgcn_sched_barrier(0);
     load_k<D, Q8>(a, blk, t);
+    __builtin_amdgcn_sched_barrier(0);
     load_v<D, Q8>(a, blk, vs_lane, t);
+    __builtin_amdgcn_sched_barrier(0);
     bool more = true;
     while (more) {
 #pragma unroll
@@ -414,7 +450,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_kernel(AttnArg
       l = 0.f;
       bool inside = true;                            // the tile in t is of segment cur
       while (inside) {
-        const int32_t t0 = cur.base + (int32_t)(fetch.at - cur.u0) * kTile;
+        const int32_t t0 = token(0);
         const bool full = t0 >= cur.first && t0 + kTile <= cur.len && page[0] >= 0 && page[1] >= 0;
         uint32_t valid = 0xFF;                       // of the lane's eight tokens
         if (!full) {
@@ -432,18 +468,13 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_kernel(AttnArg
           inside = false;
           if (more) fetch = segment_at(a, fetch.at, end, fetch.b, fetch.u0 - (fetch.u1 - fetch.u0) * fetch.ht);
         }
-        if (more) {
-          page[0] = tile_page(0);
-          page[1] = tile_page(1);
-        }
+        look_up();
         f32x4 x[2];
 #pragma unroll
         for (int st = 0; st < 2; ++st) x[st] = scores<D, Q8>(t, st, q);
-        if (more) {
-          locate();
-          load_k<D, Q8>(a, blk, t);
-          if (!inside) load_q();
-        }
+        locate();
+        if (more && !inside) load_q();
+        load_k<D, Q8>(a, blk, t);
         float y[8], top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = x[i >> 2][i & 3] * a.scale_log2;
@@ -490,7 +521,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_kernel(AttnArg
           lo[i] = (_Float16)(p[i] - (float)hi[i]);
         }
         accumulate<D, Q8>(t, hi, lo, o);
-        if (more) load_v<D, Q8>(a, blk, vs_lane, t);
+        load_v<D, Q8>(a, blk, vs_lane, t);
       }
       l += __shfl_xor(l, 16);
       l += __shfl_xor(l, 32);
@@ -553,83 +584,62 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_kernel(AttnArg
 }
 
 // Joins the parts of the head tiles that several workgroups (or a wave that went on) hold. Workgroup
-// (sequence and head tile, y) takes the heads y, y + gridDim.y, ...: the parts' largest scores and
-// sums are read at once, then the threads share out the parts, each holding one element of the
-// output.
-constexpr int kGrid = 1024;                          // workgroups of attn_kernel at most
-
-template <int D>
-__global__ __launch_bounds__(kThreads) void attn_join_kernel(AttnArgs a, uint32_t grid) {
-  constexpr int kSplit = kThreads / D;               // threads of an element
-  constexpr int kParts = kGrid + 1;                  // of a head tile at most: one a workgroup, and one left behind
-  __shared__ uint32_t scan[kWaves], slots[kParts];
-  __shared__ float red[kWaves], factor[kParts], sums[kThreads];
+// (sequence and head tile, y) takes the heads y, y + gridDim.y, ...: kSplit threads for each element
+// of the output run through the parts, every load independent of the others, with their own
+// maximum and sum, and then join these.
+template <int D, int THREADS>
+__global__ __launch_bounds__(THREADS) void attn_join_kernel(AttnArgs a, uint32_t waves) {
+  constexpr uint32_t kSplit = THREADS / D;
+  __shared__ float part_m[kSplit], part_l[kSplit], sums[kSplit][D];
   const int32_t b = blockIdx.x / a.head_tiles, ht = blockIdx.x - b * a.head_tiles;
-  uint32_t all = 0, before = 0;
-  for (int32_t k = threadIdx.x; k < a.batch; k += kThreads) {
-    const uint32_t n = (uint32_t)seen_of(a, a.lens[k]).tiles * a.head_tiles;
-    all += n;
-    before += k < b ? n : 0;
-  }
-  uint32_t total, u0;
-  block_scan(all, scan, total);
-  __syncthreads();
-  block_scan(before, scan, u0);
-  const Line line = make_line(total, grid);
+  const Line line = make_line((uint32_t)scalar_load(a.starts_in + a.batch), waves);
   const Seen s = seen_of(a, scalar_load(a.lens + b));
-  u0 += (uint32_t)ht * (uint32_t)s.tiles;
+  const uint32_t u0 = (uint32_t)scalar_load(a.starts_in + b) + (uint32_t)ht * (uint32_t)s.tiles;
   const uint32_t u1 = u0 + s.tiles, w0 = line.holder(u0), w1 = line.holder(u1 - 1);
-  // parts in order: those of workgroups, then the one of the last wave if it went on
-  const bool left = line.start(w1 + 1) > u1;
   if (w0 == w1) return;
+  // parts in order: those of workgroups, from the first of their waves, then the last wave's if it
+  // went on. Wave w0 ends on the head tile, since it is not the last.
+  const bool left = line.start(w1 + 1) > u1;
   const uint32_t e1 = left ? w1 - 1 : w1;            // the last wave that ends on the head tile
-  // wave w0 ends on it unless w0 == w1, so there is a run of workgroups from its own to e1's
-  const uint32_t n_groups = e1 / kWaves - w0 / kWaves + 1, n = n_groups + (left ? 1 : 0);
+  const uint32_t groups = e1 / kWaves - w0 / kWaves + 1, n = groups + (left ? 1 : 0);
   if (n == 1) return;
-  for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-    const uint32_t lead = i == 0 ? w0 : (w0 / kWaves + i) * kWaves;
-    slots[i] = i < n_groups ? 2 * lead + 1 : 2 * w1;
-  }
   const int32_t kvh = ht / a.tiles_per_kv, first_head = (ht - kvh * a.tiles_per_kv) * 16;
   const int32_t rows = min(16, a.group - first_head);
-  const int d = threadIdx.x & (D - 1), part = threadIdx.x / D;
+  const int d = threadIdx.x & (D - 1);
+  const uint32_t part = threadIdx.x / D;
   const int64_t stride = (int64_t)a.rows * (D + 2);
   for (int32_t r = blockIdx.y; r < rows; r += gridDim.y) {
-    __syncthreads();
-    float m = -INFINITY;
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-      factor[i] = a.slots[slots[i] * stride + a.rows * D + 2 * r];
-      m = fmaxf(m, factor[i]);
+    float m = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll 4
+    for (uint32_t i = part; i < n; i += kSplit) {
+      const uint32_t lead = i == 0 ? w0 : (w0 / kWaves + i) * kWaves;
+      const float *p = a.slots + (int64_t)(i < groups ? 2 * lead + 1 : 2 * w1) * stride;
+      const f32x2 ml = *reinterpret_cast<const f32x2 *>(p + a.rows * D + 2 * r);
+      const float x = p[r * D + d], now = fmaxf(m, ml[0]);
+      const float keep = m == now ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+      const float f = ml[0] == now ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - now);
+      o = o * keep + x * f;
+      l = l * keep + ml[1] * f;
+      m = now;
     }
-    for (int k = 32; k; k >>= 1) m = fmaxf(m, __shfl_xor(m, k));
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    float den = 0.f;
-    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-      const float f = factor[i] == m ? 1.0f : __builtin_amdgcn_exp2f(factor[i] - m);
-      den += a.slots[slots[i] * stride + a.rows * D + 2 * r + 1] * f;
-      factor[i] = f;
+    __syncthreads();                                 // of the previous row
+    sums[part][d] = o;
+    if (d == 0) {
+      part_m[part] = m;
+      part_l[part] = l;
     }
-    for (int k = 32; k; k >>= 1) den += __shfl_xor(den, k);
-    __syncthreads();                                 // red is read, factor written
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = den;
     __syncthreads();
-    den = (red[0] + red[1]) + (red[2] + red[3]);
-    const float *p = a.slots + r * D + d;
-    float sum = 0.f;
-#pragma unroll 8
-    for (uint32_t i = part; i < n; i += kSplit) sum += p[slots[i] * stride] * factor[i];
-    if constexpr (kSplit > 1) {
-      sums[threadIdx.x] = sum;
-      __syncthreads();
-      if (part == 0)
-        for (int k = 1; k < kSplit; ++k) sum += sums[k * D + d];
-    }
     if (part == 0) {
+      for (uint32_t k = 1; k < kSplit; ++k) m = fmaxf(m, part_m[k]);
+      o = l = 0.f;
+      for (uint32_t k = 0; k < kSplit; ++k) {
+        const float f = part_m[k] == m ? 1.0f : __builtin_amdgcn_exp2f(part_m[k] - m);
+        o += sums[k][d] * f;
+        l += part_l[k] * f;
+      }
       const int32_t h = kvh * a.group + first_head + r;
-      store_out<D>(a, b, h, d, sum, den);
-      if (d == 0 && a.lse) a.lse[(int64_t)b * a.heads + h] = (m + __log2f(den)) * kLn2;
+      store_out<D>(a, b, h, d, o, l);
+      if (d == 0 && a.lse) a.lse[(int64_t)b * a.heads + h] = (m + __log2f(l)) * kLn2;
     }
   }
 }
@@ -656,15 +666,31 @@ int32_t attn_grid(int64_t batch, int64_t head_tiles, int64_t tiles, int64_t dim)
   return (int32_t)(all < most ? all : most);
 }
 
+// A workgroup for each head tile instead of the split, where that is the shorter way: the split
+// evens out the work but costs a second launch (about 5 us with its wait), a head tile of n tiles
+// keeps one workgroup busy for n / 4 steps. Split against whole, int8, 32 heads on 8 of 128, us:
+// 1 sequence of 500 tokens 10.6 : 9.8, of 1000 10.9 : 14.6; 16 of 1000 17.6 : 15.2; 64 of up to
+// 2000 38.7 : 34.8; 32 of up to 4096 (fp16) 42.6 : 53.2.
+bool attn_whole(int64_t head_tiles, int64_t tiles) {
+  const int64_t most = head_tiles / 4;
+  return tiles <= (most < 16 ? 16 : most < 64 ? most : 64);
+}
+
+int64_t starts_bytes(int64_t batch) { return (4 * (batch + 1) + 15) / 16 * 16; }
+
 template <int D, bool Q8>
 int launch_attn(const AttnArgs &a, int64_t tiles, hipStream_t s) {
+  const size_t lds = sizeof(float) * a.rows * (D + 4);
+  const int64_t all = (int64_t)a.batch * a.head_tiles;
+  if (attn_whole(all, tiles))
+    return launch(attn_kernel<D, Q8, true>, dim3((unsigned)all), dim3(kThreads), kWaves * lds, s, a);
   const int32_t grid = attn_grid(a.batch, a.head_tiles, tiles, D);
-  const size_t lds = sizeof(float) * kWaves * a.rows * (D + 4);
-  if (int st = launch(attn_kernel<D, Q8>, dim3(grid), dim3(kThreads), lds, s, a)) return st;
-  if (tiles == 1) return QG_OK;                      // every head tile is one wave's
-  const int64_t all = (int64_t)a.batch * a.head_tiles, share = 1024 / all;
-  const unsigned split = (unsigned)(share < 1 ? 1 : share < a.rows ? share : a.rows);
-  return launch(attn_join_kernel<D>, dim3((unsigned)all, split), dim3(kThreads), 0, s, a, (uint32_t)grid);
+  if (int st = launch(attn_kernel<D, Q8, false>, dim3(grid), dim3(kThreads), kWaves * lds, s, a)) return st;
+  // few head tiles: a workgroup for each head, with many threads for an element; many: fewer parts each
+  const uint32_t waves = (uint32_t)grid * kWaves;
+  if (all < 256)
+    return launch(attn_join_kernel<D, 1024>, dim3((unsigned)all, (unsigned)a.rows), dim3(1024), 0, s, a, waves);
+  return launch(attn_join_kernel<D, 256>, dim3((unsigned)all), dim3(256), 0, s, a, waves);
 }
 
 template <int D>
@@ -694,8 +720,7 @@ int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t head
   if (int st = attn_shape(pool, batch, heads, max_len, &L)) return st;
   const int64_t group = heads / pool->kv_heads, rows = group < 16 ? group : 16;
   const int64_t slots = 2 * kWaves * attn_grid(batch, (group + 15) / 16 * pool->kv_heads, attn_tiles(max_len, 0), pool->head_dim);
-  *bytes = 4 * slots * rows * (pool->head_dim + 2);
-  if (*bytes < 16) *bytes = 16;
+  *bytes = starts_bytes(batch) + 4 * slots * rows * (pool->head_dim + 2);
   return QG_OK;
 }
 
@@ -745,7 +770,9 @@ int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q,
   a.ldo = batch > 1 ? ldo : cols;
   a.out_f32 = out_f32 != 0;
   a.lse = lse;
-  a.slots = static_cast<float *>(workspace);
+  a.starts = static_cast<uint32_t *>(workspace);
+  a.starts_in = static_cast<const int32_t *>(workspace);
+  a.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + starts_bytes(batch));
   const int64_t tiles = attn_tiles(max_len, a.window);
   const bool q8 = pool->kind == QG_KV_Q8;
   const hipStream_t s = static_cast<hipStream_t>(stream);
