@@ -13,6 +13,7 @@ device entry point is absent, so calling one raises instead of running anywhere 
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional
@@ -349,7 +350,8 @@ class KVPool:
     """A pool of cache pages: uint8 [num_pages, page_bytes], or [layers, num_pages, page_bytes] for
     several layers that share one page table. kind "q8": int8 groups of 32 with fp16 scales (the
     codec of kv_quantize); "f16": fp16. The record's layout is in include/qgemv.h. The pool keeps
-    `pages` alive; every call on it takes its tensors on the pool's device."""
+    `pages` alive; every call on it takes its tensors on the pool's device and runs on torch's
+    current stream of that device unless `stream` is given."""
 
     def __init__(self, pages, kind: str, kv_heads: int, head_dim: int, page_tokens: int):
         torch = _torch()
@@ -363,6 +365,7 @@ class KVPool:
         self.num_pages = pages.shape[-2]
         self.layers = pages.shape[0] if pages.dim() == 3 else 1
         self.device = pages.device
+        self._index = pages.get_device()
         self._c = _Pool(pages.data_ptr(), self.num_pages, self.layers, pages.stride(0) if self.layers > 1 else 0,
                         KV_KINDS[kind], kv_heads, head_dim, page_tokens)
         self._ref = ctypes.addressof(self._c)
@@ -376,82 +379,86 @@ class KVPool:
                    page_tokens)
 
 
-def _on(pool, call, stream):
-    """call(raw stream) with the pool's device current and `stream` (None: torch's current stream of
-    that device) as torch's current stream, so that memory allocated inside belongs to it."""
-    torch = _torch()
-    index = pool.device.index
-    if stream is None and torch.cuda.current_device() == index:
-        return call(torch.cuda.current_stream(index).cuda_stream)
-    with torch.cuda.device(index):
-        if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+def _paged(fn):
+    """A call on a pool: runs fn(pool, *args) with the pool's device current and `stream` as torch's
+    current stream, so that what it allocates belongs to that stream; fn takes the raw stream as
+    its last argument."""
+    @functools.wraps(fn)
+    def call(pool, *args, stream=None, **kwargs):
+        torch = _torch()
+        index = pool._index
+        if stream is None and torch._C._cuda_getDevice() == index:
+            return fn(pool, *args, **kwargs, stream=torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(index):
+            if stream is None:
+                return fn(pool, *args, **kwargs, stream=torch._C._cuda_getCurrentRawStream(index))
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+            with torch.cuda.stream(stream):
+                return fn(pool, *args, **kwargs, stream=stream.cuda_stream)
+    return call
 
 
 def _ints(pool, what: str, t, length=None):
     """Address of a dense int32 vector on the pool's device."""
-    if t.dtype != _torch().int32 or t.dim() != 1 or t.device != pool.device or (t.numel() > 1 and t.stride(0) != 1):
-        raise ValueError(f"{what} must be a dense int32 vector on {pool.device}")
-    if length is not None and t.numel() != length:
-        raise ValueError(f"{what} must have {length} entries")
+    if (t.dtype is not _torch().int32 or t.get_device() != pool._index or t.dim() != 1 or not t.is_contiguous()
+            or (length is not None and t.numel() != length)):
+        raise ValueError(f"{what} must be a dense int32 vector{'' if length is None else f' of {length}'} on {pool.device}")
     return t.data_ptr()
 
 
 def _table(pool, t):
     """(address, leading dimension, rows, pages a row) of a page table."""
-    if t.dtype != _torch().int32 or t.dim() != 2 or t.device != pool.device or (t.shape[1] > 1 and t.stride(1) != 1):
+    if (t.dtype is not _torch().int32 or t.get_device() != pool._index or t.dim() != 2
+            or not (t.is_contiguous() or t.shape[1] < 2 or t.stride(1) == 1)):
         raise ValueError(f"a page table must be int32 [sequences, pages] with dense rows on {pool.device}")
-    return t.data_ptr(), t.stride(0), t.shape[0], t.shape[1]
+    rows, pages = t.shape
+    return t.data_ptr(), t.stride(0), rows, pages
 
 
 def _rows16(pool, what: str, t, count: int):
     """(address, leading dimension) of fp16 rows [count, kv_heads * head_dim]."""
-    if (t.dtype != _torch().float16 or t.dim() != 2 or t.device != pool.device or t.stride(1) != 1
-            or t.shape[0] != count or t.shape[1] != pool.kv_heads * pool.head_dim):
+    if (t.dtype is not _torch().float16 or t.get_device() != pool._index or t.dim() != 2
+            or not (t.is_contiguous() or t.stride(1) == 1) or t.shape != (count, pool.kv_heads * pool.head_dim)):
         raise ValueError(f"{what} must be fp16 [{count}, {pool.kv_heads * pool.head_dim}] with dense rows on {pool.device}")
     return t.data_ptr(), t.stride(0)
 
 
+@_paged
 def kv_append(pool, table, k, v, positions, seqs=None, layer: int = 0, stream=None) -> None:
     """Write token rows into the cache: k, v fp16 [count, kv_heads * head_dim]; row i becomes token
     positions[i] of table row seqs[i] (row i when seqs is None). A row without a place (position
     -1, say) is skipped; the rows of one call must name distinct places."""
     count = positions.numel()
-    args = (pool._ref, layer, *_table(pool, table), *_rows16(pool, "k", k, count), *_rows16(pool, "v", v, count),
-            None if seqs is None else _ints(pool, "seqs", seqs, count), _ints(pool, "positions", positions), count)
-    _on(pool, lambda st: _check(_lib.qg_kv_append(*args, st), "qg_kv_append"), stream)
+    _check(_lib.qg_kv_append(pool._ref, layer, *_table(pool, table), *_rows16(pool, "k", k, count),
+                             *_rows16(pool, "v", v, count), None if seqs is None else _ints(pool, "seqs", seqs, count),
+                             _ints(pool, "positions", positions), count, stream), "qg_kv_append")
 
 
+@_paged
 def kv_gather(pool, table, positions, seqs=None, k=None, v=None, layer: int = 0, stream=None):
     """Read token rows back, decoded: (k, v) fp16 [count, kv_heads * head_dim], row i token
     positions[i] of table row seqs[i] (row i when seqs is None), zeros where there is none."""
     torch = _torch()
     count, cols = positions.numel(), pool.kv_heads * pool.head_dim
-    head = (pool._ref, layer, *_table(pool, table))
-    tail = (None if seqs is None else _ints(pool, "seqs", seqs, count), _ints(pool, "positions", positions), count)
-
-    def call(st):
-        nonlocal k, v
-        k = torch.empty((count, cols), dtype=torch.float16, device=pool.device) if k is None else k
-        v = torch.empty((count, cols), dtype=torch.float16, device=pool.device) if v is None else v
-        _check(_lib.qg_kv_gather(*head, *_rows16(pool, "k", k, count), *_rows16(pool, "v", v, count), *tail, st),
-               "qg_kv_gather")
-
-    _on(pool, call, stream)
+    if k is None:
+        k = torch.empty((count, cols), dtype=torch.float16, device=pool.device)
+    if v is None:
+        v = torch.empty((count, cols), dtype=torch.float16, device=pool.device)
+    _check(_lib.qg_kv_gather(pool._ref, layer, *_table(pool, table), *_rows16(pool, "k", k, count),
+                             *_rows16(pool, "v", v, count), None if seqs is None else _ints(pool, "seqs", seqs, count),
+                             _ints(pool, "positions", positions), count, stream), "qg_kv_gather")
     return k, v
 
 
 def paged_attention_bytes(pool, batch: int, heads: int, max_len: int) -> int:
-    """Workspace bytes of paged_attention for these sizes."""
+    """Workspace bytes of paged_attention for these sizes (0: it needs none)."""
     out = ctypes.c_int64()
     _check(_lib.qg_paged_attention_bytes(pool._ref, batch, heads, max_len, ctypes.byref(out)), "qg_paged_attention_bytes")
     return out.value
 
 
+@_paged
 def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: Optional[float] = None, window: int = 0,
                     out=None, out_f32: bool = False, lse=None, return_lse: bool = False, workspace=None, layer: int = 0,
                     stream=None):
@@ -464,10 +471,10 @@ def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: 
     lse -inf. workspace: uint8 of paged_attention_bytes(...), used by one call at a time; allocated
     here when None."""
     torch = _torch()
-    if q.dim() != 3 or q.dtype != torch.float16 or q.device != pool.device:
+    if q.dtype is not torch.float16 or q.get_device() != pool._index or q.dim() != 3:
         raise ValueError(f"q must be fp16 [batch, heads, head_dim] on {pool.device}")
-    batch, heads, dim = q.shape
-    if dim != pool.head_dim or q.stride(2) != 1 or (heads > 1 and q.stride(1) != dim):
+    shape = batch, heads, dim = q.shape
+    if dim != pool.head_dim or not (q.is_contiguous() or (q.stride(2) == 1 and (heads == 1 or q.stride(1) == dim))):
         raise ValueError(f"q must have dense heads of {pool.head_dim}")
     at, ld, rows, pages = _table(pool, table)
     if max_len is None:
@@ -476,90 +483,85 @@ def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: 
         raise ValueError("the table must have a row for each sequence, and pages for max_len tokens")
     if scale is None:
         scale = dim ** -0.5
-    lens_at = _ints(pool, "lens", lens, batch)
-    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != pool.device
-                                  or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be dense uint8 on {pool.device}")
-
-    def call(st):
-        nonlocal out, lse
-        if out is None:
-            out = torch.empty((batch, heads, dim), dtype=torch.float32 if out_f32 else torch.float16, device=pool.device)
-        elif (out.shape != q.shape or out.dtype not in (torch.float16, torch.float32) or out.device != pool.device
-              or out.stride(2) != 1 or (heads > 1 and out.stride(1) != dim)):
-            raise ValueError(f"out must be fp16 or fp32 [{batch}, {heads}, {dim}] with dense heads on {pool.device}")
-        if lse is None and return_lse:
-            lse = torch.empty((batch, heads), dtype=torch.float32, device=pool.device)
-        elif lse is not None and (lse.shape != (batch, heads) or lse.dtype != torch.float32 or lse.device != pool.device
-                                  or not lse.is_contiguous()):
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32 if out_f32 else torch.float16, device=pool.device)
+    elif (out.shape != shape or out.dtype not in (torch.float16, torch.float32) or out.device != pool.device
+          or out.stride(2) != 1 or (heads > 1 and out.stride(1) != dim)):
+        raise ValueError(f"out must be fp16 or fp32 [{batch}, {heads}, {dim}] with dense heads on {pool.device}")
+    if lse is not None:
+        if lse.shape != (batch, heads) or lse.dtype != torch.float32 or lse.device != pool.device or not lse.is_contiguous():
             raise ValueError(f"lse must be dense fp32 [{batch}, {heads}] on {pool.device}")
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(paged_attention_bytes(pool, batch, heads, max_len), dtype=torch.uint8, device=pool.device)
-        _check(_lib.qg_paged_attention(pool._ref, layer, q.data_ptr(), q.stride(0), at, ld, lens_at, batch, heads, max_len,
-                                       window, scale, out.data_ptr(), out.stride(0), int(out.dtype == torch.float32),
-                                       None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), st),
-               "qg_paged_attention")
-
-    _on(pool, call, stream)
+    elif return_lse:
+        lse = torch.empty((batch, heads), dtype=torch.float32, device=pool.device)
+    if workspace is None:
+        need = paged_attention_bytes(pool, batch, heads, max_len)
+        workspace = torch.empty(need, dtype=torch.uint8, device=pool.device) if need else None
+    elif workspace.dtype != torch.uint8 or workspace.device != pool.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be dense uint8 on {pool.device}")
+    _check(_lib.qg_paged_attention(pool._ref, layer, q.data_ptr(), q.stride(0), at, ld, _ints(pool, "lens", lens, batch),
+                                   batch, heads, max_len, window, scale, out.data_ptr(), out.stride(0),
+                                   out.dtype is torch.float32, None if lse is None else lse.data_ptr(),
+                                   *((None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())),
+                                   stream), "qg_paged_attention")
     return out if lse is None else (out, lse)
 
 
+@_paged
 def kv_copy_pages(pool, src, dst, stream=None) -> None:
     """Copy pages src[i] to dst[i] (int32 vectors on the device) in every layer of the pool."""
     count = src.numel()
-    args = (pool._ref, _ints(pool, "src", src), _ints(pool, "dst", dst, count), count)
-    _on(pool, lambda st: _check(_lib.qg_kv_copy_pages(*args, st), "qg_kv_copy_pages"), stream)
+    _check(_lib.qg_kv_copy_pages(pool._ref, _ints(pool, "src", src), _ints(pool, "dst", dst, count), count, stream),
+           "qg_kv_copy_pages")
 
 
+@_paged
 def kv_fork(pool, table, lens, refs, src_rows, dst_rows, new_pages, stream=None) -> None:
     """Table rows dst_rows become second holders of src_rows' tokens: whole pages are shared (refs
     counts them), a partly filled last page is copied to new_pages[i]. table, lens and refs are
     updated in place; free the destination rows first if they hold anything."""
-    t = _table(pool, table)
+    at, ld, rows, pages = _table(pool, table)
     count = src_rows.numel()
-    args = (pool._ref, *t, _ints(pool, "lens", lens, t[2]), _ints(pool, "refs", refs, pool.num_pages),
-            _ints(pool, "src_rows", src_rows), _ints(pool, "dst_rows", dst_rows, count),
-            _ints(pool, "new_pages", new_pages, count), count)
-    _on(pool, lambda st: _check(_lib.qg_kv_fork(*args, st), "qg_kv_fork"), stream)
+    _check(_lib.qg_kv_fork(pool._ref, at, ld, rows, pages, _ints(pool, "lens", lens, rows),
+                           _ints(pool, "refs", refs, pool.num_pages), _ints(pool, "src_rows", src_rows),
+                           _ints(pool, "dst_rows", dst_rows, count), _ints(pool, "new_pages", new_pages, count), count,
+                           stream), "qg_kv_fork")
 
 
+@_paged
 def kv_free(pool, table, lens, refs, rows, stream=None) -> None:
     """Give up the pages of table rows `rows`: their refs fall by one, the rows become empty."""
-    t = _table(pool, table)
-    args = (pool._ref, *t, _ints(pool, "lens", lens, t[2]), _ints(pool, "refs", refs, pool.num_pages),
-            _ints(pool, "rows", rows), rows.numel())
-    _on(pool, lambda st: _check(_lib.qg_kv_free(*args, st), "qg_kv_free"), stream)
+    at, ld, table_rows, pages = _table(pool, table)
+    _check(_lib.qg_kv_free(pool._ref, at, ld, table_rows, pages, _ints(pool, "lens", lens, table_rows),
+                           _ints(pool, "refs", refs, pool.num_pages), _ints(pool, "rows", rows), rows.numel(), stream),
+           "qg_kv_free")
 
 
+@_paged
 def kv_compact(pool, table, refs, table_out=None, refs_out=None, remap=None, live=None, stream=None):
     """Move the held pages of the pool to its first pages, in every layer. Returns (table_out,
     refs_out, remap, live): the table and the counts for the moved pages (pass table and refs
     themselves to update them in place), each page's new index (-1: free), and the number of
     held pages (int32 [1] on the device)."""
     torch = _torch()
-    t = _table(pool, table)
-    refs_at = _ints(pool, "refs", refs, pool.num_pages)
+    at, ld, rows, pages = _table(pool, table)
     need = ctypes.c_int64()
     _check(_lib.qg_kv_compact_bytes(pool._ref, ctypes.byref(need)), "qg_kv_compact_bytes")
 
-    def call(st):
-        nonlocal table_out, refs_out, remap, live
-        ints = lambda n: torch.empty(n, dtype=torch.int32, device=pool.device)
-        table_out = ints((t[2], t[3])) if table_out is None else table_out
-        refs_out = ints(pool.num_pages) if refs_out is None else refs_out
-        remap = ints(pool.num_pages) if remap is None else remap
-        live = ints(1) if live is None else live
-        to = _table(pool, table_out)
-        if to[2:] != t[2:]:
-            raise ValueError("table_out must have table's shape")
-        ws = ints(need.value // 4)
-        _check(_lib.qg_kv_compact(pool._ref, t[0], t[1], to[0], to[1], t[2], t[3], refs_at,
-                                  _ints(pool, "refs_out", refs_out, pool.num_pages),
-                                  _ints(pool, "remap", remap, pool.num_pages), _ints(pool, "live", live, 1),
-                                  ws.data_ptr(), need.value, st), "qg_kv_compact")
+    def ints(shape):
+        return torch.empty(shape, dtype=torch.int32, device=pool.device)
 
-    _on(pool, call, stream)
+    table_out = ints((rows, pages)) if table_out is None else table_out
+    refs_out = ints(pool.num_pages) if refs_out is None else refs_out
+    remap = ints(pool.num_pages) if remap is None else remap
+    live = ints(1) if live is None else live
+    to = _table(pool, table_out)
+    if to[2:] != (rows, pages):
+        raise ValueError("table_out must have table's shape")
+    workspace = ints(need.value // 4)
+    _check(_lib.qg_kv_compact(pool._ref, at, ld, to[0], to[1], rows, pages, _ints(pool, "refs", refs, pool.num_pages),
+                              _ints(pool, "refs_out", refs_out, pool.num_pages),
+                              _ints(pool, "remap", remap, pool.num_pages), _ints(pool, "live", live, 1),
+                              workspace.data_ptr(), need.value, stream), "qg_kv_compact")
     return table_out, refs_out, remap, live
 
 

@@ -719,7 +719,11 @@ int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t head
   KvLayout L;
   if (int st = attn_shape(pool, batch, heads, max_len, &L)) return st;
   const int64_t group = heads / pool->kv_heads, rows = group < 16 ? group : 16;
-  const int64_t slots = 2 * kWaves * attn_grid(batch, (group + 15) / 16 * pool->kv_heads, attn_tiles(max_len, 0), pool->head_dim);
+  const int64_t head_tiles = (group + 15) / 16 * pool->kv_heads, tiles = attn_tiles(max_len, 0);
+  // a window only shortens the head tiles: what needs no join without one needs none with one
+  *bytes = 0;
+  if (batch == 0 || attn_whole(batch * head_tiles, tiles)) return QG_OK;
+  const int64_t slots = 2 * kWaves * attn_grid(batch, head_tiles, tiles, pool->head_dim);
   *bytes = starts_bytes(batch) + 4 * slots * rows * (pool->head_dim + 2);
   return QG_OK;
 }
@@ -736,12 +740,12 @@ int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q,
   if (layer < 0 || layer >= pool->layers || window < 0 || (batch > 1 && (ldq < cols || ldo < cols))) return QG_ERR_SHAPE;
   if (!std::isfinite(scale)) return QG_ERR_RANGE;
   if (batch == 0) return QG_OK;
-  if (!q || !lens || !out || !workspace) return QG_ERR_NULL;
+  int64_t need = 0;
+  if (int st = qg_paged_attention_bytes(pool, batch, heads, max_len, &need)) return st;
+  if (!q || !lens || !out || (need && !workspace)) return QG_ERR_NULL;
   if (attn_misaligned(q, 16) || attn_misaligned(out, 16) || attn_misaligned(lens, 4) || attn_misaligned(lse, 4) ||
       attn_misaligned(workspace, 16) || (batch > 1 && (ldq % 8 || ldo % (out_f32 ? 4 : 8))))
     return QG_ERR_ALIGN;
-  int64_t need = 0;
-  if (int st = qg_paged_attention_bytes(pool, batch, heads, max_len, &need)) return st;
   if (workspace_bytes < need) return QG_ERR_WORKSPACE;
   AttnArgs a;
   a.pool = static_cast<const uint8_t *>(pool->pages) + (layer ? layer * pool->layer_stride : 0);

@@ -435,8 +435,9 @@ int qg_kv_gather(const qg_kv_pool *pool, int64_t layer, const int32_t *table, in
  * so that fp32 out is good to about 1e-6 and fp16 out to its one rounding.
  *
  * The cache's length is split over the workgroups, whose partial results go through
- * `workspace` (device, 16-byte aligned, at least qg_paged_attention_bytes; its contents need no
- * preparation, and calls that may run at the same time each need their own). The split follows
+ * `workspace` (device, 16-byte aligned, at least qg_paged_attention_bytes, which is 0, and NULL will
+ * do, for short lengths; its contents need no preparation, and calls that may run at the same time
+ * each need their own). The split follows
  * lens on the device, so a captured call follows lens as it changes; the result depends on the
  * split only by rounding, and equal inputs give equal bits. max_len bounds the lengths (a graph
  * that is replayed while sequences grow passes the longest it will see); the table has at least

@@ -28,7 +28,7 @@ def rows(name, pl, layer=0, table=P, ld=4, trows=3, tpages=4, k=P, ldk=1024, v=P
                                  pos, count, None)
 
 
-def attn(pl, layer=0, q=P, ldq=4096, table=P, ld=8, lens=P, batch=3, heads=32, max_len=128, window=0, scale=0.1, out=P,
+def attn(pl, layer=0, q=P, ldq=4096, table=P, ld=512, lens=P, batch=3, heads=32, max_len=8192, window=0, scale=0.1, out=P,
          ldo=4096, f32=0, lse=P, ws=P, size=None):
     ref = ctypes.addressof(pl) if pl else None
     if size is None:
@@ -86,7 +86,7 @@ def test_entry_point_rows(name, bad, status):
     (dict(table=None), NULL), (dict(q=P + 8), ALIGN), (dict(out=P + 4), ALIGN), (dict(lens=P + 2), ALIGN), (dict(lse=P + 2), ALIGN),
     (dict(ws=P + 8), ALIGN), (dict(ldq=4095), SHAPE), (dict(ldq=4100), ALIGN), (dict(ldo=4090), SHAPE), (dict(ldo=4100), ALIGN),
     (dict(ldo=4102, f32=1), ALIGN), (dict(heads=0), SHAPE), (dict(heads=33), SHAPE), (dict(batch=-1), SHAPE),
-    (dict(batch=2 ** 20), SHAPE), (dict(max_len=-1), SHAPE), (dict(max_len=2 ** 30 + 1), SHAPE), (dict(max_len=129), SHAPE),
+    (dict(batch=2 ** 20), SHAPE), (dict(max_len=-1), SHAPE), (dict(max_len=2 ** 30 + 1), SHAPE), (dict(max_len=8193), SHAPE),
     (dict(window=-1), SHAPE), (dict(scale=float("inf")), RANGE), (dict(scale=float("nan")), RANGE), (dict(size=0), WORK)])
 def test_entry_point_attention(bad, status):
     assert attn(pool(), **bad) == status
@@ -95,10 +95,11 @@ def test_entry_point_attention(bad, status):
 def test_entry_point_attention_workspace_one_byte_short():
     got = ctypes.c_int64()
     p = pool()
-    assert qg.lib.qg_paged_attention_bytes(ctypes.addressof(p), 3, 32, 128, ctypes.byref(got)) == 0 and got.value > 0
+    assert qg.lib.qg_paged_attention_bytes(ctypes.addressof(p), 3, 32, 8192, ctypes.byref(got)) == 0 and got.value > 0
     assert attn(p, size=got.value - 1) == WORK
     assert qg.lib.qg_paged_attention_bytes(ctypes.addressof(p), 3, 32, 128, None) == NULL
     assert qg.lib.qg_paged_attention_bytes(ctypes.addressof(p), 3, 31, 128, ctypes.byref(got)) == SHAPE
+    assert qg.lib.qg_paged_attention_bytes(ctypes.addressof(p), 3, 32, 128, ctypes.byref(got)) == 0 and got.value == 0
 
 
 @pytest.mark.parametrize("call,names", [(fork, ["lens", "refs", "src", "dst", "new"]), (free, ["lens", "refs", "rows_"]),
