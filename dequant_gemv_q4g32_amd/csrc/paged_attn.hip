@@ -243,10 +243,11 @@ __device__ __forceinline__ void accumulate(const Tile<D, Q8> &t, half8_t hi, hal
         e[3][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, b, kSelHigh), d);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 4; ++j)
         o[4 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), hi, o[4 * w + j], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
         o[4 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), lo, o[4 * w + j], 0, 0, 0);
-      }
     } else {
       u32x4 e[2];
 #pragma unroll
@@ -255,26 +256,21 @@ __device__ __forceinline__ void accumulate(const Tile<D, Q8> &t, half8_t hi, hal
         e[1][p] = __builtin_amdgcn_perm(t.v[2 * p + 1][w], t.v[2 * p][w], 0x07060302u);
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < 2; ++j)
         o[2 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), hi, o[2 * w + j], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
         o[2 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), lo, o[2 * w + j], 0, 0, 0);
-      }
     }
   }
 }
 
-// A part in the workspace: [rows][D] sums, then each row's largest score and denominator. Slot 2 v:
+// A part in the workspace: [rows][D] sums, then each row's largest score and denominator, in whole
+// 16 bytes. Slot 2 v:
 // what wave v left behind; slot 2 v + 1: what the waves of its workgroup from v on ended on.
+__host__ __device__ __forceinline__ int32_t slot_floats(int32_t rows, int32_t dim) { return rows * dim + (2 * rows + 3) / 4 * 4; }
 __device__ __forceinline__ float *slot_of(const AttnArgs &a, uint32_t slot, int D) {
-  return a.slots + (int64_t)slot * (a.rows * (D + 2));
-}
-
-template <int D>
-__device__ __forceinline__ void store_out(const AttnArgs &a, int32_t b, int32_t h, int d, float o, float l) {
-  const float y = l > 0.f ? o / l : l * o;          // no token: 0; NaN sums stay NaN
-  const int64_t at = b * a.ldo + (int64_t)h * D + d;
-  if (a.out_f32) static_cast<float *>(a.out)[at] = y;
-  else static_cast<uint16_t *>(a.out)[at] = __builtin_bit_cast(uint16_t, (_Float16)y);
+  return a.slots + (int64_t)slot * slot_floats(a.rows, D);
 }
 
 // A wave's part of one head tile of one sequence.
@@ -284,6 +280,8 @@ struct Segment {
   int32_t b;
   int32_t first, len, base;  // what of the sequence is seen
   int32_t ht, h0, rows;      // head tile of the sequence, its first head, heads
+  const uint8_t *kv;         // its KV head's part of page 0
+  const int32_t *row;        // the sequence's row of the table
 };
 
 // The segment at tile `at` < end of the line, at or after sequence b, which starts at seq_at.
@@ -307,21 +305,22 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs &a, uint32_t at, ui
   const int32_t kvh = g.ht / a.tiles_per_kv, first_head = (g.ht - kvh * a.tiles_per_kv) * 16;
   g.h0 = kvh * a.group + first_head;
   g.rows = min(16, a.group - first_head);
+  g.kv = a.pool + kvh * a.head_bytes;
+  g.row = a.table + b * a.ld_table;
   return g;
 }
 
 // Output rows of a whole head tile, or a part of one: 4 elements at d of row r.
 template <int D>
-__device__ __forceinline__ void store_result(const AttnArgs &a, const Segment &s, float *slot, int r, int d, f32x4 o, float m,
-                                             float l) {
+__device__ __forceinline__ void store_result(const AttnArgs &a, int32_t b, int32_t h0, float *slot, int r, int d, f32x4 o,
+                                             float m, float l) {
   if (slot) {
-    *reinterpret_cast<f32x2 *>(slot + r * D + d) = f32x2{o[0], o[1]};
-    *reinterpret_cast<f32x2 *>(slot + r * D + d + 2) = f32x2{o[2], o[3]};
+    *reinterpret_cast<f32x4 *>(slot + r * D + d) = o;
     if (d == 0) *reinterpret_cast<f32x2 *>(slot + a.rows * D + 2 * r) = f32x2{m, l};
     return;
   }
-  const int32_t h = s.h0 + r;
-  const int64_t at = s.b * a.ldo + (int64_t)h * D + d;
+  const int32_t h = h0 + r;
+  const int64_t at = b * a.ldo + (int64_t)h * D + d;
   const float inv = l > 0.f ? 1.0f / l : l;          // no token: 0; NaN sums stay NaN
   o *= inv;
   if (a.out_f32) {
@@ -332,7 +331,7 @@ __device__ __forceinline__ void store_result(const AttnArgs &a, const Segment &s
     for (int i = 0; i < 4; ++i) y[i] = (_Float16)o[i];
     *reinterpret_cast<half4_t *>(static_cast<uint16_t *>(a.out) + at) = y;
   }
-  if (d == 0 && a.lse) a.lse[(int64_t)s.b * a.heads + h] = (m + __log2f(l)) * kLn2;
+  if (d == 0 && a.lse) a.lse[(int64_t)b * a.heads + h] = (m + __log2f(l)) * kLn2;
 }
 
 // WHOLE: workgroup (sequence, head tile) takes that head tile, its waves a share each, and there is
@@ -409,27 +408,23 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_kernel(AttnArg
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
         const int32_t tok = token(st);
-        const int32_t p = fetch.at < end && tok < fetch.len ? scalar_load(a.table + fetch.b * a.ld_table + (tok >> a.tok_shift)) : -1;
-        page[st] = p >= 0 && p < a.num_pages ? p : -1;
+        page[st] = fetch.at < end && tok < fetch.len ? scalar_load(fetch.row + (tok >> a.tok_shift)) : -1;
       }
     };
     auto locate = [&]() {
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        blk[st].r = make_rsrc(a.pool + (fetch.ht / a.tiles_per_kv) * a.head_bytes + (int64_t)max(page[st], 0) * a.page_bytes,
-                              page[st] < 0 ? 0u : (uint32_t)a.head_bytes);
+        if (page[st] >= a.num_pages) page[st] = -1;
+        const uint32_t p = (uint32_t)max(page[st], 0);
+        blk[st].r = make_rsrc(fetch.kv + (uint64_t)p * (uint32_t)a.page_bytes, page[st] < 0 ? 0u : (uint32_t)a.head_bytes);
         blk[st].place = (uint32_t)token(st) & ((1u << a.tok_shift) - 1);
       }
     };
-    auto load_q = [&]() {
+    auto load_q = [&]() {                            // heads past the tile's read as zeros
+      const rsrc_t r = make_rsrc(a.q + uniform(fetch.b) * a.ldq + (int64_t)uniform(fetch.h0) * D, (uint32_t)uniform(fetch.rows) * D * 2);
 #pragma unroll
-      for (int i = 0; i < T::KD; ++i) {
-        u32x4 x = u32x4{0, 0, 0, 0};
-        if (c < fetch.rows)
-          x = ld4(reinterpret_cast<const uint8_t *>(a.q + fetch.b * a.ldq + (int64_t)(fetch.h0 + c) * D + 64 * (i >> 1) + 16 * g +
-                                                    8 * (i & 1)));
-        q[i] = __builtin_bit_cast(half8_t, x);
-      }
+      for (int i = 0; i < T::KD; ++i)
+        q[i] = __builtin_bit_cast(half8_t, bldx4<0>(r, c * (2 * D) + 32 * g, 128 * (i >> 1) + 16 * (i & 1)));
     };
     // The loads are issued in one order everywhere (q where it changes, K, V), and after the last tile
     // from empty ranges instead of not at all: only so the wait for a tile's K or V leaves the
@@ -533,7 +528,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_kernel(AttnArg
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < VJ; j += 4)
-              store_result<D>(a, cur, slot, c, VJ * (4 * g + i) + j, f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]}, ref,
+              store_result<D>(a, cur.b, cur.h0, slot, c, VJ * (4 * g + i) + j, f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]}, ref,
                               l);
         }
         cur = fetch;
@@ -579,18 +574,19 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_kernel(AttnArg
       sum += *reinterpret_cast<const f32x4 *>(sums + (k * a.rows + r) * kPad + d);
       den += wave_l[k][r] * (wave_m[k][r] == m ? 1.0f : __builtin_amdgcn_exp2f(wave_m[k][r] - m));
     }
-    store_result<D>(a, cur, slot, r, d, sum, m, den);
+    store_result<D>(a, cur.b, cur.h0, slot, r, d, sum, m, den);
   }
 }
 
 // Joins the parts of the head tiles that several workgroups (or a wave that went on) hold. Workgroup
-// (sequence and head tile, y) takes the heads y, y + gridDim.y, ...: kSplit threads for each element
-// of the output run through the parts, every load independent of the others, with their own
-// maximum and sum, and then join these.
+// (sequence and head tile, y) takes the heads y, y + gridDim.y, ...: kSplit groups of threads run
+// through the parts, four elements of the output a thread and every load independent of the others,
+// each with its own maximum and sum, and then join these.
 template <int D, int THREADS>
 __global__ __launch_bounds__(THREADS) void attn_join_kernel(AttnArgs a, uint32_t waves) {
-  constexpr uint32_t kSplit = THREADS / D;
-  __shared__ float part_m[kSplit], part_l[kSplit], sums[kSplit][D];
+  constexpr uint32_t kLanes = D / 4, kSplit = THREADS / kLanes;
+  __shared__ float part_m[kSplit], part_l[kSplit];
+  __shared__ f32x4 sums[kSplit][kLanes];
   const int32_t b = blockIdx.x / a.head_tiles, ht = blockIdx.x - b * a.head_tiles;
   const Line line = make_line((uint32_t)scalar_load(a.starts_in + a.batch), waves);
   const Seen s = seen_of(a, scalar_load(a.lens + b));
@@ -605,17 +601,17 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(AttnArgs a, uint32_t
   if (n == 1) return;
   const int32_t kvh = ht / a.tiles_per_kv, first_head = (ht - kvh * a.tiles_per_kv) * 16;
   const int32_t rows = min(16, a.group - first_head);
-  const int d = threadIdx.x & (D - 1);
-  const uint32_t part = threadIdx.x / D;
-  const int64_t stride = (int64_t)a.rows * (D + 2);
+  const uint32_t i4 = threadIdx.x % kLanes, part = threadIdx.x / kLanes;
   for (int32_t r = blockIdx.y; r < rows; r += gridDim.y) {
-    float m = -INFINITY, l = 0.f, o = 0.f;
+    float m = -INFINITY, l = 0.f;
+    f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (uint32_t i = part; i < n; i += kSplit) {
       const uint32_t lead = i == 0 ? w0 : (w0 / kWaves + i) * kWaves;
-      const float *p = a.slots + (int64_t)(i < groups ? 2 * lead + 1 : 2 * w1) * stride;
+      const float *p = slot_of(a, i < groups ? 2 * lead + 1 : 2 * w1, D);
       const f32x2 ml = *reinterpret_cast<const f32x2 *>(p + a.rows * D + 2 * r);
-      const float x = p[r * D + d], now = fmaxf(m, ml[0]);
+      const f32x4 x = *reinterpret_cast<const f32x4 *>(p + r * D + 4 * i4);
+      const float now = fmaxf(m, ml[0]);
       const float keep = m == now ? 1.0f : __builtin_amdgcn_exp2f(m - now);
       const float f = ml[0] == now ? 1.0f : __builtin_amdgcn_exp2f(ml[0] - now);
       o = o * keep + x * f;
@@ -623,23 +619,22 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(AttnArgs a, uint32_t
       m = now;
     }
     __syncthreads();                                 // of the previous row
-    sums[part][d] = o;
-    if (d == 0) {
+    sums[part][i4] = o;
+    if (i4 == 0) {
       part_m[part] = m;
       part_l[part] = l;
     }
     __syncthreads();
     if (part == 0) {
       for (uint32_t k = 1; k < kSplit; ++k) m = fmaxf(m, part_m[k]);
-      o = l = 0.f;
+      o = f32x4{0.f, 0.f, 0.f, 0.f};
+      l = 0.f;
       for (uint32_t k = 0; k < kSplit; ++k) {
         const float f = part_m[k] == m ? 1.0f : __builtin_amdgcn_exp2f(part_m[k] - m);
-        o += sums[k][d] * f;
+        o += sums[k][i4] * f;
         l += part_l[k] * f;
       }
-      const int32_t h = kvh * a.group + first_head + r;
-      store_out<D>(a, b, h, d, o, l);
-      if (d == 0 && a.lse) a.lse[(int64_t)b * a.heads + h] = (m + __log2f(l)) * kLn2;
+      store_result<D>(a, b, kvh * a.group + first_head, nullptr, r, 4 * (int)i4, o, m, l);
     }
   }
 }
@@ -659,10 +654,11 @@ int64_t attn_tiles(int64_t max_len, int64_t window) {
   return tiles > 1 ? tiles : 1;
 }
 
-// Workgroups: as many as are resident at once (two of four waves a SIMD's registers hold; four for
-// heads of 64), or as there are tiles for.
+// Workgroups: as many as are resident at once (heads of 64: four a CU, of 128: two), or as there are
+// tiles for. Heads of 256 would fit two as well, but their parts are 16 KB for 16 heads: one a CU
+// writes and joins half as many.
 int32_t attn_grid(int64_t batch, int64_t head_tiles, int64_t tiles, int64_t dim) {
-  const int64_t all = (batch * head_tiles * tiles + kWaves - 1) / kWaves, most = dim == 64 ? 1024 : 512;
+  const int64_t all = (batch * head_tiles * tiles + kWaves - 1) / kWaves, most = dim == 64 ? 1024 : dim == 128 ? 512 : 256;
   return (int32_t)(all < most ? all : most);
 }
 
@@ -686,11 +682,11 @@ int launch_attn(const AttnArgs &a, int64_t tiles, hipStream_t s) {
     return launch(attn_kernel<D, Q8, true>, dim3((unsigned)all), dim3(kThreads), kWaves * lds, s, a);
   const int32_t grid = attn_grid(a.batch, a.head_tiles, tiles, D);
   if (int st = launch(attn_kernel<D, Q8, false>, dim3(grid), dim3(kThreads), kWaves * lds, s, a)) return st;
-  // few head tiles: a workgroup for each head, with many threads for an element; many: fewer parts each
+  // few head tiles: a workgroup for each head, the more threads for an element the more parts there are
   const uint32_t waves = (uint32_t)grid * kWaves;
-  if (all < 256)
-    return launch(attn_join_kernel<D, 1024>, dim3((unsigned)all, (unsigned)a.rows), dim3(1024), 0, s, a, waves);
-  return launch(attn_join_kernel<D, 256>, dim3((unsigned)all), dim3(256), 0, s, a, waves);
+  const dim3 heads((unsigned)all, all < 256 ? (unsigned)a.rows : 1u);
+  if (grid / all >= 128) return launch(attn_join_kernel<D, 1024>, heads, dim3(1024), 0, s, a, waves);
+  return launch(attn_join_kernel<D, 256>, heads, dim3(256), 0, s, a, waves);
 }
 
 template <int D>
@@ -724,7 +720,7 @@ int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t head
   *bytes = 0;
   if (batch == 0 || attn_whole(batch * head_tiles, tiles)) return QG_OK;
   const int64_t slots = 2 * kWaves * attn_grid(batch, head_tiles, tiles, pool->head_dim);
-  *bytes = starts_bytes(batch) + 4 * slots * rows * (pool->head_dim + 2);
+  *bytes = starts_bytes(batch) + 4 * slots * slot_floats((int32_t)rows, pool->head_dim);
   return QG_OK;
 }
 
