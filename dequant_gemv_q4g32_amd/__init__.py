@@ -442,9 +442,9 @@ def kv_gather(pool, table, positions, seqs=None, k=None, v=None, layer: int = 0,
     torch = _torch()
     count, cols = positions.numel(), pool.kv_heads * pool.head_dim
     if k is None:
-        k = torch.empty((count, cols), dtype=torch.float16, device=pool.device)
+        k = positions.new_empty((count, cols), dtype=torch.float16)
     if v is None:
-        v = torch.empty((count, cols), dtype=torch.float16, device=pool.device)
+        v = torch.empty_like(k) if k.is_contiguous() else positions.new_empty((count, cols), dtype=torch.float16)
     _check(_lib.qg_kv_gather(pool._ref, layer, *_table(pool, table), *_rows16(pool, "k", k, count),
                              *_rows16(pool, "v", v, count), None if seqs is None else _ints(pool, "seqs", seqs, count),
                              _ints(pool, "positions", positions), count, stream), "qg_kv_gather")
@@ -484,7 +484,7 @@ def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: 
     if scale is None:
         scale = dim ** -0.5
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32 if out_f32 else torch.float16, device=pool.device)
+        out = q.new_empty(shape, dtype=torch.float32) if out_f32 else q.new_empty(shape)
     elif (out.shape != shape or out.dtype not in (torch.float16, torch.float32) or out.device != pool.device
           or out.stride(2) != 1 or (heads > 1 and out.stride(1) != dim)):
         raise ValueError(f"out must be fp16 or fp32 [{batch}, {heads}, {dim}] with dense heads on {pool.device}")
@@ -492,10 +492,10 @@ def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: 
         if lse.shape != (batch, heads) or lse.dtype != torch.float32 or lse.device != pool.device or not lse.is_contiguous():
             raise ValueError(f"lse must be dense fp32 [{batch}, {heads}] on {pool.device}")
     elif return_lse:
-        lse = torch.empty((batch, heads), dtype=torch.float32, device=pool.device)
+        lse = q.new_empty((batch, heads), dtype=torch.float32)
     if workspace is None:
         need = paged_attention_bytes(pool, batch, heads, max_len)
-        workspace = torch.empty(need, dtype=torch.uint8, device=pool.device) if need else None
+        workspace = q.new_empty(need, dtype=torch.uint8) if need else None
     elif workspace.dtype != torch.uint8 or workspace.device != pool.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be dense uint8 on {pool.device}")
     _check(_lib.qg_paged_attention(pool._ref, layer, q.data_ptr(), q.stride(0), at, ld, _ints(pool, "lens", lens, batch),
@@ -547,17 +547,14 @@ def kv_compact(pool, table, refs, table_out=None, refs_out=None, remap=None, liv
     need = ctypes.c_int64()
     _check(_lib.qg_kv_compact_bytes(pool._ref, ctypes.byref(need)), "qg_kv_compact_bytes")
 
-    def ints(shape):
-        return torch.empty(shape, dtype=torch.int32, device=pool.device)
-
-    table_out = ints((rows, pages)) if table_out is None else table_out
-    refs_out = ints(pool.num_pages) if refs_out is None else refs_out
-    remap = ints(pool.num_pages) if remap is None else remap
-    live = ints(1) if live is None else live
+    table_out = table.new_empty((rows, pages)) if table_out is None else table_out
+    refs_out = refs.new_empty(pool.num_pages) if refs_out is None else refs_out
+    remap = refs.new_empty(pool.num_pages) if remap is None else remap
+    live = refs.new_empty(1) if live is None else live
     to = _table(pool, table_out)
     if to[2:] != (rows, pages):
         raise ValueError("table_out must have table's shape")
-    workspace = ints(need.value // 4)
+    workspace = refs.new_empty(need.value // 4)
     _check(_lib.qg_kv_compact(pool._ref, at, ld, to[0], to[1], rows, pages, _ints(pool, "refs", refs, pool.num_pages),
                               _ints(pool, "refs_out", refs_out, pool.num_pages),
                               _ints(pool, "remap", remap, pool.num_pages), _ints(pool, "live", live, 1),

@@ -45,50 +45,66 @@ __device__ __forceinline__ uint8_t *row_page(const RowsArgs &a, uint32_t row, in
   return a.pool + (int64_t)page * a.page_bytes;
 }
 
-// blockIdx.y: 0 for K, 1 for V. A lane's 8 elements lie in one head and one group of 32, and
-// the 4 lanes of a group are neighbours in a wave (head_dim / 8 lanes a head, a multiple of 4).
+// A lane takes 8 elements of K and the same 8 of V: both share the look-up of the place. They lie in
+// one head and one group of 32, and the 4 lanes of a group are neighbours in a wave (head_dim / 8
+// lanes a head, a multiple of 4).
 template <bool Q8, bool APPEND>
 __global__ __launch_bounds__(kPageThreads) void kv_rows_kernel(RowsArgs a) {
   const uint32_t i = blockIdx.x * kPageThreads + threadIdx.x;
-  const int which = blockIdx.y;
   const bool live = i < a.lanes;
   const uint32_t row = live ? i / a.per_row : 0, c = live ? i - row * a.per_row : 0;
+  u32x4 v[2] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
+  if constexpr (APPEND) {                            // on their way while the place is looked up
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+      if (live) v[w] = *reinterpret_cast<const u32x4 *>(a.x[w] + (int64_t)row * a.ldx[w] + 8 * c);
+  }
   int32_t at = 0;
   uint8_t *page = live ? row_page(a, row, at) : nullptr;
-  uint16_t *x = a.x[which] + (int64_t)row * a.ldx[which] + 8 * c;
   const uint32_t head = c >> a.lane_shift, e = 8 * (c & ((1u << a.lane_shift) - 1));   // element within the head
-  const int32_t dim = 8 << a.lane_shift;
-  const int64_t base = (int64_t)head * a.head_bytes + (which ? a.v_off : 0);
+  const int32_t dim = 8 << a.lane_shift, group = e / kKvGroup;
+  uint8_t *part = page + (int64_t)head * a.head_bytes;
   const int64_t elem = (int64_t)at * dim + e;
-  if constexpr (!Q8) {
-    if (!live) return;
-    if constexpr (APPEND) {
-      if (page) *reinterpret_cast<u32x4 *>(page + base + 2 * elem) = *reinterpret_cast<const u32x4 *>(x);
-    } else {
-      *reinterpret_cast<u32x4 *>(x) =
-          page ? *reinterpret_cast<const u32x4 *>(page + base + 2 * elem) : u32x4{0, 0, 0, 0};
+  const int64_t off[2] = {Q8 ? elem : 2 * elem, a.v_off + (Q8 ? elem : 2 * elem)};
+  const int64_t scale_off[2] = {a.ks_off + 2 * ((int64_t)at * (dim / kKvGroup) + group),
+                                a.vs_off + 2 * (((int64_t)group << a.tok_shift) + at)};
+  if constexpr (APPEND) {
+    uint16_t d[2];
+    u32x2 codes[2];
+    if constexpr (Q8) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) codes[w] = kv_encode8(v[w], d[w]);   // every lane: the quad's maximum needs all four
+    }
+    if (!page) return;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      if constexpr (Q8) {
+        *reinterpret_cast<u32x2 *>(part + off[w]) = codes[w];
+        if ((c & 3) == 0) *reinterpret_cast<uint16_t *>(part + scale_off[w]) = d[w];
+      } else {
+        *reinterpret_cast<u32x4 *>(part + off[w]) = v[w];
+      }
     }
   } else {
-    const int32_t group = e / kKvGroup;
-    const int64_t scale_at = (int64_t)head * a.head_bytes +
-                             (which ? a.vs_off + 2 * (((int64_t)group << a.tok_shift) + at)
-                                    : a.ks_off + 2 * ((int64_t)at * (dim / kKvGroup) + group));
-    if constexpr (APPEND) {
-      u32x4 v = u32x4{0, 0, 0, 0};
-      if (page) v = *reinterpret_cast<const u32x4 *>(x);
-      uint16_t d;
-      const u32x2 codes = kv_encode8(v, d);   // every lane: the quad's maximum needs all four
-      if (!page) return;
-      *reinterpret_cast<u32x2 *>(page + base + elem) = codes;
-      if ((c & 3) == 0) *reinterpret_cast<uint16_t *>(page + scale_at) = d;
-    } else {
-      if (!live) return;
-      u32x4 v = u32x4{0, 0, 0, 0};
-      if (page)
-        v = kv_decode8(*reinterpret_cast<const u32x2 *>(page + base + elem),
-                       half_bits(*reinterpret_cast<const uint16_t *>(page + scale_at)));
-      *reinterpret_cast<u32x4 *>(x) = v;
+    if (!live) return;
+    if (page) {
+      if constexpr (Q8) {
+        u32x2 codes[2];
+        uint16_t d[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          codes[w] = *reinterpret_cast<const u32x2 *>(part + off[w]);
+          d[w] = *reinterpret_cast<const uint16_t *>(part + scale_off[w]);
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) v[w] = kv_decode8(codes[w], half_bits(d[w]));
+      } else {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) v[w] = *reinterpret_cast<const u32x4 *>(part + off[w]);
+      }
     }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) *reinterpret_cast<u32x4 *>(a.x[w] + (int64_t)row * a.ldx[w] + 8 * c) = v[w];
   }
 }
 
@@ -103,7 +119,9 @@ struct PoolArgs {
 
 constexpr int64_t kChunk = 16384;                  // 4 loads of 16 bytes in flight a lane
 
-// One workgroup copies chunk `c` of a page.
+// One workgroup copies chunk `c` of a page, past the caches (every byte is touched once): 268 MB
+// copied in 100 us = 5.4 TB/s read and written, cached loads and stores 107 us; chunks of 8 KB the
+// same, of 32 KB 133 us.
 __device__ __forceinline__ void copy_chunk(const PoolArgs &p, int32_t layer, int32_t src, int32_t dst, int32_t c) {
   const int64_t base = (int64_t)layer * p.layer_stride;
   const int64_t first = (int64_t)c * kChunk;
@@ -115,12 +133,12 @@ __device__ __forceinline__ void copy_chunk(const PoolArgs &p, int32_t layer, int
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int32_t o = u * kStep + 16 * (int)threadIdx.x;
-    if (o < n) v[u] = *reinterpret_cast<const u32x4 *>(s + o);
+    if (o < n) v[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(s + o));
   }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int32_t o = u * kStep + 16 * (int)threadIdx.x;
-    if (o < n) *reinterpret_cast<u32x4 *>(d + o) = v[u];
+    if (o < n) __builtin_nontemporal_store(v[u], reinterpret_cast<u32x4 *>(d + o));
   }
 }
 
@@ -213,8 +231,9 @@ __global__ __launch_bounds__(kPageThreads) void kv_free_kernel(TableArgs t, int3
 //
 // With lp(p) the number of held pages before p and L = lp(num_pages), a held page p >= L is the
 // (lp(p) - lp(L))-th that moves, and a free page p < L the (p - lp(p))-th that receives one; there
-// are as many of the one as of the other. Three launches: counts of held pages by block; the
-// ranks, as lists of sources and destinations; the copies, with the table and the counts.
+// are as many of the one as of the other. Three launches: counts of held pages by block (left out
+// for small pools, where every workgroup of the second counts for itself); the ranks, as lists of
+// sources and destinations; the copies, with the table and the counts.
 
 constexpr int kScanPages = 4 * kPageThreads;       // pages a workgroup of the first two launches covers
 
@@ -224,6 +243,7 @@ struct CompactArgs {
   int32_t *blocks;                                   // held pages of each block
   int32_t *src, *dst, *moves;                        // lists of up to num_pages / 2 pages, and their length
   int32_t num_pages, num_blocks;
+  int32_t direct;                                    // the second launch counts for itself
 };
 
 // Sum over the workgroup, in every thread; red: 4 ints of LDS.
@@ -252,15 +272,23 @@ __global__ __launch_bounds__(kPageThreads) void kv_rank_kernel(CompactArgs c) {
   const int32_t b = blockIdx.x;
   // held pages in all blocks, and in the blocks before this one
   int32_t all = 0, before = 0;
-  for (int32_t k = threadIdx.x; k < c.num_blocks; k += kPageThreads) {
-    const int32_t n = c.blocks[k];
-    all += n;
-    before += k < b ? n : 0;
+  if (c.direct) {
+    for (int32_t p = threadIdx.x; p < c.num_pages; p += kPageThreads) {
+      const int32_t held = c.refs[p] > 0;
+      all += held;
+      before += p < b * kScanPages ? held : 0;
+    }
+  } else {
+    for (int32_t k = threadIdx.x; k < c.num_blocks; k += kPageThreads) {
+      const int32_t n = c.blocks[k];
+      all += n;
+      before += k < b ? n : 0;
+    }
   }
   const int32_t live = block_sum(all, red);
   before = block_sum(before, red);
   // held pages before page `live`: whole blocks, and the part of its own block
-  const int32_t lb = live / kScanPages;
+  const int32_t lb = c.direct ? 0 : live / kScanPages;
   int32_t low = 0;
   for (int32_t k = threadIdx.x; k < lb; k += kPageThreads) low += c.blocks[k];
   for (int32_t p = lb * kScanPages + threadIdx.x; p < live; p += kPageThreads) low += c.refs[p] > 0;
@@ -398,7 +426,7 @@ int kv_rows(bool append, const qg_kv_pool *pool, int64_t layer, const int32_t *t
   a.per_row = (uint32_t)per_row;
   a.lane_shift = log2_of(pool->head_dim / 8);
   a.tok_shift = log2_of(pool->page_tokens);
-  const dim3 grid((a.lanes + kPageThreads - 1) / kPageThreads, 2), block(kPageThreads);
+  const dim3 grid((a.lanes + kPageThreads - 1) / kPageThreads), block(kPageThreads);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (pool->kind == QG_KV_Q8)
     return append ? launch(kv_rows_kernel<true, true>, grid, block, 0, s, a)
@@ -411,6 +439,7 @@ int kv_rows(bool append, const qg_kv_pool *pool, int64_t layer, const int32_t *t
 int64_t compact_ints(int64_t num_pages) { return (num_pages + kScanPages - 1) / kScanPages + 2 * (num_pages / 2 + 1) + 1; }
 
 constexpr int64_t kCompactPages = int64_t(1) << 24;
+constexpr int64_t kDirectPages = 4096;          // 301 pages: 8.6 us in three launches, 7.0 in two
 constexpr int64_t kMaxCount = int64_t(1) << 23;     // workgroups of 256 threads in a grid's x axis
 
 }  // namespace
@@ -516,7 +545,9 @@ int qg_kv_compact(const qg_kv_pool *pool, const int32_t *table, int64_t ld_table
   c.moves = c.dst + n / 2 + 1;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const dim3 block(kPageThreads);
-  if (int st = launch(kv_count_kernel, dim3(c.num_blocks), block, 0, s, c)) return st;
+  c.direct = n <= kDirectPages;
+  if (!c.direct)
+    if (int st = launch(kv_count_kernel, dim3(c.num_blocks), block, 0, s, c)) return st;
   if (int st = launch(kv_rank_kernel, dim3(c.num_blocks), block, 0, s, c)) return st;
   const int64_t entries = table_rows * table_pages;
   const int64_t groups = (entries + 4 * kPageThreads - 1) / (4 * kPageThreads);
