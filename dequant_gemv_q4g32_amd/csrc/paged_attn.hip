@@ -337,7 +337,7 @@ __device__ __forceinline__ void store_result(const AttnArgs &a, int32_t b, int32
 // WHOLE: workgroup (sequence, head tile) takes that head tile, its waves a share each, and there is
 // nothing to join afterwards. Else the workgroups' waves take the parts of the line.
 template <int D, bool Q8, bool WHOLE>
-__global__ __launch_bounds__(kThreads, D == 64 ? 4 : 2) void attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn_kernel(AttnArgs a) {
   constexpr int NW = kWaves;
   using T = Tile<D, Q8>;
   constexpr int VJ = T::VJ;
