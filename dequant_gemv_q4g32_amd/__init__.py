@@ -12,10 +12,11 @@ device entry point is absent, so calling one raises instead of running anywhere 
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
-import functools
 import os
 import re
+import sys
 from typing import Optional
 
 import numpy as np
@@ -379,29 +380,30 @@ class KVPool:
                    page_tokens)
 
 
-def _paged(fn):
-    """A call on a pool: runs fn(pool, *args) with the pool's device current and `stream` as torch's
-    current stream, so that what it allocates belongs to that stream; fn takes the raw stream as
-    its last argument."""
-    @functools.wraps(fn)
-    def call(pool, *args, stream=None, **kwargs):
-        torch = _torch()
-        index = pool._index
-        if stream is None and torch._C._cuda_getDevice() == index:
-            return fn(pool, *args, **kwargs, stream=torch._C._cuda_getCurrentRawStream(index))
-        with torch.cuda.device(index):
-            if stream is None:
-                return fn(pool, *args, **kwargs, stream=torch._C._cuda_getCurrentRawStream(index))
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-            with torch.cuda.stream(stream):
-                return fn(pool, *args, **kwargs, stream=stream.cuda_stream)
-    return call
+# torch's own accessors behind torch.cuda.current_device and current_stream, which cost a decode
+# step's launch time each
+_th = sys.modules.get("torch")
+_device_now = getattr(getattr(_th, "_C", None), "_cuda_getDevice", None)
+_stream_now = getattr(getattr(_th, "_C", None), "_cuda_getCurrentRawStream", None)
+
+
+@contextlib.contextmanager
+def _on(pool, stream):
+    """The pool's device current and `stream` (None: that device's current one) torch's current
+    stream, so that what a call allocates inside belongs to the stream it runs on."""
+    with _th.cuda.device(pool._index):
+        if stream is None:
+            yield
+            return
+        if isinstance(stream, int):
+            stream = _th.cuda.ExternalStream(stream) if stream else _th.cuda.default_stream()
+        with _th.cuda.stream(stream):
+            yield
 
 
 def _ints(pool, what: str, t, length=None):
     """Address of a dense int32 vector on the pool's device."""
-    if (t.dtype is not _torch().int32 or t.get_device() != pool._index or t.dim() != 1 or not t.is_contiguous()
+    if (t.dtype is not _th.int32 or t.get_device() != pool._index or t.dim() != 1 or not t.is_contiguous()
             or (length is not None and t.numel() != length)):
         raise ValueError(f"{what} must be a dense int32 vector{'' if length is None else f' of {length}'} on {pool.device}")
     return t.data_ptr()
@@ -409,7 +411,7 @@ def _ints(pool, what: str, t, length=None):
 
 def _table(pool, t):
     """(address, leading dimension, rows, pages a row) of a page table."""
-    if (t.dtype is not _torch().int32 or t.get_device() != pool._index or t.dim() != 2
+    if (t.dtype is not _th.int32 or t.get_device() != pool._index or t.dim() != 2
             or not (t.is_contiguous() or t.shape[1] < 2 or t.stride(1) == 1)):
         raise ValueError(f"a page table must be int32 [sequences, pages] with dense rows on {pool.device}")
     rows, pages = t.shape
@@ -418,36 +420,39 @@ def _table(pool, t):
 
 def _rows16(pool, what: str, t, count: int):
     """(address, leading dimension) of fp16 rows [count, kv_heads * head_dim]."""
-    if (t.dtype is not _torch().float16 or t.get_device() != pool._index or t.dim() != 2
+    if (t.dtype is not _th.float16 or t.get_device() != pool._index or t.dim() != 2
             or not (t.is_contiguous() or t.stride(1) == 1) or t.shape != (count, pool.kv_heads * pool.head_dim)):
         raise ValueError(f"{what} must be fp16 [{count}, {pool.kv_heads * pool.head_dim}] with dense rows on {pool.device}")
     return t.data_ptr(), t.stride(0)
 
 
-@_paged
 def kv_append(pool, table, k, v, positions, seqs=None, layer: int = 0, stream=None) -> None:
     """Write token rows into the cache: k, v fp16 [count, kv_heads * head_dim]; row i becomes token
     positions[i] of table row seqs[i] (row i when seqs is None). A row without a place (position
     -1, say) is skipped; the rows of one call must name distinct places."""
+    if stream is not None or _device_now() != pool._index:
+        with _on(pool, stream):
+            return kv_append(pool, table, k, v, positions, seqs, layer)
     count = positions.numel()
     _check(_lib.qg_kv_append(pool._ref, layer, *_table(pool, table), *_rows16(pool, "k", k, count),
                              *_rows16(pool, "v", v, count), None if seqs is None else _ints(pool, "seqs", seqs, count),
-                             _ints(pool, "positions", positions), count, stream), "qg_kv_append")
+                             _ints(pool, "positions", positions), count, _stream_now(pool._index)), "qg_kv_append")
 
 
-@_paged
 def kv_gather(pool, table, positions, seqs=None, k=None, v=None, layer: int = 0, stream=None):
     """Read token rows back, decoded: (k, v) fp16 [count, kv_heads * head_dim], row i token
     positions[i] of table row seqs[i] (row i when seqs is None), zeros where there is none."""
-    torch = _torch()
+    if stream is not None or _device_now() != pool._index:
+        with _on(pool, stream):
+            return kv_gather(pool, table, positions, seqs, k, v, layer)
     count, cols = positions.numel(), pool.kv_heads * pool.head_dim
     if k is None:
-        k = positions.new_empty((count, cols), dtype=torch.float16)
+        k = positions.new_empty((count, cols), dtype=_th.float16)
     if v is None:
-        v = torch.empty_like(k) if k.is_contiguous() else positions.new_empty((count, cols), dtype=torch.float16)
+        v = _th.empty_like(k) if k.is_contiguous() else positions.new_empty((count, cols), dtype=_th.float16)
     _check(_lib.qg_kv_gather(pool._ref, layer, *_table(pool, table), *_rows16(pool, "k", k, count),
                              *_rows16(pool, "v", v, count), None if seqs is None else _ints(pool, "seqs", seqs, count),
-                             _ints(pool, "positions", positions), count, stream), "qg_kv_gather")
+                             _ints(pool, "positions", positions), count, _stream_now(pool._index)), "qg_kv_gather")
     return k, v
 
 
@@ -458,7 +463,6 @@ def paged_attention_bytes(pool, batch: int, heads: int, max_len: int) -> int:
     return out.value
 
 
-@_paged
 def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: Optional[float] = None, window: int = 0,
                     out=None, out_f32: bool = False, lse=None, return_lse: bool = False, workspace=None, layer: int = 0,
                     stream=None):
@@ -470,8 +474,10 @@ def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: 
     with return_lse or when lse (fp32 [batch, heads]) is given. A sequence without tokens gets zeros and
     lse -inf. workspace: uint8 of paged_attention_bytes(...), used by one call at a time; allocated
     here when None."""
-    torch = _torch()
-    if q.dtype is not torch.float16 or q.get_device() != pool._index or q.dim() != 3:
+    if stream is not None or _device_now() != pool._index:
+        with _on(pool, stream):
+            return paged_attention(pool, q, table, lens, max_len, scale, window, out, out_f32, lse, return_lse, workspace, layer)
+    if q.dtype is not _th.float16 or q.get_device() != pool._index or q.dim() != 3:
         raise ValueError(f"q must be fp16 [batch, heads, head_dim] on {pool.device}")
     shape = batch, heads, dim = q.shape
     if dim != pool.head_dim or not (q.is_contiguous() or (q.stride(2) == 1 and (heads == 1 or q.stride(1) == dim))):
@@ -484,65 +490,72 @@ def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: 
     if scale is None:
         scale = dim ** -0.5
     if out is None:
-        out = q.new_empty(shape, dtype=torch.float32) if out_f32 else q.new_empty(shape)
-    elif (out.shape != shape or out.dtype not in (torch.float16, torch.float32) or out.device != pool.device
+        out = q.new_empty(shape, dtype=_th.float32) if out_f32 else q.new_empty(shape)
+    elif (out.shape != shape or out.dtype not in (_th.float16, _th.float32) or out.device != pool.device
           or out.stride(2) != 1 or (heads > 1 and out.stride(1) != dim)):
         raise ValueError(f"out must be fp16 or fp32 [{batch}, {heads}, {dim}] with dense heads on {pool.device}")
     if lse is not None:
-        if lse.shape != (batch, heads) or lse.dtype != torch.float32 or lse.device != pool.device or not lse.is_contiguous():
+        if lse.shape != (batch, heads) or lse.dtype != _th.float32 or lse.device != pool.device or not lse.is_contiguous():
             raise ValueError(f"lse must be dense fp32 [{batch}, {heads}] on {pool.device}")
     elif return_lse:
-        lse = q.new_empty((batch, heads), dtype=torch.float32)
+        lse = q.new_empty((batch, heads), dtype=_th.float32)
     if workspace is None:
         need = paged_attention_bytes(pool, batch, heads, max_len)
-        workspace = q.new_empty(need, dtype=torch.uint8) if need else None
-    elif workspace.dtype != torch.uint8 or workspace.device != pool.device or not workspace.is_contiguous():
+        workspace = q.new_empty(need, dtype=_th.uint8) if need else None
+    elif workspace.dtype != _th.uint8 or workspace.device != pool.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be dense uint8 on {pool.device}")
     _check(_lib.qg_paged_attention(pool._ref, layer, q.data_ptr(), q.stride(0), at, ld, _ints(pool, "lens", lens, batch),
                                    batch, heads, max_len, window, scale, out.data_ptr(), out.stride(0),
-                                   out.dtype is torch.float32, None if lse is None else lse.data_ptr(),
+                                   out.dtype is _th.float32, None if lse is None else lse.data_ptr(),
                                    *((None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())),
-                                   stream), "qg_paged_attention")
+                                   _stream_now(pool._index)), "qg_paged_attention")
     return out if lse is None else (out, lse)
 
 
-@_paged
 def kv_copy_pages(pool, src, dst, stream=None) -> None:
     """Copy pages src[i] to dst[i] (int32 vectors on the device) in every layer of the pool."""
+    if stream is not None or _device_now() != pool._index:
+        with _on(pool, stream):
+            return kv_copy_pages(pool, src, dst)
     count = src.numel()
-    _check(_lib.qg_kv_copy_pages(pool._ref, _ints(pool, "src", src), _ints(pool, "dst", dst, count), count, stream),
-           "qg_kv_copy_pages")
+    _check(_lib.qg_kv_copy_pages(pool._ref, _ints(pool, "src", src), _ints(pool, "dst", dst, count), count,
+                                 _stream_now(pool._index)), "qg_kv_copy_pages")
 
 
-@_paged
 def kv_fork(pool, table, lens, refs, src_rows, dst_rows, new_pages, stream=None) -> None:
     """Table rows dst_rows become second holders of src_rows' tokens: whole pages are shared (refs
     counts them), a partly filled last page is copied to new_pages[i]. table, lens and refs are
     updated in place; free the destination rows first if they hold anything."""
+    if stream is not None or _device_now() != pool._index:
+        with _on(pool, stream):
+            return kv_fork(pool, table, lens, refs, src_rows, dst_rows, new_pages)
     at, ld, rows, pages = _table(pool, table)
     count = src_rows.numel()
     _check(_lib.qg_kv_fork(pool._ref, at, ld, rows, pages, _ints(pool, "lens", lens, rows),
                            _ints(pool, "refs", refs, pool.num_pages), _ints(pool, "src_rows", src_rows),
                            _ints(pool, "dst_rows", dst_rows, count), _ints(pool, "new_pages", new_pages, count), count,
-                           stream), "qg_kv_fork")
+                           _stream_now(pool._index)), "qg_kv_fork")
 
 
-@_paged
 def kv_free(pool, table, lens, refs, rows, stream=None) -> None:
     """Give up the pages of table rows `rows`: their refs fall by one, the rows become empty."""
+    if stream is not None or _device_now() != pool._index:
+        with _on(pool, stream):
+            return kv_free(pool, table, lens, refs, rows)
     at, ld, table_rows, pages = _table(pool, table)
     _check(_lib.qg_kv_free(pool._ref, at, ld, table_rows, pages, _ints(pool, "lens", lens, table_rows),
-                           _ints(pool, "refs", refs, pool.num_pages), _ints(pool, "rows", rows), rows.numel(), stream),
-           "qg_kv_free")
+                           _ints(pool, "refs", refs, pool.num_pages), _ints(pool, "rows", rows), rows.numel(),
+                           _stream_now(pool._index)), "qg_kv_free")
 
 
-@_paged
 def kv_compact(pool, table, refs, table_out=None, refs_out=None, remap=None, live=None, stream=None):
     """Move the held pages of the pool to its first pages, in every layer. Returns (table_out,
     refs_out, remap, live): the table and the counts for the moved pages (pass table and refs
     themselves to update them in place), each page's new index (-1: free), and the number of
     held pages (int32 [1] on the device)."""
-    torch = _torch()
+    if stream is not None or _device_now() != pool._index:
+        with _on(pool, stream):
+            return kv_compact(pool, table, refs, table_out, refs_out, remap, live)
     at, ld, rows, pages = _table(pool, table)
     need = ctypes.c_int64()
     _check(_lib.qg_kv_compact_bytes(pool._ref, ctypes.byref(need)), "qg_kv_compact_bytes")
@@ -558,7 +571,7 @@ def kv_compact(pool, table, refs, table_out=None, refs_out=None, remap=None, liv
     _check(_lib.qg_kv_compact(pool._ref, at, ld, to[0], to[1], rows, pages, _ints(pool, "refs", refs, pool.num_pages),
                               _ints(pool, "refs_out", refs_out, pool.num_pages),
                               _ints(pool, "remap", remap, pool.num_pages), _ints(pool, "live", live, 1),
-                              workspace.data_ptr(), need.value, stream), "qg_kv_compact")
+                              workspace.data_ptr(), need.value, _stream_now(pool._index)), "qg_kv_compact")
     return table_out, refs_out, remap, live
 
 
