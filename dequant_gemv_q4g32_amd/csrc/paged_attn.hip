@@ -57,21 +57,28 @@ __device__ __forceinline__ int32_t scalar_load(const int32_t *p) {
 }
 
 // What of sequence b is seen: tokens [first, len), in tiles from base = first rounded down.
+// On the line (below) a head tile of few tiles counts one unit more: its start costs a wave about as
+// much as half a tile, which a wave with many short sequences would be late by.
 struct Seen {
   int32_t first, len, base, tiles;
+  uint32_t lead, units;
 };
+constexpr int32_t kShort = 16;                       // tiles below which a head tile has that unit
+template <bool WHOLE>
 __device__ __forceinline__ Seen seen_of(const AttnArgs &a, int32_t raw) {
   Seen s;
   s.len = min(max(raw, 0), a.max_len);
   s.first = a.window ? max(0, s.len - a.window) : 0;
   s.base = s.first & ~(kTile - 1);
   s.tiles = max(1, (s.len - s.base + kTile - 1) / kTile);      // an empty sequence still gets its zeros written
+  s.lead = !WHOLE && s.tiles < kShort ? 1 : 0;
+  s.units = (uint32_t)s.tiles + s.lead;
   return s;
 }
 
-// The split. All tiles of all sequences and head tiles, sequence by sequence and head tile by head
-// tile, are one line of `total` tiles (below 2^31), of which wave v of `waves` takes the v-th part:
-// quota tiles, and one more if v < extra. Every wave finds its place on the line from lens alone.
+// The split. The units of all sequences and head tiles, sequence by sequence and head tile by head
+// tile, are one line of `total` units (below 2^31), of which wave v of `waves` takes the v-th part:
+// quota units, and one more if v < extra. Every wave finds its place on the line from lens alone.
 // A head tile [u0, u1) of the line is thus covered by neighbouring waves. A wave that goes on
 // past u1 (its range ends beyond) has left the head tile behind as a part of its own; the waves whose
 // range ends within the head tile end on it, and those of one workgroup join their parts. So the
@@ -80,7 +87,7 @@ __device__ __forceinline__ Seen seen_of(const AttnArgs &a, int32_t raw) {
 struct Line {
   uint32_t total, waves, quota, extra, first;
   __device__ __forceinline__ uint32_t start(uint32_t v) const { return first + v * quota + min(v, extra); }
-  // the wave that holds tile u
+  // the wave that holds unit u
   __device__ __forceinline__ uint32_t holder(uint32_t u) const {
     const uint32_t big = extra * (quota + 1);
     return u < big ? u / (quota + 1) : extra + (u - big) / quota;
@@ -276,7 +283,9 @@ __device__ __forceinline__ float *slot_of(const AttnArgs &a, uint32_t slot, int 
 // A wave's part of one head tile of one sequence.
 struct Segment {
   uint32_t u0, u1;           // the head tile on the line
-  uint32_t at, end;          // the wave's part of it
+  uint32_t tile0;            // where its tiles start
+  uint32_t at, end;          // the wave's part of it; at < tile0: a tile before the first, all masked
+  bool from_start;           // the wave's part starts with the head tile
   int32_t b;
   int32_t first, len, base;  // what of the sequence is seen
   int32_t ht, h0, rows;      // head tile of the sequence, its first head, heads
@@ -284,20 +293,23 @@ struct Segment {
   const int32_t *row;        // the sequence's row of the table
 };
 
-// The segment at tile `at` < end of the line, at or after sequence b, which starts at seq_at.
+// The segment at unit `at` < end of the line, at or after sequence b, which starts at seq_at.
+template <bool WHOLE>
 __device__ __forceinline__ Segment segment_at(const AttnArgs &a, uint32_t at, uint32_t end, int32_t b, uint32_t seq_at) {
   Segment g;
-  Seen s = seen_of(a, scalar_load(a.lens + b));
-  while (at - seq_at >= (uint32_t)s.tiles * a.head_tiles) {
-    seq_at += (uint32_t)s.tiles * a.head_tiles;
+  Seen s = seen_of<WHOLE>(a, scalar_load(a.lens + b));
+  while (at - seq_at >= s.units * a.head_tiles) {
+    seq_at += s.units * a.head_tiles;
     ++b;
-    s = seen_of(a, scalar_load(a.lens + b));
+    s = seen_of<WHOLE>(a, scalar_load(a.lens + b));
   }
-  g.ht = (int32_t)((at - seq_at) / (uint32_t)s.tiles);
-  g.u0 = seq_at + (uint32_t)g.ht * s.tiles;
-  g.u1 = g.u0 + s.tiles;
-  g.at = at;
+  g.ht = (int32_t)((at - seq_at) / s.units);
+  g.u0 = seq_at + (uint32_t)g.ht * s.units;
+  g.u1 = g.u0 + s.units;
+  g.tile0 = g.u0 + s.lead;
   g.end = min(end, g.u1);
+  g.from_start = at == g.u0;
+  g.at = at < g.tile0 && g.tile0 < g.end ? g.tile0 : at;
   g.b = b;
   g.first = s.first;
   g.len = s.len;
@@ -355,7 +367,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
   if constexpr (WHOLE) {
     from_b = blockIdx.x / a.head_tiles;
     from_at = 0;
-    const uint32_t tiles = seen_of(a, scalar_load(a.lens + from_b)).tiles;
+    const uint32_t tiles = seen_of<true>(a, scalar_load(a.lens + from_b)).units;
     line = make_line(tiles, NW);
     line.first = (blockIdx.x - from_b * a.head_tiles) * tiles;
     v0 = 0;
@@ -363,7 +375,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
     const int32_t per = (a.batch + kThreads - 1) / kThreads, my_b = (int32_t)threadIdx.x * per;
     uint32_t mine = 0;
     for (int32_t i = 0; i < per; ++i)
-      if (my_b + i < a.batch) mine += (uint32_t)seen_of(a, a.lens[my_b + i]).tiles * a.head_tiles;
+      if (my_b + i < a.batch) mine += seen_of<false>(a, a.lens[my_b + i]).units * a.head_tiles;
     uint32_t total;
     const uint32_t before = block_scan(mine, scan, total);
     if (blockIdx.x == 0) {                           // for the join
@@ -371,7 +383,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
       for (int32_t i = 0; i < per; ++i)
         if (my_b + i < a.batch) {
           a.starts[my_b + i] = at;
-          at += (uint32_t)seen_of(a, a.lens[my_b + i]).tiles * a.head_tiles;
+          at += seen_of<false>(a, a.lens[my_b + i]).units * a.head_tiles;
         }
       if (threadIdx.x == 0) a.starts[a.batch] = total;
     }
@@ -401,14 +413,14 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
     half8_t q[T::KD];
     Block blk[2];
     int32_t page[2];                                 // of the tile in t; below 0: none
-    cur = segment_at(a, line.start(v), end, (int32_t)from_b, from_at);
+    cur = segment_at<WHOLE>(a, line.start(v), end, (int32_t)from_b, from_at);
     Segment fetch = cur;                             // the segment of the tile in t, fetch.at that tile
-    auto token = [&](int st) { return fetch.base + (int32_t)(fetch.at - fetch.u0) * kTile + 16 * st; };
+    auto token = [&](int st) { return fetch.base + (int32_t)(fetch.at - fetch.tile0) * kTile + 16 * st; };
     auto look_up = [&]() {
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
         const int32_t tok = token(st);
-        page[st] = fetch.at < end && tok < fetch.len ? scalar_load(fetch.row + (tok >> a.tok_shift)) : -1;
+        page[st] = fetch.at < end && tok >= 0 && tok < fetch.len ? scalar_load(fetch.row + (tok >> a.tok_shift)) : -1;
       }
     };
     auto locate = [&]() {
@@ -461,7 +473,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
         more = fetch.at + 1 < end;
         if (++fetch.at == fetch.end) {
           inside = false;
-          if (more) fetch = segment_at(a, fetch.at, end, fetch.b, fetch.u0 - (fetch.u1 - fetch.u0) * fetch.ht);
+          if (more) fetch = segment_at<WHOLE>(a, fetch.at, end, fetch.b, fetch.u0 - (fetch.u1 - fetch.u0) * fetch.ht);
         }
         look_up();
         f32x4 x[2];
@@ -522,7 +534,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
       l += __shfl_xor(l, 32);
       if (more) {
         // going on past this head tile: its result if the wave had all of it, else a part
-        float *slot = cur.at == cur.u0 ? nullptr : slot_of(a, 2 * v, D);
+        float *slot = cur.from_start ? nullptr : slot_of(a, 2 * v, D);
         if (c < cur.rows) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -589,9 +601,9 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(AttnArgs a, uint32_t
   __shared__ f32x4 sums[kSplit][kLanes];
   const int32_t b = blockIdx.x / a.head_tiles, ht = blockIdx.x - b * a.head_tiles;
   const Line line = make_line((uint32_t)scalar_load(a.starts_in + a.batch), waves);
-  const Seen s = seen_of(a, scalar_load(a.lens + b));
-  const uint32_t u0 = (uint32_t)scalar_load(a.starts_in + b) + (uint32_t)ht * (uint32_t)s.tiles;
-  const uint32_t u1 = u0 + s.tiles, w0 = line.holder(u0), w1 = line.holder(u1 - 1);
+  const Seen s = seen_of<false>(a, scalar_load(a.lens + b));
+  const uint32_t u0 = (uint32_t)scalar_load(a.starts_in + b) + (uint32_t)ht * s.units;
+  const uint32_t u1 = u0 + s.units, w0 = line.holder(u0), w1 = line.holder(u1 - 1);
   if (w0 == w1) return;
   // parts in order: those of workgroups, from the first of their waves, then the last wave's if it
   // went on. Wave w0 ends on the head tile, since it is not the last.
@@ -698,7 +710,7 @@ int attn_shape(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max
   if (int st = kv_pool_layout(pool, L)) return st;
   if (batch < 0 || heads < 1 || heads % pool->kv_heads || heads > (1 << 22) || batch > (1 << 22) / heads) return QG_ERR_SHAPE;
   if (max_len < 0 || max_len > (1 << 30)) return QG_ERR_SHAPE;
-  if (batch * heads * attn_tiles(max_len, 0) > 0x7FFFFFFF) return QG_ERR_SHAPE;   // the line fits 31 bits
+  if (batch * heads * (attn_tiles(max_len, 0) + 1) > 0x7FFFFFFF) return QG_ERR_SHAPE;   // the line fits 31 bits
   return QG_OK;
 }
 

@@ -440,6 +440,7 @@ int64_t compact_ints(int64_t num_pages) { return (num_pages + kScanPages - 1) / 
 
 constexpr int64_t kCompactPages = int64_t(1) << 24;
 constexpr int64_t kDirectPages = 4096;          // 301 pages: 8.6 us in three launches, 7.0 in two
+constexpr int64_t kMaxForks = 4096;                  // every workgroup of a fork looks through all of them
 constexpr int64_t kMaxCount = int64_t(1) << 23;     // workgroups of 256 threads in a grid's x axis
 
 }  // namespace
@@ -482,7 +483,7 @@ int qg_kv_fork(const qg_kv_pool *pool, int32_t *table, int64_t ld_table, int64_t
   KvLayout L;
   if (int st = kv_pool_layout(pool, &L)) return st;
   if (int st = kv_table_check(table, ld_table, table_rows, table_pages)) return st;
-  if (count < 0 || count > kMaxCount) return QG_ERR_SHAPE;
+  if (count < 0 || count > kMaxForks) return QG_ERR_SHAPE;
   if (count == 0 || table_rows == 0) return QG_OK;
   if (!lens || !refs || !src_rows || !dst_rows || !new_pages) return QG_ERR_NULL;
   if (misaligned(lens, 4) || misaligned(refs, 4) || misaligned(src_rows, 4) || misaligned(dst_rows, 4) ||

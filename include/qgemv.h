@@ -454,8 +454,8 @@ int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q,
 
 /* Copy whole pages in every layer: page src[i] to page dst[i] for i < count (device arrays). A
  * pair with an index outside [0, num_pages) is skipped. No page may be a destination twice, or
- * both a source and a destination of different pairs. count is at most 2^23 (also of forks and
- * freed rows below). */
+ * both a source and a destination of different pairs. count is at most 2^23 (also of freed
+ * rows below). */
 int qg_kv_copy_pages(const qg_kv_pool *pool, const int32_t *src, const int32_t *dst, int64_t count, void *stream);
 
 /* Fork: for i < count, table row dst_rows[i] becomes a second holder of row src_rows[i]'s
@@ -465,7 +465,8 @@ int qg_kv_copy_pages(const qg_kv_pool *pool, const int32_t *src, const int32_t *
  * before is overwritten, not released (qg_kv_free releases it). new_pages[i] is read only when
  * a last page is copied. A fork is skipped, its row left as it was, when a row is outside the
  * table, when dst_rows[i] is also a source row or an earlier destination row of the call, or
- * when a copy is needed and new_pages[i] is outside the pool or named earlier in the call. */
+ * when a copy is needed and new_pages[i] is outside the pool or named earlier in the call.
+ * count is at most 4096. */
 int qg_kv_fork(const qg_kv_pool *pool, int32_t *table, int64_t ld_table, int64_t table_rows, int64_t table_pages,
                int32_t *lens, int32_t *refs, const int32_t *src_rows, const int32_t *dst_rows,
                const int32_t *new_pages, int64_t count, void *stream);

@@ -157,11 +157,12 @@ def test_scales_and_peaked_scores(scale):
     check_attention(out, lse, paged.attention(c, 0, q, table, lens, 512, scale), 500, 64)
 
 
-def test_infinite_and_nan_entries_stay_in_their_head():
+@pytest.mark.parametrize("kind", ["q8", "f16"])
+def test_infinite_and_nan_entries_stay_in_their_head(kind):
     """An infinite q makes its own head NaN or infinite as the formula says; other heads and
     sequences are untouched."""
     lens = [50, 50]
-    rng, c, table, q = _problem("f16", 8, 2, 64, 16, lens, 12)
+    rng, c, table, q = _problem(kind, 8, 2, 64, 16, lens, 12)
     clean = qg.paged_attention(upload(c), dev(q, np.float16), dev(table), dev(lens), return_lse=True)
     q2 = q.copy()
     q2[0, 3, 5] = np.inf

@@ -181,6 +181,24 @@ def test_random_batches(seed):
     check_attention(out, lse, ref, most, dim)
 
 
+@pytest.mark.parametrize("seed,batch,kv_heads,group,dim,most", [
+    (1, 300, 8, 4, 128, 600), (2, 300, 8, 1, 64, 70), (3, 700, 4, 2, 64, 33), (4, 90, 8, 8, 128, 1500), (5, 257, 3, 17, 128, 480),
+    (6, 64, 1, 16, 256, 700), (7, 1000, 8, 1, 64, 500), (8, 31, 16, 2, 128, 5000)])
+def test_split_over_many_sequences(seed, batch, kv_heads, group, dim, most):
+    """Many sequences under a long max_len, so that a wave's part of the split starts and ends anywhere
+    in them: some of one tile, some empty, some longer than a wave's part."""
+    rng = np.random.default_rng(seed)
+    kind, tokens = ("q8", "f16")[seed % 2], (16, 32, 64)[seed % 3]
+    pool, values, gen = _filled(kind, kv_heads, dim, tokens, 200, seed)
+    lens = rng.integers(0, most + 1, batch) * (rng.random(batch) < 0.9)
+    table = dev(rng.integers(0, 200, (batch, 8192 // tokens)))
+    q = (torch.randn((batch, group * kv_heads, dim), generator=gen, device="cuda") * 1.5).half()
+    window = 0 if seed % 4 else 100
+    out, lse = qg.paged_attention(pool, q, table, dev(lens), window=window, out_f32=True, return_lse=True)
+    assert qg.paged_attention_bytes(pool, batch, group * kv_heads, 8192) > 0
+    check_attention(out, lse, _torch_reference(*values, table, lens.tolist(), q, dim ** -0.5, window), most, dim)
+
+
 # ---- graphs ------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("kind,max_len", [("q8", 256), ("f16", 8192)])
