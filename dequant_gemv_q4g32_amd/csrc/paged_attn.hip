@@ -125,7 +125,8 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *lds, uint32
 
 // 16 codes of one group to 16 fp16 values: code + 128 under the exponent of 1024 (a byte permute
 // and an exact subtraction for two), times the scale, rounded to fp16 as qg_kv_dequantize does.
-// MODE.FP16_OVFL (set at the start of the kernel) saturates the product at +-65504.
+// MODE.FP16_OVFL (set at the start of the kernel) saturates the product at +-65504: without it the
+// one scale that can pass it (516) would need two more operations for every pair.
 __device__ __forceinline__ uint32_t scaled_pair(uint32_t magic_pair, uint32_t scale) {
   const h2_t off = __builtin_bit_cast(h2_t, 0x64806480u);       // 1152 = 1024 + 128
   return __builtin_bit_cast(uint32_t, (__builtin_bit_cast(h2_t, magic_pair) - off) * __builtin_bit_cast(h2_t, scale));
@@ -227,6 +228,21 @@ __device__ __forceinline__ f32x4 scores(const Tile<D, Q8> &t, int st, const half
       s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, t.k[st][i]), q[i], s, 0, 0, 0);
   }
   return s;
+}
+
+// Whether the lane's part of q holds a NaN or an infinity. FP16_OVFL makes the matrix units take
+// either as a finite number, so with int8 pages such a head is marked instead: its scores are
+// infinite or NaN against any finite K, and its softmax is NaN.
+template <int KD>
+__device__ __forceinline__ bool nonfinite(const half8_t *q) {
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < KD; ++i) {
+    const u32x4 x = __builtin_bit_cast(u32x4, q[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bad |= (x[j] & 0x7C007C00u) + 0x04000400u;   // an exponent of ones carries into bit 15
+  }
+  return (bad & 0x80008000u) != 0;
 }
 
 // O^T += V^T P^T with the weights as hi + lo fp16 pairs. Column c of V^T's block j is element
@@ -456,6 +472,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
       ref = -INFINITY;
       l = 0.f;
       bool inside = true;                            // the tile in t is of segment cur
+      bool fresh = true;                             // and its first
       while (inside) {
         const int32_t t0 = token(0);
         const bool full = t0 >= cur.first && t0 + kTile <= cur.len && page[0] >= 0 && page[1] >= 0;
@@ -479,6 +496,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
         f32x4 x[2];
 #pragma unroll
         for (int st = 0; st < 2; ++st) x[st] = scores<D, Q8>(t, st, q);
+        if (Q8 && fresh) {
+          if (nonfinite<T::KD>(q)) l = __builtin_nanf("");
+          fresh = false;
+        }
         locate();
         if (more && !inside) load_q();
         load_k<D, Q8>(a, blk, t);

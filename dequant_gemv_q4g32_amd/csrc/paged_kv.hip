@@ -45,67 +45,88 @@ __device__ __forceinline__ uint8_t *row_page(const RowsArgs &a, uint32_t row, in
   return a.pool + (int64_t)page * a.page_bytes;
 }
 
-// A lane takes 8 elements of K and the same 8 of V: both share the look-up of the place. They lie in
-// one head and one group of 32, and the 4 lanes of a group are neighbours in a wave (head_dim / 8
-// lanes a head, a multiple of 4).
-template <bool Q8, bool APPEND>
-__global__ __launch_bounds__(kPageThreads) void kv_rows_kernel(RowsArgs a) {
+// Where 8 elements of a row lie in its page: the lane's elements are in one head and one group of
+// 32, and the 4 lanes of a group are neighbours in a wave (head_dim / 8 lanes a head, a multiple of 4).
+template <bool Q8>
+struct RowPlace {
+  uint8_t *part;                 // the head's part of the page; nullptr: no place
+  int64_t off[2], scale_off[2];  // of K and V
+};
+template <bool Q8>
+__device__ __forceinline__ RowPlace<Q8> row_place(const RowsArgs &a, uint32_t row, uint32_t c) {
+  RowPlace<Q8> p;
+  int32_t at;
+  uint8_t *page = row_page(a, row, at);
+  const uint32_t head = c >> a.lane_shift, e = 8 * (c & ((1u << a.lane_shift) - 1));   // element within the head
+  const int32_t dim = 8 << a.lane_shift, group = e / kKvGroup;
+  const int64_t elem = (int64_t)at * dim + e;
+  p.part = page ? page + (int64_t)head * a.head_bytes : nullptr;
+  p.off[0] = Q8 ? elem : 2 * elem;
+  p.off[1] = a.v_off + p.off[0];
+  p.scale_off[0] = a.ks_off + 2 * ((int64_t)at * (dim / kKvGroup) + group);
+  p.scale_off[1] = a.vs_off + 2 * (((int64_t)group << a.tok_shift) + at);
+  return p;
+}
+
+// A lane takes 8 elements of K and the same 8 of V: both share the look-up of the place, and are on
+// their way while it runs. 2048 int8 rows of 8 heads of 128: 5.7 us; a decode step's 64 rows: 3.3 us,
+// a launch and the look-up's latency.
+template <bool Q8>
+__global__ __launch_bounds__(kPageThreads) void kv_append_kernel(RowsArgs a) {
   const uint32_t i = blockIdx.x * kPageThreads + threadIdx.x;
   const bool live = i < a.lanes;
   const uint32_t row = live ? i / a.per_row : 0, c = live ? i - row * a.per_row : 0;
   u32x4 v[2] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
-  if constexpr (APPEND) {                            // on their way while the place is looked up
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
-      if (live) v[w] = *reinterpret_cast<const u32x4 *>(a.x[w] + (int64_t)row * a.ldx[w] + 8 * c);
+  for (int w = 0; w < 2; ++w)
+    if (live) v[w] = *reinterpret_cast<const u32x4 *>(a.x[w] + (int64_t)row * a.ldx[w] + 8 * c);
+  const RowPlace<Q8> p = row_place<Q8>(a, row, c);
+  uint16_t d[2];
+  u32x2 codes[2];
+  if constexpr (Q8) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) codes[w] = kv_encode8(v[w], d[w]);   // every lane: the quad's maximum needs all four
   }
-  int32_t at = 0;
-  uint8_t *page = live ? row_page(a, row, at) : nullptr;
-  const uint32_t head = c >> a.lane_shift, e = 8 * (c & ((1u << a.lane_shift) - 1));   // element within the head
-  const int32_t dim = 8 << a.lane_shift, group = e / kKvGroup;
-  uint8_t *part = page + (int64_t)head * a.head_bytes;
-  const int64_t elem = (int64_t)at * dim + e;
-  const int64_t off[2] = {Q8 ? elem : 2 * elem, a.v_off + (Q8 ? elem : 2 * elem)};
-  const int64_t scale_off[2] = {a.ks_off + 2 * ((int64_t)at * (dim / kKvGroup) + group),
-                                a.vs_off + 2 * (((int64_t)group << a.tok_shift) + at)};
-  if constexpr (APPEND) {
-    uint16_t d[2];
-    u32x2 codes[2];
+  if (!live || !p.part) return;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
     if constexpr (Q8) {
-#pragma unroll
-      for (int w = 0; w < 2; ++w) codes[w] = kv_encode8(v[w], d[w]);   // every lane: the quad's maximum needs all four
+      *reinterpret_cast<u32x2 *>(p.part + p.off[w]) = codes[w];
+      if ((c & 3) == 0) *reinterpret_cast<uint16_t *>(p.part + p.scale_off[w]) = d[w];
+    } else {
+      *reinterpret_cast<u32x4 *>(p.part + p.off[w]) = v[w];
     }
-    if (!page) return;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      if constexpr (Q8) {
-        *reinterpret_cast<u32x2 *>(part + off[w]) = codes[w];
-        if ((c & 3) == 0) *reinterpret_cast<uint16_t *>(part + scale_off[w]) = d[w];
-      } else {
-        *reinterpret_cast<u32x4 *>(part + off[w]) = v[w];
-      }
-    }
-  } else {
-    if (!live) return;
-    if (page) {
-      if constexpr (Q8) {
-        u32x2 codes[2];
-        uint16_t d[2];
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          codes[w] = *reinterpret_cast<const u32x2 *>(part + off[w]);
-          d[w] = *reinterpret_cast<const uint16_t *>(part + scale_off[w]);
-        }
-#pragma unroll
-        for (int w = 0; w < 2; ++w) v[w] = kv_decode8(codes[w], half_bits(d[w]));
-      } else {
-#pragma unroll
-        for (int w = 0; w < 2; ++w) v[w] = *reinterpret_cast<const u32x4 *>(part + off[w]);
-      }
-    }
-#pragma unroll
-    for (int w = 0; w < 2; ++w) *reinterpret_cast<u32x4 *>(a.x[w] + (int64_t)row * a.ldx[w] + 8 * c) = v[w];
   }
+}
+
+// The way back. 8192 int8 rows of 8 heads of 128 (51 MB read and written) take 12.2 us: a launch
+// and the three dependent loads before the data's own, then the data at the streaming rate. Two
+// rows a lane gained 5% there and lost 25% of a decode step's 64 rows (2.7 us).
+template <bool Q8>
+__global__ __launch_bounds__(kPageThreads) void kv_gather_kernel(RowsArgs a) {
+  const uint32_t i = blockIdx.x * kPageThreads + threadIdx.x;
+  if (i >= a.lanes) return;
+  const uint32_t row = i / a.per_row, c = i - row * a.per_row;
+  const RowPlace<Q8> p = row_place<Q8>(a, row, c);
+  u32x4 v[2] = {u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
+  if (p.part) {
+    if constexpr (Q8) {
+      u32x2 codes[2];
+      uint16_t d[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        codes[w] = *reinterpret_cast<const u32x2 *>(p.part + p.off[w]);
+        d[w] = *reinterpret_cast<const uint16_t *>(p.part + p.scale_off[w]);
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w) v[w] = kv_decode8(codes[w], half_bits(d[w]));
+    } else {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) v[w] = *reinterpret_cast<const u32x4 *>(p.part + p.off[w]);
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) *reinterpret_cast<u32x4 *>(a.x[w] + (int64_t)row * a.ldx[w] + 8 * c) = v[w];
 }
 
 // ---- page copies ----------------------------------------------------------------------------
@@ -426,13 +447,12 @@ int kv_rows(bool append, const qg_kv_pool *pool, int64_t layer, const int32_t *t
   a.per_row = (uint32_t)per_row;
   a.lane_shift = log2_of(pool->head_dim / 8);
   a.tok_shift = log2_of(pool->page_tokens);
-  const dim3 grid((a.lanes + kPageThreads - 1) / kPageThreads), block(kPageThreads);
+  const bool q8 = pool->kind == QG_KV_Q8;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (pool->kind == QG_KV_Q8)
-    return append ? launch(kv_rows_kernel<true, true>, grid, block, 0, s, a)
-                  : launch(kv_rows_kernel<true, false>, grid, block, 0, s, a);
-  return append ? launch(kv_rows_kernel<false, true>, grid, block, 0, s, a)
-                : launch(kv_rows_kernel<false, false>, grid, block, 0, s, a);
+  const dim3 block(kPageThreads), grid((a.lanes + kPageThreads - 1) / kPageThreads);
+  if (append)
+    return q8 ? launch(kv_append_kernel<true>, grid, block, 0, s, a) : launch(kv_append_kernel<false>, grid, block, 0, s, a);
+  return q8 ? launch(kv_gather_kernel<true>, grid, block, 0, s, a) : launch(kv_gather_kernel<false>, grid, block, 0, s, a);
 }
 
 // Workspace of a compaction: block counts, the two lists and their length.

@@ -427,7 +427,8 @@ int qg_kv_gather(const qg_kv_pool *pool, int64_t layer, const int32_t *table, in
  *   s_j = scale * <q[b][h], K[g][j]>   for the tokens max(0, n - window) <= j < n (all j < n
  *                                      when window is 0) that lie in a page of the pool,
  *   out[b][h] = sum_j e^(s_j) V[g][j] / sum_j e^(s_j),   lse[b][h] = ln sum_j e^(s_j).
- * A sequence without such a token gets out = 0 and lse = -inf. q: fp16, row b at q + b * ldq,
+ * A sequence without such a token gets out = 0 and lse = -inf; a head whose q holds a NaN or an
+ * infinity gets NaN. q: fp16, row b at q + b * ldq,
  * heads dense; out: fp16, or fp32 with out_f32 != 0, row b at out + b * ldo, heads dense; lse:
  * fp32 [batch][heads], or NULL. The new token's own K and V are in the cache before the call
  * (qg_kv_append) and counted by lens. Products, the softmax and its sums are fp32; the weights
