@@ -1,4 +1,27 @@
 // Attention of one new token a sequence over a paged KV cache, gfx950.
+//
+// For a sequence b, a head h of KV head g and its cached tokens j:
+//   s_j = scale <q, K_j>,  out = sum_j e^(s_j) V_j / sum_j e^(s_j)
+// in one pass over K and V. With powers of two (s in units of log2) and a running reference `ref`
+// per head, a wave keeps o = sum 2^(s_j - ref) V_j and l = sum 2^(s_j - ref); moving ref scales both
+// by 2^(old - new), and two such results join by scaling to the larger ref.
+//
+// Work of a wave: up to 16 heads of one KV head (a head tile) against 32 tokens a step, two blocks
+// of 16. S^T = K Q^T and O^T += V^T P^T run on v_mfma_f32_16x16x32_f16 with fp32 sums. S^T's lanes
+// hold one head and four tokens each, which is the layout the weights P^T need as the next
+// product's operand, so the softmax never leaves the registers: no shuffle but the largest score's,
+// and that only when ref moves. int8 K and V are decoded to fp16 in registers; the row-major V is
+// turned by byte permutes on the way (8 tokens of one element are an operand). The weights meet V
+// as hi + lo fp16 pairs, 22 bits.
+//
+// What bounds it: each cached byte is read once, so HBM, and for int8 also instruction issue (about
+// 380 vector and 130 scalar instructions a step of 8.7 KB; a wave alone needs 1.3 us for it). The
+// next step's K is on its way while the softmax and the products with V run, its V from then on.
+// Measured (GPU time; a plain stream of reads reaches 6.8 TB/s here): 64 sequences of 8192 tokens,
+// 64 heads on 8 of 128: fp16 322 us = 6.7 TB/s, int8 187 us = 6.1 TB/s; one of 131072 tokens, int8,
+// 55 us = 5.2 TB/s; 32 of up to 8192, int8, 47 us = 4.9 TB/s; 48 of up to 6007 with one KV head of
+// 256, int8, 28 us; one of 1000 tokens 10 us, of 100 tokens 6 us (a launch and four dependent
+// memory latencies: length, page, K, and the first step). HBM reads are the algorithm's bytes.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -39,13 +62,14 @@ typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 4;                          // waves of a workgroup that takes a part of the line
-constexpr int kTile = 32;                          // tokens of a wave's step, the grain of the split: two 16-token blocks
+constexpr int kWaves = 4;                          // waves of a workgroup
+constexpr int kTile = 32;                          // tokens of a wave's step, the grain of the split
 constexpr int kThreads = 64 * kWaves;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-// Weights are 2^(s - ref) with ref moved to (largest s) - 7 once a score passes ref + 15: they
-// stay below fp16's 65504, and numbers down to 2^-31 of the largest keep their bits.
+// Weights are 2^(s - ref) with ref moved to (largest s) - 7 once a score passes ref + 15: they stay
+// below fp16's 65504 and small ones lose nothing above 2^-31 of the largest, while most steps find
+// ref good as it is.
 constexpr float kLow = 7.0f, kHigh = 15.0f;
 
 template <typename T>
@@ -58,7 +82,8 @@ __device__ __forceinline__ int32_t scalar_load(const int32_t *p) {
 
 // What of sequence b is seen: tokens [first, len), in tiles from base = first rounded down.
 // On the line (below) a head tile of few tiles counts one unit more: its start costs a wave about as
-// much as half a tile, which a wave with many short sequences would be late by.
+// much as half a tile, which a wave with many short sequences would be late by (32 sequences of up to
+// 8192 tokens, some of none or one: 56 us without the unit, 51 with it).
 struct Seen {
   int32_t first, len, base, tiles;
   uint32_t lead, units;
@@ -83,7 +108,8 @@ __device__ __forceinline__ Seen seen_of(const AttnArgs &a, int32_t raw) {
 // past u1 (its range ends beyond) has left the head tile behind as a part of its own; the waves whose
 // range ends within the head tile end on it, and those of one workgroup join their parts. So the
 // parts of a head tile are: one for each workgroup with such waves (named by the first of them,
-// the leader), and one for a wave that goes on past u1.
+// the leader), and one for a wave that goes on past u1. A workgroup for each head tile instead would
+// put one long sequence on as many CUs as it has KV heads, and wait for the longest of ragged ones.
 struct Line {
   uint32_t total, waves, quota, extra, first;
   __device__ __forceinline__ uint32_t start(uint32_t v) const { return first + v * quota + min(v, extra); }
@@ -153,7 +179,10 @@ struct Block {
   uint32_t place;
 };
 
-
+// Cache policy: V's codes past the caches (each line is one instruction's), K cached, since two or
+// four instructions share each of its lines, and the scales, whose lines many lanes share. 64
+// sequences of 8192 tokens: all cached 361 us (fp16) and 205 us (int8), all past the caches 316 and
+// 192, this way 322 and 187, and the ragged and short cases all fastest.
 template <int N, int AUX>
 __device__ __forceinline__ void load_words(rsrc_t r, uint32_t voff, uint32_t soff, uint32_t *w) {
   if constexpr (N == 1) {
@@ -288,10 +317,12 @@ __device__ __forceinline__ void accumulate(const Tile<D, Q8> &t, half8_t hi, hal
   }
 }
 
-// A part in the workspace: [rows][D] sums, then each row's largest score and denominator, in whole
-// 16 bytes. Slot 2 v:
-// what wave v left behind; slot 2 v + 1: what the waves of its workgroup from v on ended on.
-__host__ __device__ __forceinline__ int32_t slot_floats(int32_t rows, int32_t dim) { return rows * dim + (2 * rows + 3) / 4 * 4; }
+// A part in the workspace: [rows][D] sums, then each row's reference and denominator, in whole 16
+// bytes. Slot 2 v: what wave v left behind; slot 2 v + 1: what the waves of its workgroup from v on
+// ended on.
+__host__ __device__ __forceinline__ int32_t slot_floats(int32_t rows, int32_t dim) {
+  return rows * dim + (2 * rows + 3) / 4 * 4;
+}
 __device__ __forceinline__ float *slot_of(const AttnArgs &a, uint32_t slot, int D) {
   return a.slots + (int64_t)slot * slot_floats(a.rows, D);
 }
@@ -366,13 +397,12 @@ __device__ __forceinline__ void store_result(const AttnArgs &a, int32_t b, int32
 // nothing to join afterwards. Else the workgroups' waves take the parts of the line.
 template <int D, bool Q8, bool WHOLE>
 __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn_kernel(AttnArgs a) {
-  constexpr int NW = kWaves;
   using T = Tile<D, Q8>;
   constexpr int VJ = T::VJ;
   constexpr int kPad = D + 4;                        // LDS rows of neighbouring heads start in other banks
-  extern __shared__ float sums[];                    // [NW][rows][kPad], rows = heads of a tile
-  __shared__ uint32_t scan[NW], found[2][NW];
-  __shared__ float wave_m[NW][16], wave_l[NW][16];
+  extern __shared__ float sums[];                    // [kWaves][rows][kPad], rows = heads of a tile
+  __shared__ uint32_t scan[kWaves], found[2][kWaves];
+  __shared__ float wave_m[kWaves][16], wave_l[kWaves][16];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
   if constexpr (Q8) __builtin_amdgcn_s_setreg(1 | (23 << 6) | (0 << 11), 1);   // hwreg(MODE, 23, 1): FP16_OVFL
   const uint32_t vs_lane = 2 * ((((VJ * (uint32_t)c) / 32) << a.tok_shift) + 4 * g);   // the lane's V scales
@@ -384,7 +414,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
     from_b = blockIdx.x / a.head_tiles;
     from_at = 0;
     const uint32_t tiles = seen_of<true>(a, scalar_load(a.lens + from_b)).units;
-    line = make_line(tiles, NW);
+    line = make_line(tiles, kWaves);
     line.first = (blockIdx.x - from_b * a.head_tiles) * tiles;
     v0 = 0;
   } else {
@@ -403,11 +433,11 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
         }
       if (threadIdx.x == 0) a.starts[a.batch] = total;
     }
-    line = make_line(total, gridDim.x * NW);
-    v0 = blockIdx.x * NW;
+    line = make_line(total, gridDim.x * kWaves);
+    v0 = blockIdx.x * kWaves;
     if (v0 >= line.waves) return;
 #pragma unroll
-    for (int k = 0; k < NW; ++k) {
+    for (int k = 0; k < kWaves; ++k) {
       const uint32_t at = line.start(v0 + k);
       if (at >= before && at - before < mine) {
         found[0][k] = (uint32_t)my_b;
@@ -418,7 +448,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
     from_b = uniform(found[0][wave]);
     from_at = uniform(found[1][wave]);
   }
-  const uint32_t v = v0 + wave, live = min((uint32_t)NW, line.waves - v0);   // waves with a part of the line
+  const uint32_t v = v0 + wave, live = min((uint32_t)kWaves, line.waves - v0);   // waves with a part of the line
 
   f32x4 o[VJ];
   float ref = -INFINITY, l = 0.f;
@@ -449,7 +479,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
       }
     };
     auto load_q = [&]() {                            // heads past the tile's read as zeros
-      const rsrc_t r = make_rsrc(a.q + uniform(fetch.b) * a.ldq + (int64_t)uniform(fetch.h0) * D, (uint32_t)uniform(fetch.rows) * D * 2);
+      const uint16_t *at = a.q + uniform(fetch.b) * a.ldq + (int64_t)uniform(fetch.h0) * D;
+      const rsrc_t r = make_rsrc(at, (uint32_t)uniform(fetch.rows) * D * 2);
 #pragma unroll
       for (int i = 0; i < T::KD; ++i)
         q[i] = __builtin_bit_cast(half8_t, bldx4<0>(r, c * (2 * D) + 32 * g, 128 * (i >> 1) + 16 * (i & 1)));
@@ -561,8 +592,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < VJ; j += 4)
-              store_result<D>(a, cur.b, cur.h0, slot, c, VJ * (4 * g + i) + j, f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]}, ref,
-                              l);
+              store_result<D>(a, cur.b, cur.h0, slot, c, VJ * (4 * g + i) + j,
+                              f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]}, ref, l);
         }
         cur = fetch;
       }
@@ -614,7 +645,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
 // Joins the parts of the head tiles that several workgroups (or a wave that went on) hold. Workgroup
 // (sequence and head tile, y) takes the heads y, y + gridDim.y, ...: kSplit groups of threads run
 // through the parts, four elements of the output a thread and every load independent of the others,
-// each with its own maximum and sum, and then join these.
+// each with its own maximum and sum, and then join these. Latency-bound (4 to 7 us): the lengths,
+// then all parts at once; one element a thread instead of four took 1 to 3 us more.
 template <int D, int THREADS>
 __global__ __launch_bounds__(THREADS) void attn_join_kernel(AttnArgs a, uint32_t waves) {
   constexpr uint32_t kLanes = D / 4, kSplit = THREADS / kLanes;
@@ -717,7 +749,7 @@ int launch_attn(const AttnArgs &a, int64_t tiles, hipStream_t s) {
   if (int st = launch(attn_kernel<D, Q8, false>, dim3(grid), dim3(kThreads), kWaves * lds, s, a)) return st;
   // few head tiles: a workgroup for each head, the more threads for an element the more parts there are
   const uint32_t waves = (uint32_t)grid * kWaves;
-  const dim3 heads((unsigned)all, all < 256 ? (unsigned)a.rows : 1u);
+  const dim3 heads((unsigned)all, all * a.rows <= 2048 ? (unsigned)a.rows : 1u);
   if (grid / all >= 128) return launch(attn_join_kernel<D, 1024>, heads, dim3(1024), 0, s, a, waves);
   return launch(attn_join_kernel<D, 256>, heads, dim3(256), 0, s, a, waves);
 }
