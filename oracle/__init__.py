@@ -22,6 +22,8 @@ What it defines, following the two source pages:
     a stored permuted order, restored at inference), in ``actorder``;
   * the 8-bit KV-cache group codec ("二三五六位量化" section 4.1: one fp16 scale per 32
     elements, about 1.06 bytes per element), in ``kvcache``;
+  * the paged KV cache built on that codec (page records, append and gather, attention of one
+    token a sequence, page copy, fork, free and compaction), in ``paged``;
   * format variants: INT4 groups of 16/64/128, asymmetric INT4 with a zero point
     ("二三五六位量化" section 2.1) and INT4 with fp16 group scales (section 2.1) in ``int4``;
     super-block formats with bf16 super-scales (section 2.3) in ``superblock`` / ``bf16``.
