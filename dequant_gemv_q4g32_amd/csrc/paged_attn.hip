@@ -799,7 +799,7 @@ int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q,
   const int64_t pages = (max_len + pool->page_tokens - 1) / pool->page_tokens;
   if (int st = kv_table_check(table, ld_table, batch, pages)) return st;
   if (layer < 0 || layer >= pool->layers || window < 0 || (batch > 1 && (ldq < cols || ldo < cols))) return QG_ERR_SHAPE;
-  if (!std::isfinite(scale)) return QG_ERR_RANGE;
+  if (!std::isfinite(scale * kLog2e)) return QG_ERR_RANGE;   // scores are kept in units of log2
   if (batch == 0) return QG_OK;
   int64_t need = 0;
   if (int st = qg_paged_attention_bytes(pool, batch, heads, max_len, &need)) return st;

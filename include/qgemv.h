@@ -428,7 +428,8 @@ int qg_kv_gather(const qg_kv_pool *pool, int64_t layer, const int32_t *table, in
  *                                      when window is 0) that lie in a page of the pool,
  *   out[b][h] = sum_j e^(s_j) V[g][j] / sum_j e^(s_j),   lse[b][h] = ln sum_j e^(s_j).
  * A sequence without such a token gets out = 0 and lse = -inf; a head whose q holds a NaN or an
- * infinity gets NaN. q: fp16, row b at q + b * ldq,
+ * infinity gets NaN. What is cached for those tokens is finite, and so are their scores times
+ * log2(e) in fp32; what lies elsewhere in a page may be anything. q: fp16, row b at q + b * ldq,
  * heads dense; out: fp16, or fp32 with out_f32 != 0, row b at out + b * ldo, heads dense; lse:
  * fp32 [batch][heads], or NULL. The new token's own K and V are in the cache before the call
  * (qg_kv_append) and counted by lens. Products, the softmax and its sums are fp32; the weights
@@ -445,8 +446,9 @@ int qg_kv_gather(const qg_kv_pool *pool, int64_t layer, const int32_t *table, in
  * ceil(max_len / T) entries a row. q and out: 16-byte aligned, ldq a multiple of 8 (ldo of 8, of
  * 4 for fp32) and at least heads * head_dim when batch > 1. heads is a multiple of kv_heads;
  * batch * heads is at most 2^22, max_len at most 2^30, batch * heads * ceil(max_len / 32) below
- * 2^31, window >= 0, scale finite.
- * Errors: also QG_ERR_WORKSPACE, and QG_ERR_RANGE for a scale that is not finite. */
+ * 2^31, window >= 0, scale * log2(e) finite in fp32. out, lse and the workspace overlap nothing
+ * that the call reads: one workgroup's q may be loaded after another's out is stored.
+ * Errors: also QG_ERR_WORKSPACE, and QG_ERR_RANGE for any other scale. */
 int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_len, int64_t *bytes);
 int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q, int64_t ldq, const int32_t *table,
                        int64_t ld_table, const int32_t *lens, int64_t batch, int64_t heads, int64_t max_len,
@@ -463,8 +465,8 @@ int qg_kv_copy_pages(const qg_kv_pool *pool, const int32_t *src, const int32_t *
  * tokens. Its whole pages are shared (refs + 1 each); a last page that is only partly filled is
  * copied in every layer to page new_pages[i], whose refs become 1, so that the two rows grow
  * apart. Further entries of the row become -1 and lens[dst] = lens[src]. What the row held
- * before is overwritten, not released (qg_kv_free releases it). new_pages[i] is read only when
- * a last page is copied. A fork is skipped, its row left as it was, when a row is outside the
+ * before is overwritten, not released (qg_kv_free releases it). new_pages[i] is a free page, read
+ * only when a last page is copied; one that some row holds would be overwritten. A fork is skipped, its row left as it was, when a row is outside the
  * table, when dst_rows[i] is also a source row or an earlier destination row of the call, or
  * when a copy is needed and new_pages[i] is outside the pool or named earlier in the call.
  * count is at most 4096. */

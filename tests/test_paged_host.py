@@ -139,3 +139,9 @@ def test_entry_point_nothing_to_do(call, kw):
 
 def test_workspace_status_text():
     assert qg.lib.qg_strerror(-9) != b"unknown status"
+
+
+@pytest.mark.parametrize("scale", [3.0e38, -3.0e38])
+def test_entry_point_attention_scale_past_fp32(scale):
+    """scale * log2(e) has to be a number: 2.4e38 is the largest scale."""
+    assert attn(pool(), scale=scale) == RANGE
