@@ -393,8 +393,8 @@ __device__ __forceinline__ void store_result(const AttnArgs &a, int32_t b, int32
   if (d == 0 && a.lse) a.lse[(int64_t)b * a.heads + h] = (m + __log2f(l)) * kLn2;
 }
 
-// WHOLE: workgroup (sequence, head tile) takes that head tile, its waves a share each, and there is
-// nothing to join afterwards. Else the workgroups' waves take the parts of the line.
+// WHOLE: workgroup (sequence, head tile) of one to four waves takes that head tile, its waves a share
+// each, and there is nothing to join afterwards. Else the workgroups' waves take the parts of the line.
 template <int D, bool Q8, bool WHOLE>
 __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn_kernel(AttnArgs a) {
   using T = Tile<D, Q8>;
@@ -414,7 +414,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
     from_b = blockIdx.x / a.head_tiles;
     from_at = 0;
     const uint32_t tiles = seen_of<true>(a, scalar_load(a.lens + from_b)).units;
-    line = make_line(tiles, kWaves);
+    line = make_line(tiles, blockDim.x / 64);
     line.first = (blockIdx.x - from_b * a.head_tiles) * tiles;
     v0 = 0;
   } else {
@@ -719,22 +719,38 @@ int64_t attn_tiles(int64_t max_len, int64_t window) {
   return tiles > 1 ? tiles : 1;
 }
 
-// Workgroups: as many as are resident at once (heads of 64: four a CU, of 128: two), or as there are
-// tiles for. Heads of 256 would fit two as well, but their parts are 16 KB for 16 heads: one a CU
-// writes and joins half as many.
+// Workgroups of four waves that are resident at once (heads of 64: four a CU, of 128: two). Heads of
+// 256 would fit two as well, but their parts are 16 KB for 16 heads: one a CU writes and joins half
+// as many.
+int64_t attn_resident(int64_t dim) { return dim == 64 ? 1024 : dim == 128 ? 512 : 256; }
+
+// Workgroups of the split: those resident, or as many as there are tiles for.
 int32_t attn_grid(int64_t batch, int64_t head_tiles, int64_t tiles, int64_t dim) {
-  const int64_t all = (batch * head_tiles * tiles + kWaves - 1) / kWaves, most = dim == 64 ? 1024 : dim == 128 ? 512 : 256;
+  const int64_t all = (batch * head_tiles * tiles + kWaves - 1) / kWaves, most = attn_resident(dim);
   return (int32_t)(all < most ? all : most);
 }
 
 // A workgroup for each head tile instead of the split, where that is the shorter way: the split
 // evens out the work but costs a second launch (about 5 us with its wait), a head tile of n tiles
-// keeps one workgroup busy for n / 4 steps. Split against whole, int8, 32 heads on 8 of 128, us:
+// keeps one workgroup busy for n / 4 steps. Split against whole, 32 heads on 8 of 128, int8, us:
 // 1 sequence of 500 tokens 10.6 : 9.8, of 1000 10.9 : 14.6; 16 of 1000 17.6 : 15.2; 64 of up to
-// 2000 38.7 : 34.8; 32 of up to 4096 (fp16) 42.6 : 53.2.
-bool attn_whole(int64_t head_tiles, int64_t tiles) {
-  const int64_t most = head_tiles / 4;
+// 2000 38.7 : 34.8; 32 of up to 4096 (fp16) 42.6 : 53.2. Heads of 256, 4 KV heads, 130 sequences: of
+// 500 tokens 42.5 : 46, of up to 500 30.1 : 26.8, of 1000 68 : 76, of up to 1000 39.6 : 40.4.
+bool attn_whole(int64_t head_tiles, int64_t tiles, int64_t dim) {
+  const int64_t most = dim == 256 ? 16 : head_tiles / 4;
   return tiles <= (most < 16 ? 16 : most < 64 ? most : 64);
+}
+
+// Waves of such a workgroup: fewer where more short head tiles wait than fit at once, so that more
+// of them share the latency of a start (two or three dependent loads) and the LDS holds fewer sums. Four
+// waves against these, int8, us: 4 heads of 256 and 130 sequences of 100 tokens 25.9 : 16.6 (one
+// wave), 80 of 500 30.4 : 24.3 (two); 8 heads of 128 and 512 of up to 120 tokens 32.4 : 22.2 (one),
+// 128 of them 13.1 : 10.2 (two), 64 of 500, which all fit, 16.9 : 19.7 with two. Long ones keep the
+// card full with four: fp16, 512 sequences of 1000 tokens on 4 heads of 128 173 : 188 with two.
+int whole_waves(int64_t head_tiles, int64_t tiles, int64_t dim) {
+  const int64_t resident = attn_resident(dim);
+  if (head_tiles <= resident || tiles > 16) return kWaves;
+  return head_tiles >= 4 * resident || (head_tiles > 2 * resident && tiles <= 8) ? 1 : 2;
 }
 
 int64_t starts_bytes(int64_t batch) { return (4 * (batch + 1) + 15) / 16 * 16; }
@@ -743,8 +759,10 @@ template <int D, bool Q8>
 int launch_attn(const AttnArgs &a, int64_t tiles, hipStream_t s) {
   const size_t lds = sizeof(float) * a.rows * (D + 4);
   const int64_t all = (int64_t)a.batch * a.head_tiles;
-  if (attn_whole(all, tiles))
-    return launch(attn_kernel<D, Q8, true>, dim3((unsigned)all), dim3(kThreads), kWaves * lds, s, a);
+  if (attn_whole(all, tiles, D)) {
+    const int waves = whole_waves(all, tiles, D);
+    return launch(attn_kernel<D, Q8, true>, dim3((unsigned)all), dim3(64 * waves), waves * lds, s, a);
+  }
   const int32_t grid = attn_grid(a.batch, a.head_tiles, tiles, D);
   if (int st = launch(attn_kernel<D, Q8, false>, dim3(grid), dim3(kThreads), kWaves * lds, s, a)) return st;
   // few head tiles: a workgroup for each head, the more threads for an element the more parts there are
@@ -783,7 +801,7 @@ int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t head
   const int64_t head_tiles = (group + 15) / 16 * pool->kv_heads, tiles = attn_tiles(max_len, 0);
   // a window only shortens the head tiles: what needs no join without one needs none with one
   *bytes = 0;
-  if (batch == 0 || attn_whole(batch * head_tiles, tiles)) return QG_OK;
+  if (batch == 0 || attn_whole(batch * head_tiles, tiles, pool->head_dim)) return QG_OK;
   const int64_t slots = 2 * kWaves * attn_grid(batch, head_tiles, tiles, pool->head_dim);
   *bytes = starts_bytes(batch) + 4 * slots * slot_floats((int32_t)rows, pool->head_dim);
   return QG_OK;

@@ -199,6 +199,24 @@ def test_split_over_many_sequences(seed, batch, kv_heads, group, dim, most):
     check_attention(out, lse, _torch_reference(*values, table, lens.tolist(), q, dim ** -0.5, window), most, dim)
 
 
+@pytest.mark.parametrize("kind,batch,kv_heads,group,dim,most,window", [
+    ("q8", 300, 2, 4, 128, 130, 0), ("f16", 530, 2, 3, 128, 250, 0), ("q8", 530, 2, 5, 128, 500, 77), ("q8", 260, 1, 16, 256, 500, 0),
+    ("f16", 520, 1, 20, 256, 60, 0), ("q8", 520, 2, 1, 64, 100, 0), ("f16", 1100, 4, 2, 64, 40, 9), ("q8", 2100, 1, 3, 128, 1, 0),
+    ("f16", 700, 1, 1, 256, 512, 0), ("q8", 1100, 1, 16, 256, 300, 0)])
+def test_many_short_sequences(kind, batch, kv_heads, group, dim, most, window):
+    """More short sequences than there are workgroups at once, each head tile with one or two waves."""
+    rng = np.random.default_rng(batch + dim)
+    tokens = int(rng.choice([16, 32, 64]))
+    pool, values, gen = _filled(kind, kv_heads, dim, tokens, 300, batch)
+    lens = rng.integers(0, most + 1, batch) * (rng.random(batch) < 0.9)
+    lens[-1] = most
+    table = dev(rng.integers(0, 300, (batch, -(-most // tokens))))
+    q = (torch.randn((batch, group * kv_heads, dim), generator=gen, device="cuda") * 1.5).half()
+    assert qg.paged_attention_bytes(pool, batch, group * kv_heads, most) == 0
+    out, lse = qg.paged_attention(pool, q, table, dev(lens), max_len=most, window=window, out_f32=True, return_lse=True)
+    check_attention(out, lse, _torch_reference(*values, table, lens.tolist(), q, dim ** -0.5, window), most, dim)
+
+
 # ---- graphs ------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("kind,max_len", [("q8", 256), ("f16", 8192)])
