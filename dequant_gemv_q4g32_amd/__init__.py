@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import re
 import sys
@@ -347,6 +348,12 @@ def kv_page_bytes(kind: str, kv_heads: int, head_dim: int, page_tokens: int) -> 
     return out.value
 
 
+def _workspace(what: str, c: _Pool, *sizes) -> int:
+    out = ctypes.c_int64()
+    _check(getattr(_lib, what)(ctypes.addressof(c), *sizes, ctypes.byref(out)), what)
+    return out.value
+
+
 class KVPool:
     """A pool of cache pages: uint8 [num_pages, page_bytes], or [layers, num_pages, page_bytes] for
     several layers that share one page table. kind "q8": int8 groups of 32 with fp16 scales (the
@@ -370,6 +377,9 @@ class KVPool:
         self._c = _Pool(pages.data_ptr(), self.num_pages, self.layers, pages.stride(0) if self.layers > 1 else 0,
                         KV_KINDS[kind], kv_heads, head_dim, page_tokens)
         self._ref = ctypes.addressof(self._c)
+        # workspace sizes, kept by the sizes they follow from: asking the library takes 1 us of a call's 15
+        self._attention_bytes = functools.lru_cache(256)(functools.partial(_workspace, "qg_paged_attention_bytes", self._c))
+        self._compact_bytes = functools.lru_cache(1)(functools.partial(_workspace, "qg_kv_compact_bytes", self._c))
 
     @classmethod
     def zeros(cls, kind: str, kv_heads: int, head_dim: int, page_tokens: int, num_pages: int, layers: int = 1,
@@ -458,9 +468,7 @@ def kv_gather(pool, table, positions, seqs=None, k=None, v=None, layer: int = 0,
 
 def paged_attention_bytes(pool, batch: int, heads: int, max_len: int) -> int:
     """Workspace bytes of paged_attention for these sizes (0: it needs none)."""
-    out = ctypes.c_int64()
-    _check(_lib.qg_paged_attention_bytes(pool._ref, batch, heads, max_len, ctypes.byref(out)), "qg_paged_attention_bytes")
-    return out.value
+    return pool._attention_bytes(batch, heads, max_len)
 
 
 def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: Optional[float] = None, window: int = 0,
@@ -500,7 +508,7 @@ def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: 
     elif return_lse:
         lse = q.new_empty((batch, heads), dtype=_th.float32)
     if workspace is None:
-        need = paged_attention_bytes(pool, batch, heads, max_len)
+        need = pool._attention_bytes(batch, heads, max_len)
         workspace = q.new_empty(need, dtype=_th.uint8) if need else None
     elif workspace.dtype != _th.uint8 or workspace.device != pool.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be dense uint8 on {pool.device}")
@@ -552,26 +560,30 @@ def kv_compact(pool, table, refs, table_out=None, refs_out=None, remap=None, liv
     """Move the held pages of the pool to its first pages, in every layer. Returns (table_out,
     refs_out, remap, live): the table and the counts for the moved pages (pass table and refs
     themselves to update them in place), each page's new index (-1: free), and the number of
-    held pages (int32 [1] on the device)."""
+    held pages (int32 [1] on the device). What is not given is allocated, the last three as views of
+    one buffer when none of them is."""
     if stream is not None or _device_now() != pool._index:
         with _on(pool, stream):
             return kv_compact(pool, table, refs, table_out, refs_out, remap, live)
     at, ld, rows, pages = _table(pool, table)
-    need = ctypes.c_int64()
-    _check(_lib.qg_kv_compact_bytes(pool._ref, ctypes.byref(need)), "qg_kv_compact_bytes")
+    need = pool._compact_bytes()
 
     table_out = table.new_empty((rows, pages)) if table_out is None else table_out
-    refs_out = refs.new_empty(pool.num_pages) if refs_out is None else refs_out
-    remap = refs.new_empty(pool.num_pages) if remap is None else remap
-    live = refs.new_empty(1) if live is None else live
+    n = pool.num_pages
+    if refs_out is None and remap is None and live is None:      # one allocation for what is counted in pages
+        refs_out, remap, live, workspace = refs.new_empty(2 * n + 1 + need // 4).split_with_sizes((n, n, 1, need // 4))
+    else:
+        refs_out = refs.new_empty(n) if refs_out is None else refs_out
+        remap = refs.new_empty(n) if remap is None else remap
+        live = refs.new_empty(1) if live is None else live
+        workspace = refs.new_empty(need // 4)
     to = _table(pool, table_out)
     if to[2:] != (rows, pages):
         raise ValueError("table_out must have table's shape")
-    workspace = refs.new_empty(need.value // 4)
     _check(_lib.qg_kv_compact(pool._ref, at, ld, to[0], to[1], rows, pages, _ints(pool, "refs", refs, pool.num_pages),
                               _ints(pool, "refs_out", refs_out, pool.num_pages),
                               _ints(pool, "remap", remap, pool.num_pages), _ints(pool, "live", live, 1),
-                              workspace.data_ptr(), need.value, _stream_now(pool._index)), "qg_kv_compact")
+                              workspace.data_ptr(), need, _stream_now(pool._index)), "qg_kv_compact")
     return table_out, refs_out, remap, live
 
 
