@@ -261,7 +261,7 @@ __device__ __forceinline__ f32x4 scores(const Tile<D, Q8> &t, int st, const half
 
 // Whether the lane's part of q holds a NaN or an infinity. FP16_OVFL makes the matrix units take
 // either as a finite number, so with int8 pages such a head is marked instead: its scores are
-// infinite or NaN against any finite K, and its softmax is NaN.
+// infinite or NaN against any finite K, and its softmax is NaN as soon as it sees a token.
 template <int KD>
 __device__ __forceinline__ bool nonfinite(const half8_t *q) {
   uint32_t bad = 0;
@@ -503,7 +503,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
       ref = -INFINITY;
       l = 0.f;
       bool inside = true;                            // the tile in t is of segment cur
-      bool fresh = true;                             // and its first
+      bool fresh = true, bad = false;                // and its first; the lane's part of q is not finite
       while (inside) {
         const int32_t t0 = token(0);
         const bool full = t0 >= cur.first && t0 + kTile <= cur.len && page[0] >= 0 && page[1] >= 0;
@@ -528,7 +528,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
 #pragma unroll
         for (int st = 0; st < 2; ++st) x[st] = scores<D, Q8>(t, st, q);
         if (Q8 && fresh) {
-          if (nonfinite<T::KD>(q)) l = __builtin_nanf("");
+          bad = nonfinite<T::KD>(q);
           fresh = false;
         }
         locate();
@@ -582,6 +582,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
         accumulate<D, Q8>(t, hi, lo, o);
         load_v<D, Q8>(a, blk, vs_lane, t);
       }
+      if (Q8 && bad && ref > -INFINITY) l = __builtin_nanf("");   // ref: moved by the first token that is seen
       l += __shfl_xor(l, 16);
       l += __shfl_xor(l, 32);
       if (more) {

@@ -427,8 +427,8 @@ int qg_kv_gather(const qg_kv_pool *pool, int64_t layer, const int32_t *table, in
  *   s_j = scale * <q[b][h], K[g][j]>   for the tokens max(0, n - window) <= j < n (all j < n
  *                                      when window is 0) that lie in a page of the pool,
  *   out[b][h] = sum_j e^(s_j) V[g][j] / sum_j e^(s_j),   lse[b][h] = ln sum_j e^(s_j).
- * A sequence without such a token gets out = 0 and lse = -inf; a head whose q holds a NaN or an
- * infinity gets NaN. What is cached for those tokens is finite, and so are their scores times
+ * A sequence without such a token gets out = 0 and lse = -inf whatever its q holds; else a head
+ * whose q holds a NaN or an infinity gets NaN. What is cached for those tokens is finite, and so are their scores times
  * log2(e) in fp32; what lies elsewhere in a page may be anything. q: fp16, row b at q + b * ldq,
  * heads dense; out: fp16, or fp32 with out_f32 != 0, row b at out + b * ldo, heads dense; lse:
  * fp32 [batch][heads], or NULL. The new token's own K and V are in the cache before the call

@@ -175,6 +175,30 @@ def test_infinite_and_nan_entries_stay_in_their_head(kind):
     assert not torch.any(torch.isfinite(out[0, 3]))
 
 
+@pytest.mark.parametrize("kind", ["q8", "f16"])
+@pytest.mark.parametrize("max_len", [64, 40000])
+def test_rows_without_tokens_ignore_q(kind, max_len):
+    """A padded batch's empty rows may hold anything in q: no token, so zeros and -inf. The same for
+    a row whose pages are all missing, and a first page missing does not hide a NaN."""
+    lens = [0, 40, 40, -3, 40, 64]
+    rng, c, table, q = _problem(kind, 8, 2, 64, 16, lens, 13)
+    wide = np.full((len(lens), max(max_len // 16, table.shape[1])), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    wide[2] = -1
+    wide[5, :2] = -1
+    q[0] = np.nan
+    q[2] = np.inf
+    q[3, :, 1::2] = -np.inf
+    q[5, 6, 40] = np.nan
+    out, lse = qg.paged_attention(upload(c), dev(q, np.float16), dev(wide), dev(lens), max_len=max_len, return_lse=True)
+    for b in (0, 2, 3):
+        assert torch.all(out[b] == 0) and torch.all(lse[b] == -float("inf")), b
+    keep = torch.ones((len(lens), 8), dtype=torch.bool)
+    keep[5, 6] = False
+    assert torch.all(torch.isnan(out[5, 6])) and torch.isnan(lse[5, 6])
+    assert torch.all(torch.isfinite(out.cpu()[keep]))
+
+
 def _reference(pool_values, table, lens, q, scale):
     """fp64 torch reference on the GPU for long caches: pool_values (K, V) fp16 [pages, heads, T, D]."""
     batch, heads, dim = q.shape
