@@ -129,18 +129,24 @@ __device__ __forceinline__ Line make_line(uint32_t total, uint32_t waves) {
   return l;
 }
 
+// Sum of `v` over this lane and those before it: within rows of 16, then over the rows.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false);   // row_shr:1
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false);   // row_shr:2
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false);   // row_shr:4
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false);   // row_shr:8
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);   // row_bcast:15
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);   // row_bcast:31
+  return v;
+}
+
 // Sum of `v` over the threads before this one; total: over all. lds: a value for each wave.
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *lds, uint32_t &total) {
-  uint32_t scan = v;
-  const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint32_t up = __shfl_up(scan, o);
-    scan += lane >= o ? up : 0;
-  }
-  if (lane == 63) lds[threadIdx.x >> 6] = scan;
+  const uint32_t scan = wave_scan(v);
+  if ((threadIdx.x & 63) == 63) lds[threadIdx.x >> 6] = scan;
   __syncthreads();
   uint32_t before = 0, all = 0;
-  for (int w = 0; w < waves; ++w) {
+  for (int w = 0; w < kWaves; ++w) {
     const uint32_t t = lds[w];
     before += w < (int)(threadIdx.x >> 6) ? t : 0;
     all += t;
@@ -340,11 +346,13 @@ struct Segment {
   const int32_t *row;        // the sequence's row of the table
 };
 
-// The segment at unit `at` < end of the line, at or after sequence b, which starts at seq_at.
+// The segment at unit `at` < end of the line, at or after sequence b of `len` tokens, which starts
+// at seq_at.
 template <bool WHOLE>
-__device__ __forceinline__ Segment segment_at(const AttnArgs &a, uint32_t at, uint32_t end, int32_t b, uint32_t seq_at) {
+__device__ __forceinline__ Segment segment_at(const AttnArgs &a, uint32_t at, uint32_t end, int32_t b, uint32_t seq_at,
+                                              int32_t len) {
   Segment g;
-  Seen s = seen_of<WHOLE>(a, scalar_load(a.lens + b));
+  Seen s = seen_of<WHOLE>(a, len);
   while (at - seq_at >= s.units * a.head_tiles) {
     seq_at += s.units * a.head_tiles;
     ++b;
@@ -401,29 +409,45 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
   constexpr int VJ = T::VJ;
   constexpr int kPad = D + 4;                        // LDS rows of neighbouring heads start in other banks
   extern __shared__ float sums[];                    // [kWaves][rows][kPad], rows = heads of a tile
-  __shared__ uint32_t scan[kWaves], found[2][kWaves];
-  __shared__ float wave_m[kWaves][16], wave_l[kWaves][16];
+  __shared__ uint32_t scan[kWaves], found[3][kWaves];
+  __shared__ float wave_m[kWaves][16], wave_l[kWaves][16], run_m[kWaves][16];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
   if constexpr (Q8) __builtin_amdgcn_s_setreg(1 | (23 << 6) | (0 << 11), 1);   // hwreg(MODE, 23, 1): FP16_OVFL
   const uint32_t vs_lane = 2 * ((((VJ * (uint32_t)c) / 32) << a.tok_shift) + 4 * g);   // the lane's V scales
 
   // this workgroup's waves on the line
   Line line;
-  uint32_t v0, from_b, from_at;                      // first wave; a sequence at or before this wave's part, and its start
+  uint32_t v0, from_b, from_at;                      // first wave; a sequence at or before this wave's part, its start
+  int32_t from_len;                                  // and its length
   if constexpr (WHOLE) {
     from_b = blockIdx.x / a.head_tiles;
-    from_at = 0;
-    const uint32_t tiles = seen_of<true>(a, scalar_load(a.lens + from_b)).units;
+    from_len = scalar_load(a.lens + from_b);
+    const uint32_t tiles = seen_of<true>(a, from_len).units;
     line = make_line(tiles, blockDim.x / 64);
     line.first = (blockIdx.x - from_b * a.head_tiles) * tiles;
+    from_at = 0;
     v0 = 0;
   } else {
-    const int32_t per = (a.batch + kThreads - 1) / kThreads, my_b = (int32_t)threadIdx.x * per;
+    // Every wave for itself where the batch fits its lanes (no LDS and no barrier in the way of the
+    // first loads), else a share of the batch for each thread of the workgroup.
+    const bool one = a.batch <= 64;
+    const int32_t per = one ? 1 : (a.batch + kThreads - 1) / kThreads, my_b = (one ? lane : (int32_t)threadIdx.x) * per;
     uint32_t mine = 0;
+    int32_t my_len = 0;                              // of sequence my_b
     for (int32_t i = 0; i < per; ++i)
-      if (my_b + i < a.batch) mine += seen_of<false>(a, a.lens[my_b + i]).units * a.head_tiles;
-    uint32_t total;
-    const uint32_t before = block_scan(mine, scan, total);
+      if (my_b + i < a.batch) {
+        const int32_t len = a.lens[my_b + i];
+        if (i == 0) my_len = len;
+        mine += seen_of<false>(a, len).units * a.head_tiles;
+      }
+    uint32_t total, before;
+    if (one) {
+      const uint32_t scan = wave_scan(mine);
+      before = scan - mine;
+      total = __builtin_amdgcn_readlane(scan, 63);
+    } else {
+      before = block_scan(mine, scan, total);
+    }
     if (blockIdx.x == 0) {                           // for the join
       uint32_t at = before;
       for (int32_t i = 0; i < per; ++i)
@@ -436,17 +460,28 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
     line = make_line(total, gridDim.x * kWaves);
     v0 = blockIdx.x * kWaves;
     if (v0 >= line.waves) return;
+    if (one) {
+      const uint32_t at = line.start(v0 + wave);
+      const uint64_t here = __ballot(at >= before && at - before < mine);
+      const int32_t i = here ? __builtin_ctzll(here) : 0;    // none: a wave without a part
+      from_b = i;
+      from_at = __builtin_amdgcn_readlane(before, i);
+      from_len = __builtin_amdgcn_readlane(my_len, i);
+    } else {
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) {
-      const uint32_t at = line.start(v0 + k);
-      if (at >= before && at - before < mine) {
-        found[0][k] = (uint32_t)my_b;
-        found[1][k] = before;
+      for (int k = 0; k < kWaves; ++k) {
+        const uint32_t at = line.start(v0 + k);
+        if (at >= before && at - before < mine) {
+          found[0][k] = (uint32_t)my_b;
+          found[1][k] = before;
+          found[2][k] = (uint32_t)my_len;
+        }
       }
+      __syncthreads();
+      from_b = uniform(found[0][wave]);
+      from_at = uniform(found[1][wave]);
+      from_len = (int32_t)uniform(found[2][wave]);
     }
-    __syncthreads();
-    from_b = uniform(found[0][wave]);
-    from_at = uniform(found[1][wave]);
   }
   const uint32_t v = v0 + wave, live = min((uint32_t)kWaves, line.waves - v0);   // waves with a part of the line
 
@@ -459,7 +494,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
     half8_t q[T::KD];
     Block blk[2];
     int32_t page[2];                                 // of the tile in t; below 0: none
-    cur = segment_at<WHOLE>(a, line.start(v), end, (int32_t)from_b, from_at);
+    cur = segment_at<WHOLE>(a, line.start(v), end, (int32_t)from_b, from_at, from_len);
     Segment fetch = cur;                             // the segment of the tile in t, fetch.at that tile
     auto token = [&](int st) { return fetch.base + (int32_t)(fetch.at - fetch.tile0) * kTile + 16 * st; };
     auto look_up = [&]() {
@@ -521,7 +556,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
         more = fetch.at + 1 < end;
         if (++fetch.at == fetch.end) {
           inside = false;
-          if (more) fetch = segment_at<WHOLE>(a, fetch.at, end, fetch.b, fetch.u0 - (fetch.u1 - fetch.u0) * fetch.ht);
+          if (more) fetch = segment_at<WHOLE>(a, fetch.at, end, fetch.b, fetch.u0 - (fetch.u1 - fetch.u0) * fetch.ht, fetch.len);
         }
         look_up();
         f32x4 x[2];
@@ -602,10 +637,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
   }
 
   // the waves that ended on one head tile join their parts; the leader stores the sum
-  if ((uint32_t)wave < live && g == 0) {
-    wave_m[wave][c] = ref;
-    wave_l[wave][c] = l;
-  }
+  if ((uint32_t)wave < live && g == 0) wave_m[wave][c] = ref;
   __syncthreads();
   uint32_t lead = 0, tail = 0;                       // first and last wave that end on this wave's head tile
   if ((uint32_t)wave < live) {
@@ -615,6 +647,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
     float m = ref;
     for (uint32_t k = lead; k <= tail; ++k) m = fmaxf(m, wave_m[k][c]);
     const float f = ref == m ? 1.0f : __builtin_amdgcn_exp2f(ref - m);
+    if (g == 0) {
+      wave_l[wave][c] = l * f;
+      run_m[wave][c] = m;
+    }
     if (c < cur.rows) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -631,15 +667,13 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
                                                                                     : slot_of(a, 2 * (v0 + lead) + 1, D);
   for (int i = 4 * (64 * (wave - (int)lead) + lane); i < cur.rows * D; i += 256 * (int)(tail - lead + 1)) {
     const int r = i / D, d = i & (D - 1);
-    float m = wave_m[lead][r];
-    for (uint32_t k = lead + 1; k <= tail; ++k) m = fmaxf(m, wave_m[k][r]);
     f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
     float den = 0.f;
     for (uint32_t k = lead; k <= tail; ++k) {
       sum += *reinterpret_cast<const f32x4 *>(sums + (k * a.rows + r) * kPad + d);
-      den += wave_l[k][r] * (wave_m[k][r] == m ? 1.0f : __builtin_amdgcn_exp2f(wave_m[k][r] - m));
+      den += wave_l[k][r];
     }
-    store_result<D>(a, cur.b, cur.h0, slot, r, d, sum, m, den);
+    store_result<D>(a, cur.b, cur.h0, slot, r, d, sum, run_m[wave][r], den);
   }
 }
 
