@@ -18,9 +18,9 @@
 // 380 vector and 130 scalar instructions a step of 8.7 KB; a wave alone needs 1.3 us for it). The
 // next step's K is on its way while the softmax and the products with V run, its V from then on.
 // Measured (GPU time; a plain stream of reads reaches 6.8 TB/s here): 64 sequences of 8192 tokens,
-// 64 heads on 8 of 128: fp16 322 us = 6.7 TB/s, int8 187 us = 6.1 TB/s; one of 131072 tokens, int8,
-// 55 us = 5.2 TB/s; 32 of up to 8192, int8, 47 us = 4.9 TB/s; 48 of up to 6007 with one KV head of
-// 256, int8, 28 us; one of 1000 tokens 10 us, of 100 tokens 6 us (a launch and four dependent
+// 64 heads on 8 of 128: fp16 319 us = 6.7 TB/s, int8 186 us = 6.1 TB/s; one of 131072 tokens, int8,
+// 54 us = 5.3 TB/s; 32 of up to 8192, int8, 47 us = 4.9 TB/s; 48 of up to 6007 with one KV head of
+// 256, int8, 28 us; one of 1000 tokens 9.5 us, of 100 tokens 6 us (a launch and four dependent
 // memory latencies: length, page, K, and the first step). HBM reads are the algorithm's bytes.
 #include <hip/hip_runtime.h>
 
