@@ -6,8 +6,8 @@
 // per head, a wave keeps o = sum 2^(s_j - ref) V_j and l = sum 2^(s_j - ref); moving ref scales both
 // by 2^(old - new), and two such results join by scaling to the larger ref.
 //
-// Work of a wave: up to 16 heads of one KV head (a head tile) against 32 tokens a step, two blocks
-// of 16. S^T = K Q^T and O^T += V^T P^T run on v_mfma_f32_16x16x32_f16 with fp32 sums. S^T's lanes
+// Work of a wave: up to 16 or 32 heads of one KV head (a head tile) against 32 tokens a step, two
+// blocks of 16. S^T = K Q^T and O^T += V^T P^T run on v_mfma_f32_16x16x32_f16 with fp32 sums. S^T's lanes
 // hold one head and four tokens each, which is the layout the weights P^T need as the next
 // product's operand, so the softmax never leaves the registers: no shuffle but the largest score's,
 // and that only when ref moves. int8 K and V are decoded to fp16 in registers; the row-major V is
@@ -44,7 +44,8 @@ struct AttnArgs {
   int64_t ld_table;
   const int32_t *lens;
   int32_t batch, heads, group;   // group = heads / kv_heads
-  int32_t tiles_per_kv, head_tiles;   // 16-head tiles of a KV head, and of all of them
+  int32_t tile_heads;            // heads of a head tile: 16, or 32 where a KV head has more than 16
+  int32_t tiles_per_kv, head_tiles;   // head tiles of a KV head, and of all of them
   int32_t rows;                  // heads of a tile that a partial result has room for
   int32_t max_len, window;
   float scale_log2;              // scale * log2(e)
@@ -238,10 +239,11 @@ __device__ __forceinline__ void load_v(const AttnArgs &a, const Block *blk, uint
   }
 }
 
-// Scores of a block: S^T [16 tokens x 16 heads] = K Q^T. Lane: head c, tokens 4 g + i.
-template <int D, bool Q8>
-__device__ __forceinline__ f32x4 scores(const Tile<D, Q8> &t, int st, const half8_t *q) {
-  f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+// Scores of a block against each 16 heads: S^T [16 tokens x 16 heads] = K Q^T. Lane: head c, tokens 4 g + i.
+template <int D, bool Q8, int HT>
+__device__ __forceinline__ void scores(const Tile<D, Q8> &t, int st, const half8_t (*q)[D / 32], f32x4 *s) {
+#pragma unroll
+  for (int u = 0; u < HT; ++u) s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
   if constexpr (Q8) {
     const uint32_t pick = (threadIdx.x & 32) ? 0x03020302u : 0x01000100u;   // the group of the lane's 16 elements
 #pragma unroll
@@ -254,15 +256,19 @@ __device__ __forceinline__ f32x4 scores(const Tile<D, Q8> &t, int st, const half
         w[j >> 1][2 * (j & 1)] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, x, kSelLow), d);
         w[j >> 1][2 * (j & 1) + 1] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, x, kSelHigh), d);
       }
-      s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w[0]), q[2 * i], s, 0, 0, 0);
-      s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w[1]), q[2 * i + 1], s, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < HT; ++u) {
+        s[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w[0]), q[u][2 * i], s[u], 0, 0, 0);
+        s[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w[1]), q[u][2 * i + 1], s[u], 0, 0, 0);
+      }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
-      s = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, t.k[st][i]), q[i], s, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < HT; ++u)
+        s[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, t.k[st][i]), q[u][i], s[u], 0, 0, 0);
   }
-  return s;
 }
 
 // Whether the lane's part of q holds a NaN or an infinity. FP16_OVFL makes the matrix units take
@@ -282,8 +288,8 @@ __device__ __forceinline__ bool nonfinite(const half8_t *q) {
 
 // O^T += V^T P^T with the weights as hi + lo fp16 pairs. Column c of V^T's block j is element
 // VJ * c + j, so O^T's lane holds head c and elements VJ * (4 g + i) + j.
-template <int D, bool Q8>
-__device__ __forceinline__ void accumulate(const Tile<D, Q8> &t, half8_t hi, half8_t lo, f32x4 *o) {
+template <int D, bool Q8, int HT>
+__device__ __forceinline__ void accumulate(const Tile<D, Q8> &t, const half8_t *hi, const half8_t *lo, f32x4 (*o)[D / 16]) {
   constexpr int VW = Tile<D, Q8>::VW;
 #pragma unroll
   for (int w = 0; w < VW; ++w) {
@@ -301,11 +307,14 @@ __device__ __forceinline__ void accumulate(const Tile<D, Q8> &t, half8_t hi, hal
         e[3][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, b, kSelHigh), d);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o[4 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), hi, o[4 * w + j], 0, 0, 0);
+      for (int u = 0; u < HT; ++u) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        o[4 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), lo, o[4 * w + j], 0, 0, 0);
+        for (int j = 0; j < 4; ++j)
+          o[u][4 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), hi[u], o[u][4 * w + j], 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[u][4 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), lo[u], o[u][4 * w + j], 0, 0, 0);
+      }
     } else {
       u32x4 e[2];
 #pragma unroll
@@ -314,11 +323,14 @@ __device__ __forceinline__ void accumulate(const Tile<D, Q8> &t, half8_t hi, hal
         e[1][p] = __builtin_amdgcn_perm(t.v[2 * p + 1][w], t.v[2 * p][w], 0x07060302u);
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        o[2 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), hi, o[2 * w + j], 0, 0, 0);
+      for (int u = 0; u < HT; ++u) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        o[2 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), lo, o[2 * w + j], 0, 0, 0);
+        for (int j = 0; j < 2; ++j)
+          o[u][2 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), hi[u], o[u][2 * w + j], 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          o[u][2 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), lo[u], o[u][2 * w + j], 0, 0, 0);
+      }
     }
   }
 }
@@ -369,9 +381,9 @@ __device__ __forceinline__ Segment segment_at(const AttnArgs &a, uint32_t at, ui
   g.first = s.first;
   g.len = s.len;
   g.base = s.base;
-  const int32_t kvh = g.ht / a.tiles_per_kv, first_head = (g.ht - kvh * a.tiles_per_kv) * 16;
+  const int32_t kvh = g.ht / a.tiles_per_kv, first_head = (g.ht - kvh * a.tiles_per_kv) * a.tile_heads;
   g.h0 = kvh * a.group + first_head;
-  g.rows = min(16, a.group - first_head);
+  g.rows = min(a.tile_heads, a.group - first_head);
   g.kv = a.pool + kvh * a.head_bytes;
   g.row = a.table + b * a.ld_table;
   return g;
@@ -403,14 +415,14 @@ __device__ __forceinline__ void store_result(const AttnArgs &a, int32_t b, int32
 
 // WHOLE: workgroup (sequence, head tile) of one to four waves takes that head tile, its waves a share
 // each, and there is nothing to join afterwards. Else the workgroups' waves take the parts of the line.
-template <int D, bool Q8, bool WHOLE>
-__global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn_kernel(AttnArgs a) {
+template <int D, bool Q8, bool WHOLE, int HT>
+__global__ __launch_bounds__(kThreads, D == 64 ? (HT == 1 ? 4 : 3) : D == 128 ? 2 : 1) void attn_kernel(AttnArgs a) {
   using T = Tile<D, Q8>;
   constexpr int VJ = T::VJ;
   constexpr int kPad = D + 4;                        // LDS rows of neighbouring heads start in other banks
   extern __shared__ float sums[];                    // [kWaves][rows][kPad], rows = heads of a tile
   __shared__ uint32_t scan[kWaves], found[3][kWaves];
-  __shared__ float wave_m[kWaves][16], wave_l[kWaves][16], run_m[kWaves][16];
+  __shared__ float wave_m[kWaves][16 * HT], wave_l[kWaves][16 * HT], run_m[kWaves][16 * HT];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
   if constexpr (Q8) __builtin_amdgcn_s_setreg(1 | (23 << 6) | (0 << 11), 1);   // hwreg(MODE, 23, 1): FP16_OVFL
   const uint32_t vs_lane = 2 * ((((VJ * (uint32_t)c) / 32) << a.tok_shift) + 4 * g);   // the lane's V scales
@@ -485,13 +497,13 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
   }
   const uint32_t v = v0 + wave, live = min((uint32_t)kWaves, line.waves - v0);   // waves with a part of the line
 
-  f32x4 o[VJ];
-  float ref = -INFINITY, l = 0.f;
+  f32x4 o[HT][VJ];
+  float ref[HT], l[HT];
   Segment cur;
   if ((uint32_t)wave < live) {
     const uint32_t end = line.start(v + 1);
     T t;
-    half8_t q[T::KD];
+    half8_t q[HT][T::KD];
     Block blk[2];
     int32_t page[2];                                 // of the tile in t; below 0: none
     cur = segment_at<WHOLE>(a, line.start(v), end, (int32_t)from_b, from_at, from_len);
@@ -517,8 +529,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
       const uint16_t *at = a.q + uniform(fetch.b) * a.ldq + (int64_t)uniform(fetch.h0) * D;
       const rsrc_t r = make_rsrc(at, (uint32_t)uniform(fetch.rows) * D * 2);
 #pragma unroll
-      for (int i = 0; i < T::KD; ++i)
-        q[i] = __builtin_bit_cast(half8_t, bldx4<0>(r, c * (2 * D) + 32 * g, 128 * (i >> 1) + 16 * (i & 1)));
+      for (int u = 0; u < HT; ++u)
+#pragma unroll
+        for (int i = 0; i < T::KD; ++i)
+          q[u][i] = __builtin_bit_cast(half8_t, bldx4<0>(r, c * (2 * D) + 32 * g, 32 * D * u + 128 * (i >> 1) + 16 * (i & 1)));
     };
     // The loads are issued in one order everywhere (q where it changes, K, V), and after the last tile
     // from empty ranges instead of not at all: only so the wait for a tile's K or V leaves the
@@ -533,12 +547,16 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
     __builtin_amdgcn_sched_barrier(0);
     bool more = true;
     while (more) {
+      bool bad[HT];                                  // the lane's part of q is not finite
 #pragma unroll
-      for (int j = 0; j < VJ; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      ref = -INFINITY;
-      l = 0.f;
-      bool inside = true;                            // the tile in t is of segment cur
-      bool fresh = true, bad = false;                // and its first; the lane's part of q is not finite
+      for (int u = 0; u < HT; ++u) {
+#pragma unroll
+        for (int j = 0; j < VJ; ++j) o[u][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        ref[u] = -INFINITY;
+        l[u] = 0.f;
+        bad[u] = false;
+      }
+      bool inside = true, fresh = true;              // the tile in t is of segment cur, and its first
       while (inside) {
         const int32_t t0 = token(0);
         const bool full = t0 >= cur.first && t0 + kTile <= cur.len && page[0] >= 0 && page[1] >= 0;
@@ -559,105 +577,123 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : D == 128 ? 2 : 1) void attn
           if (more) fetch = segment_at<WHOLE>(a, fetch.at, end, fetch.b, fetch.u0 - (fetch.u1 - fetch.u0) * fetch.ht, fetch.len);
         }
         look_up();
-        f32x4 x[2];
+        f32x4 x[2][HT];
 #pragma unroll
-        for (int st = 0; st < 2; ++st) x[st] = scores<D, Q8>(t, st, q);
+        for (int st = 0; st < 2; ++st) scores<D, Q8, HT>(t, st, q, x[st]);
         if (Q8 && fresh) {
-          bad = nonfinite<T::KD>(q);
+#pragma unroll
+          for (int u = 0; u < HT; ++u) bad[u] = nonfinite<T::KD>(q[u]);
           fresh = false;
         }
         locate();
         if (more && !inside) load_q();
         load_k<D, Q8>(a, blk, t);
-        float y[8], top = -INFINITY;
+        half8_t hi[HT], lo[HT];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i >> 2][i & 3] * a.scale_log2;
-        if (!full) {
+        for (int u = 0; u < HT; ++u) {
+          float y[8], top = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = (valid >> i & 1) ? y[i] : -INFINITY;
-        }
+          for (int i = 0; i < 8; ++i) y[i] = x[i >> 2][u][i & 3] * a.scale_log2;
+          if (!full) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
-        if (__any(top > ref + kHigh)) {
-          top = fmaxf(top, __shfl_xor(top, 16));
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const float now = fmaxf(ref, top - kLow);
-          const float keep = now == ref ? 1.0f : __builtin_amdgcn_exp2f(ref - now);
-          ref = now;
-          l *= keep;
+            for (int i = 0; i < 8; ++i) y[i] = (valid >> i & 1) ? y[i] : -INFINITY;
+          }
 #pragma unroll
-          for (int j = 0; j < VJ; ++j) o[j] *= keep;
-        }
-        float p[8];
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
+          if (__any(top > ref[u] + kHigh)) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float now = fmaxf(ref[u], top - kLow);
+            const float keep = now == ref[u] ? 1.0f : __builtin_amdgcn_exp2f(ref[u] - now);
+            ref[u] = now;
+            l[u] *= keep;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(y[i] - ref);
-        if (!full) {                                 // masked places may hold anything: zero times NaN is NaN
+            for (int j = 0; j < VJ; ++j) o[u][j] *= keep;
+          }
+          float p[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) p[i] = (valid >> i & 1) ? p[i] : 0.f;
-          if constexpr (Q8) {
+          for (int i = 0; i < 8; ++i) p[i] = __builtin_amdgcn_exp2f(y[i] - ref[u]);
+          if (!full) {                               // masked places may hold anything: zero times NaN is NaN
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t m = (valid >> i & 1) ? 0u : (i & 1) ? 0xFFFF0000u : 0x0000FFFFu;
-              t.vs[i >> 2][(i & 3) >> 1] &= ~m;
+            for (int i = 0; i < 8; ++i) p[i] = (valid >> i & 1) ? p[i] : 0.f;
+            if (u == 0) {
+              if constexpr (Q8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const uint32_t m = (valid >> i & 1) ? 0u : (i & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+                  t.vs[i >> 2][(i & 3) >> 1] &= ~m;
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                  for (int k = 0; k < T::VW; ++k) t.v[i][k] = (valid >> i & 1) ? t.v[i][k] : 0u;
+              }
             }
-          } else {
+          }
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-              for (int k = 0; k < T::VW; ++k) t.v[i][k] = (valid >> i & 1) ? t.v[i][k] : 0u;
+          for (int i = 0; i < 8; ++i) {
+            l[u] += p[i];
+            hi[u][i] = (_Float16)p[i];
+            lo[u][i] = (_Float16)(p[i] - (float)hi[u][i]);
           }
         }
-        half8_t hi, lo;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          l += p[i];
-          hi[i] = (_Float16)p[i];
-          lo[i] = (_Float16)(p[i] - (float)hi[i]);
-        }
-        accumulate<D, Q8>(t, hi, lo, o);
+        accumulate<D, Q8, HT>(t, hi, lo, o);
         load_v<D, Q8>(a, blk, vs_lane, t);
       }
-      if (Q8 && bad && ref > -INFINITY) l = __builtin_nanf("");   // ref: moved by the first token that is seen
-      l += __shfl_xor(l, 16);
-      l += __shfl_xor(l, 32);
+#pragma unroll
+      for (int u = 0; u < HT; ++u) {
+        if (Q8 && bad[u] && ref[u] > -INFINITY) l[u] = __builtin_nanf("");   // ref: moved by the first token that is seen
+        l[u] += __shfl_xor(l[u], 16);
+        l[u] += __shfl_xor(l[u], 32);
+      }
       if (more) {
         // going on past this head tile: its result if the wave had all of it, else a part
         float *slot = cur.from_start ? nullptr : slot_of(a, 2 * v, D);
-        if (c < cur.rows) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+        for (int u = 0; u < HT; ++u)
+          if (16 * u + c < cur.rows) {
 #pragma unroll
-            for (int j = 0; j < VJ; j += 4)
-              store_result<D>(a, cur.b, cur.h0, slot, c, VJ * (4 * g + i) + j,
-                              f32x4{o[j][i], o[j + 1][i], o[j + 2][i], o[j + 3][i]}, ref, l);
-        }
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < VJ; j += 4)
+                store_result<D>(a, cur.b, cur.h0, slot, 16 * u + c, VJ * (4 * g + i) + j,
+                                f32x4{o[u][j][i], o[u][j + 1][i], o[u][j + 2][i], o[u][j + 3][i]}, ref[u], l[u]);
+          }
         cur = fetch;
       }
     }
   }
 
   // the waves that ended on one head tile join their parts; the leader stores the sum
-  if ((uint32_t)wave < live && g == 0) wave_m[wave][c] = ref;
+  if ((uint32_t)wave < live && g == 0) {
+#pragma unroll
+    for (int u = 0; u < HT; ++u) wave_m[wave][16 * u + c] = ref[u];
+  }
   __syncthreads();
   uint32_t lead = 0, tail = 0;                       // first and last wave that end on this wave's head tile
   if ((uint32_t)wave < live) {
     lead = tail = wave;
     while (lead > 0 && line.start(v0 + lead) > cur.u0) --lead;
     while (tail + 1 < live && line.start(v0 + tail + 2) <= cur.u1) ++tail;
-    float m = ref;
-    for (uint32_t k = lead; k <= tail; ++k) m = fmaxf(m, wave_m[k][c]);
-    const float f = ref == m ? 1.0f : __builtin_amdgcn_exp2f(ref - m);
-    if (g == 0) {
-      wave_l[wave][c] = l * f;
-      run_m[wave][c] = m;
-    }
-    if (c < cur.rows) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int u = 0; u < HT; ++u) {
+      const int r = 16 * u + c;
+      float m = ref[u];
+      for (uint32_t k = lead; k <= tail; ++k) m = fmaxf(m, wave_m[k][r]);
+      const float f = ref[u] == m ? 1.0f : __builtin_amdgcn_exp2f(ref[u] - m);
+      if (g == 0) {
+        wave_l[wave][r] = l[u] * f;
+        run_m[wave][r] = m;
+      }
+      if (r < cur.rows) {
 #pragma unroll
-        for (int j = 0; j < VJ; j += 4)
-          *reinterpret_cast<f32x4 *>(sums + (wave * a.rows + c) * kPad + VJ * (4 * g + i) + j) =
-              f32x4{o[j][i] * f, o[j + 1][i] * f, o[j + 2][i] * f, o[j + 3][i] * f};
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < VJ; j += 4)
+            *reinterpret_cast<f32x4 *>(sums + (wave * a.rows + r) * kPad + VJ * (4 * g + i) + j) =
+                f32x4{o[u][j][i] * f, o[u][j + 1][i] * f, o[u][j + 2][i] * f, o[u][j + 3][i] * f};
+      }
     }
   }
   __syncthreads();
@@ -699,8 +735,8 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(AttnArgs a, uint32_t
   const uint32_t e1 = left ? w1 - 1 : w1;            // the last wave that ends on the head tile
   const uint32_t groups = e1 / kWaves - w0 / kWaves + 1, n = groups + (left ? 1 : 0);
   if (n == 1) return;
-  const int32_t kvh = ht / a.tiles_per_kv, first_head = (ht - kvh * a.tiles_per_kv) * 16;
-  const int32_t rows = min(16, a.group - first_head);
+  const int32_t kvh = ht / a.tiles_per_kv, first_head = (ht - kvh * a.tiles_per_kv) * a.tile_heads;
+  const int32_t rows = min(a.tile_heads, a.group - first_head);
   const uint32_t i4 = threadIdx.x % kLanes, part = threadIdx.x / kLanes;
   for (int32_t r = blockIdx.y; r < rows; r += gridDim.y) {
     float m = -INFINITY, l = 0.f;
@@ -754,14 +790,25 @@ int64_t attn_tiles(int64_t max_len, int64_t window) {
   return tiles > 1 ? tiles : 1;
 }
 
-// Workgroups of four waves that are resident at once (heads of 64: four a CU, of 128: two). Heads of
-// 256 would fit two as well, but their parts are 16 KB for 16 heads: one a CU writes and joins half
-// as many.
-int64_t attn_resident(int64_t dim) { return dim == 64 ? 1024 : dim == 128 ? 512 : 256; }
+// Workgroups of four waves that are resident at once (heads of 64: four a CU, three with 32 heads a
+// tile; of 128: two). Heads of 256 would fit two as well, but their parts are 16 KB for 16 heads: one a
+// CU writes and joins half as many.
+int64_t attn_resident(int64_t dim, int64_t tile_heads) { return dim == 64 ? (tile_heads == 16 ? 1024 : 768) : dim == 128 ? 512 : 256; }
+
+// Heads of a head tile. More than 16 heads of a KV head in two tiles of 16 read and decode its K and V
+// twice, so a tile takes 32 where the waves have steps enough for that to count; with few steps
+// the larger parts cost more than this gains. 16 against 32 heads a tile, us: 32 sequences of 8192 tokens
+// and 8 KV heads of 128 with 32 heads each, fp16 298 : 178, int8 168 : 113; 48 and 4 KV heads with 20
+// each, int8, 141 : 93; but 16 of up to 8000 and 2 KV heads with 32 each 24.5 : 26, one sequence of
+// 4000 and 71 heads of 64 9.9 : 11.6.
+int32_t attn_tile_heads(int64_t group, int64_t kv_heads, int64_t batch, int64_t tiles, int64_t dim) {
+  const int64_t steps = batch * kv_heads * ((group + 15) / 16) * tiles;
+  return group > 16 && steps >= 8 * kWaves * attn_resident(dim, 16) ? 32 : 16;
+}
 
 // Workgroups of the split: those resident, or as many as there are tiles for.
-int32_t attn_grid(int64_t batch, int64_t head_tiles, int64_t tiles, int64_t dim) {
-  const int64_t all = (batch * head_tiles * tiles + kWaves - 1) / kWaves, most = attn_resident(dim);
+int32_t attn_grid(int64_t batch, int64_t head_tiles, int64_t tiles, int64_t dim, int64_t tile_heads) {
+  const int64_t all = (batch * head_tiles * tiles + kWaves - 1) / kWaves, most = attn_resident(dim, tile_heads);
   return (int32_t)(all < most ? all : most);
 }
 
@@ -782,34 +829,37 @@ bool attn_whole(int64_t head_tiles, int64_t tiles, int64_t dim) {
 // wave), 80 of 500 30.4 : 24.3 (two); 8 heads of 128 and 512 of up to 120 tokens 32.4 : 22.2 (one),
 // 128 of them 13.1 : 10.2 (two), 64 of 500, which all fit, 16.9 : 19.7 with two. Long ones keep the
 // card full with four: fp16, 512 sequences of 1000 tokens on 4 heads of 128 173 : 188 with two.
-int whole_waves(int64_t head_tiles, int64_t tiles, int64_t dim) {
-  const int64_t resident = attn_resident(dim);
+int whole_waves(int64_t head_tiles, int64_t tiles, int64_t dim, int64_t tile_heads) {
+  const int64_t resident = attn_resident(dim, tile_heads);
   if (head_tiles <= resident || tiles > 16) return kWaves;
   return head_tiles >= 4 * resident || (head_tiles > 2 * resident && tiles <= 8) ? 1 : 2;
 }
 
 int64_t starts_bytes(int64_t batch) { return (4 * (batch + 1) + 15) / 16 * 16; }
 
-template <int D, bool Q8>
+template <int D, bool Q8, int HT>
 int launch_attn(const AttnArgs &a, int64_t tiles, hipStream_t s) {
   const size_t lds = sizeof(float) * a.rows * (D + 4);
   const int64_t all = (int64_t)a.batch * a.head_tiles;
   if (attn_whole(all, tiles, D)) {
-    const int waves = whole_waves(all, tiles, D);
-    return launch(attn_kernel<D, Q8, true>, dim3((unsigned)all), dim3(64 * waves), waves * lds, s, a);
+    const int waves = whole_waves(all, tiles, D, a.tile_heads);
+    return launch(attn_kernel<D, Q8, true, HT>, dim3((unsigned)all), dim3(64 * waves), waves * lds, s, a);
   }
-  const int32_t grid = attn_grid(a.batch, a.head_tiles, tiles, D);
-  if (int st = launch(attn_kernel<D, Q8, false>, dim3(grid), dim3(kThreads), kWaves * lds, s, a)) return st;
-  // few head tiles: a workgroup for each head, the more threads for an element the more parts there are
+  const int32_t grid = attn_grid(a.batch, a.head_tiles, tiles, D, a.tile_heads);
+  if (int st = launch(attn_kernel<D, Q8, false, HT>, dim3(grid), dim3(kThreads), kWaves * lds, s, a)) return st;
+  // few head tiles: their heads shared out over workgroups (about 2048 in all), the more threads for an
+  // element the more parts there are. 128 head tiles of 32 heads: 85 us with one workgroup each, 57 so.
   const uint32_t waves = (uint32_t)grid * kWaves;
-  const dim3 heads((unsigned)all, all * a.rows <= 2048 ? (unsigned)a.rows : 1u);
+  const int64_t share = 2048 / all;
+  const dim3 heads((unsigned)all, (unsigned)(share < 1 ? 1 : share < a.rows ? share : a.rows));
   if (grid / all >= 128) return launch(attn_join_kernel<D, 1024>, heads, dim3(1024), 0, s, a, waves);
   return launch(attn_join_kernel<D, 256>, heads, dim3(256), 0, s, a, waves);
 }
 
 template <int D>
 int launch_dim(const AttnArgs &a, int64_t tiles, bool q8, hipStream_t s) {
-  return q8 ? launch_attn<D, true>(a, tiles, s) : launch_attn<D, false>(a, tiles, s);
+  if (a.tile_heads == 16) return q8 ? launch_attn<D, true, 1>(a, tiles, s) : launch_attn<D, false, 1>(a, tiles, s);
+  return q8 ? launch_attn<D, true, 2>(a, tiles, s) : launch_attn<D, false, 2>(a, tiles, s);
 }
 
 int attn_shape(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_len, KvLayout *L) {
@@ -832,13 +882,14 @@ int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t head
   if (!bytes) return QG_ERR_NULL;
   KvLayout L;
   if (int st = attn_shape(pool, batch, heads, max_len, &L)) return st;
-  const int64_t group = heads / pool->kv_heads, rows = group < 16 ? group : 16;
-  const int64_t head_tiles = (group + 15) / 16 * pool->kv_heads, tiles = attn_tiles(max_len, 0);
-  // a window only shortens the head tiles: what needs no join without one needs none with one
+  const int64_t group = heads / pool->kv_heads, tiles = attn_tiles(max_len, 0), dim = pool->head_dim;
+  const int64_t tile = attn_tile_heads(group, pool->kv_heads, batch, tiles, dim);
+  // a window only shortens the head tiles: what needs no join without one needs none with one, and
+  // a call that is left with tiles of 16 heads has no more waves than counted here, nor larger parts
   *bytes = 0;
-  if (batch == 0 || attn_whole(batch * head_tiles, tiles, pool->head_dim)) return QG_OK;
-  const int64_t slots = 2 * kWaves * attn_grid(batch, head_tiles, tiles, pool->head_dim);
-  *bytes = starts_bytes(batch) + 4 * slots * slot_floats((int32_t)rows, pool->head_dim);
+  if (batch == 0 || attn_whole(batch * pool->kv_heads * ((group + tile - 1) / tile), tiles, dim)) return QG_OK;
+  const int64_t slots = 2 * kWaves * attn_grid(batch, (group + 15) / 16 * pool->kv_heads, tiles, dim, 16);
+  *bytes = starts_bytes(batch) + 4 * slots * slot_floats((int32_t)(group < tile ? group : tile), (int32_t)dim);
   return QG_OK;
 }
 
@@ -862,6 +913,8 @@ int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q,
     return QG_ERR_ALIGN;
   if (workspace_bytes < need) return QG_ERR_WORKSPACE;
   AttnArgs a;
+  a.window = (int32_t)(window > max_len ? 0 : window);
+  const int64_t tiles = attn_tiles(max_len, a.window);
   a.pool = static_cast<const uint8_t *>(pool->pages) + (layer ? layer * pool->layer_stride : 0);
   a.page_bytes = L.page_bytes;
   a.head_bytes = L.head_bytes;
@@ -878,11 +931,11 @@ int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q,
   a.batch = (int32_t)batch;
   a.heads = (int32_t)heads;
   a.group = (int32_t)(heads / pool->kv_heads);
-  a.tiles_per_kv = (a.group + 15) / 16;
+  a.tile_heads = attn_tile_heads(a.group, pool->kv_heads, batch, tiles, pool->head_dim);
+  a.tiles_per_kv = (a.group + a.tile_heads - 1) / a.tile_heads;
   a.head_tiles = a.tiles_per_kv * pool->kv_heads;
-  a.rows = a.group < 16 ? a.group : 16;
+  a.rows = a.group < a.tile_heads ? a.group : a.tile_heads;
   a.max_len = (int32_t)max_len;
-  a.window = (int32_t)(window > max_len ? 0 : window);
   a.scale_log2 = scale * kLog2e;
   a.out = out;
   a.ldo = batch > 1 ? ldo : cols;
@@ -891,7 +944,6 @@ int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q,
   a.starts = static_cast<uint32_t *>(workspace);
   a.starts_in = static_cast<const int32_t *>(workspace);
   a.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + starts_bytes(batch));
-  const int64_t tiles = attn_tiles(max_len, a.window);
   const bool q8 = pool->kind == QG_KV_Q8;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   switch (pool->head_dim) {

@@ -217,6 +217,32 @@ def test_many_short_sequences(kind, batch, kv_heads, group, dim, most, window):
     check_attention(out, lse, _torch_reference(*values, table, lens.tolist(), q, dim ** -0.5, window), most, dim)
 
 
+@pytest.mark.parametrize("kind,batch,kv_heads,group,dim,max_len,most,window", [
+    ("q8", 8, 1, 20, 256, 16384, 700, 0), ("f16", 9, 1, 33, 256, 16384, 300, 40), ("q8", 40, 2, 17, 128, 8192, 400, 0),
+    ("f16", 33, 3, 71, 128, 8192, 1500, 0), ("q8", 64, 1, 48, 64, 16384, 900, 5000), ("f16", 70, 4, 32, 64, 8192, 250, 0),
+    ("q8", 600, 1, 40, 128, 512, 512, 0), ("f16", 700, 1, 33, 64, 512, 200, 70), ("q8", 230, 1, 64, 256, 512, 300, 0),
+    ("f16", 200, 1, 45, 256, 512, 512, 0), ("q8", 1100, 1, 18, 64, 512, 90, 0), ("f16", 600, 1, 50, 128, 500, 500, 100)])
+def test_more_than_sixteen_heads(kind, batch, kv_heads, group, dim, max_len, most, window):
+    """Head tiles of 32 heads, full and ragged, whole and split; lens of all sizes under max_len."""
+    rng = np.random.default_rng(batch + group)
+    tokens = int(rng.choice([16, 32, 64]))
+    pool, values, gen = _filled(kind, kv_heads, dim, tokens, 300, group)
+    lens = rng.integers(0, most + 1, batch) * (rng.random(batch) < 0.9)
+    lens[0] = most
+    table = dev(rng.integers(0, 300, (batch, -(-max_len // tokens))))
+    q = (torch.randn((batch, group * kv_heads, dim), generator=gen, device="cuda") * 1.5).half()
+    q[1, -1, 3] = float("nan")                       # the last head of a ragged tile
+    lens[1] = 33
+    out, lse = qg.paged_attention(pool, q, table, dev(lens), max_len=max_len, window=window, out_f32=True, return_lse=True)
+    assert torch.all(torch.isnan(out[1, -1])) and torch.isnan(lse[1, -1])
+    q[1, -1] = 0
+    again, lse2 = qg.paged_attention(pool, q, table, dev(lens), max_len=max_len, window=window, out_f32=True, return_lse=True)
+    same = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+    same[1, -1] = False
+    assert torch.equal(again[same], out[same]) and torch.equal(lse2[same], lse[same])
+    check_attention(again, lse2, _torch_reference(*values, table, lens.tolist(), q, dim ** -0.5, window), most, dim)
+
+
 # ---- graphs ------------------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("kind,max_len", [("q8", 256), ("f16", 8192)])
