@@ -525,14 +525,14 @@ __global__ __launch_bounds__(kThreads, D == 64 ? (HT == 1 ? 4 : 3) : D == 128 ? 
         blk[st].place = (uint32_t)token(st) & ((1u << a.tok_shift) - 1);
       }
     };
-    auto load_q = [&]() {                            // heads past the tile's read as zeros
+    auto load_q = [&]() {                            // heads past the tile's read as zeros: their lanes' own offsets are out of range
       const uint16_t *at = a.q + uniform(fetch.b) * a.ldq + (int64_t)uniform(fetch.h0) * D;
       const rsrc_t r = make_rsrc(at, (uint32_t)uniform(fetch.rows) * D * 2);
 #pragma unroll
       for (int u = 0; u < HT; ++u)
 #pragma unroll
         for (int i = 0; i < T::KD; ++i)
-          q[u][i] = __builtin_bit_cast(half8_t, bldx4<0>(r, c * (2 * D) + 32 * g, 32 * D * u + 128 * (i >> 1) + 16 * (i & 1)));
+          q[u][i] = __builtin_bit_cast(half8_t, bldx4<0>(r, (16 * u + c) * (2 * D) + 32 * g, 128 * (i >> 1) + 16 * (i & 1)));
     };
     // The loads are issued in one order everywhere (q where it changes, K, V), and after the last tile
     // from empty ranges instead of not at all: only so the wait for a tile's K or V leaves the
@@ -799,7 +799,8 @@ int64_t attn_resident(int64_t dim, int64_t tile_heads) { return dim == 64 ? (til
 // twice, so a tile takes 32 where the waves have steps enough for that to count; with few steps
 // the larger parts cost more than this gains. 16 against 32 heads a tile, us: 32 sequences of 8192 tokens
 // and 8 KV heads of 128 with 32 heads each, fp16 298 : 178, int8 168 : 113; 48 and 4 KV heads with 20
-// each, int8, 141 : 93; but 16 of up to 8000 and 2 KV heads with 32 each 24.5 : 26, one sequence of
+// each, int8, 141 : 93; 32 of 8000 and 2 of 256 with 32 each, fp16 (15 registers spilled) 166 : 123; but
+// 16 of up to 8000 and 2 KV heads with 32 each 24.5 : 26, one sequence of
 // 4000 and 71 heads of 64 9.9 : 11.6.
 int32_t attn_tile_heads(int64_t group, int64_t kv_heads, int64_t batch, int64_t tiles, int64_t dim) {
   const int64_t steps = batch * kv_heads * ((group + 15) / 16) * tiles;
