@@ -68,9 +68,10 @@ constexpr int kTile = 32;                          // tokens of a wave's step, t
 constexpr int kThreads = 64 * kWaves;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-// Weights are 2^(s - ref) with ref moved to (largest s) - 7 once a score passes ref + 15: they stay
-// below fp16's 65504 and small ones lose nothing above 2^-31 of the largest, while most steps find
-// ref good as it is.
+// Weights are 2^(s - ref) with ref moved to (largest s) - 7 once s - ref passes 15: they stay below
+// fp16's 65504 and small ones lose nothing above 2^-31 of the largest, while most steps find ref good
+// as it is. The difference itself is compared, as the weights use it: ref + 15 rounds up to ref + 16
+// for scores of 2^24 to 2^28.
 constexpr float kLow = 7.0f, kHigh = 15.0f;
 
 template <typename T>
@@ -600,7 +601,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? (HT == 1 ? 4 : 3) : D == 128 ? 
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
-          if (__any(top > ref[u] + kHigh)) {
+          if (__any(top - ref[u] > kHigh)) {         // ref -inf: moves for any score, not for none (NaN)
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
             const float now = fmaxf(ref[u], top - kLow);
