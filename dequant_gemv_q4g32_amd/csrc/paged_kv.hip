@@ -200,33 +200,35 @@ __global__ __launch_bounds__(kPageThreads) void kv_fork_kernel(PoolArgs p, Table
   const int32_t n = row_len(t, s);
   const int32_t whole = n >> t.tok_shift;
   const bool rest = (n & ((1 << t.tok_shift) - 1)) != 0;
-  if (!rest && !table_part) return;
-  const int32_t fresh = new_pages[i];
-  bool drop = rest && (fresh < 0 || fresh >= p.num_pages);
-  for (int32_t k = threadIdx.x; k < count; k += kPageThreads)
-    drop |= src_rows[k] == d || (k < i && (dst_rows[k] == d || (rest && new_pages[k] == fresh)));
-  if (__syncthreads_or(drop)) return;
   const int32_t *from = t.table + (int64_t)s * t.ld;
+  // a partly filled last page is copied; where the source's entry is no page, so is the new row's
   const int32_t tail = rest ? from[whole] : -1;
-  const bool tail_ok = tail >= 0 && tail < p.num_pages;
+  const bool copy = tail >= 0 && tail < p.num_pages;
+  if (!copy && !table_part) return;
+  const int32_t fresh = new_pages[i];
+  bool drop = copy && (fresh < 0 || fresh >= p.num_pages);
+  for (int32_t k = threadIdx.x; k < count; k += kPageThreads)
+    drop |= src_rows[k] == d || (k < i && (dst_rows[k] == d || (copy && new_pages[k] == fresh)));
+  if (__syncthreads_or(drop)) return;
   if (!table_part) {
-    if (tail_ok && tail != fresh) copy_chunk(p, blockIdx.z, tail, fresh, blockIdx.y - 1);
+    if (tail != fresh) copy_chunk(p, blockIdx.z, tail, fresh, blockIdx.y - 1);
     return;
   }
+  const int32_t taken = whole + (rest && !copy ? 1 : 0);    // entries that are the source's own
   int32_t *to = t.table + (int64_t)d * t.ld;
   for (int32_t j = threadIdx.x; j < t.pages; j += kPageThreads) {
     int32_t e = -1;
-    if (j < whole) {
+    if (j < taken) {
       e = from[j];
       if (e >= 0 && e < p.num_pages) atomicAdd(t.refs + e, 1);
-    } else if (j == whole && rest) {
+    } else if (j == whole && copy) {
       e = fresh;
     }
     to[j] = e;
   }
   if (threadIdx.x == 0) {
     t.lens[d] = n;
-    if (rest) t.refs[fresh] = 1;
+    if (copy) t.refs[fresh] = 1;
   }
 }
 

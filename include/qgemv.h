@@ -464,11 +464,13 @@ int qg_kv_copy_pages(const qg_kv_pool *pool, const int32_t *src, const int32_t *
 /* Fork: for i < count, table row dst_rows[i] becomes a second holder of row src_rows[i]'s
  * tokens. Its whole pages are shared (refs + 1 each); a last page that is only partly filled is
  * copied in every layer to page new_pages[i], whose refs become 1, so that the two rows grow
- * apart. Further entries of the row become -1 and lens[dst] = lens[src]. What the row held
- * before is overwritten, not released (qg_kv_free releases it). new_pages[i] is a free page, read
- * only when a last page is copied; one that some row holds would be overwritten. A fork is skipped, its row left as it was, when a row is outside the
- * table, when dst_rows[i] is also a source row or an earlier destination row of the call, or
- * when a copy is needed and new_pages[i] is outside the pool or named earlier in the call.
+ * apart. Where an entry of the source row is no page, the new row's is the same, a last one
+ * included: nothing is copied then, and new_pages[i] stays as it is. Further entries of the row
+ * become -1 and lens[dst] = lens[src]. What the row held before is overwritten, not released
+ * (qg_kv_free releases it). new_pages[i] is a free page, used only when a last page is copied; one
+ * that some row holds would be overwritten. A fork is skipped, its row left as it was, when a row
+ * is outside the table, when dst_rows[i] is also a source row or an earlier destination row of the
+ * call, or when a copy is needed and new_pages[i] is outside the pool or named earlier in the call.
  * count is at most 4096. */
 int qg_kv_fork(const qg_kv_pool *pool, int32_t *table, int64_t ld_table, int64_t table_rows, int64_t table_pages,
                int32_t *lens, int32_t *refs, const int32_t *src_rows, const int32_t *dst_rows,

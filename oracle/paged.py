@@ -135,19 +135,21 @@ def fork(cache, table, lens, refs, src_rows, dst_rows, new_pages):
             continue
         n = min(max(int(lens[s]), 0), table.shape[1] * cache.tokens)
         whole, rest = divmod(n, cache.tokens)
-        if rest and (not 0 <= fresh < cache.pages or fresh in new_pages[:i]):
+        tail = int(table[s, whole]) if rest else -1
+        copied = 0 <= tail < cache.pages                  # a last page that is partly filled, and is a page
+        if copied and (not 0 <= fresh < cache.pages or fresh in new_pages[:i]):
             continue
         row = np.full(table.shape[1], -1, table.dtype)
         row[:whole] = table[s, :whole]
         for e in row[:whole]:
             if 0 <= e < cache.pages:
                 refs[e] += 1
-        if rest:
-            tail = table[s, whole]
-            if 0 <= tail < cache.pages:
-                cache.copy_page(tail, fresh)
+        if copied:
+            cache.copy_page(tail, fresh)
             row[whole] = fresh
             refs[fresh] = 1
+        elif rest:
+            row[whole] = tail                             # no page there, as in the source
         table[d] = row
         lens[d] = n
 
