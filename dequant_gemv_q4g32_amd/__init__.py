@@ -359,7 +359,8 @@ class KVPool:
     several layers that share one page table. kind "q8": int8 groups of 32 with fp16 scales (the
     codec of kv_quantize); "f16": fp16. The record's layout is in include/qgemv.h. The pool keeps
     `pages` alive; every call on it takes its tensors on the pool's device and runs on torch's
-    current stream of that device unless `stream` is given."""
+    current stream of that device unless `stream` (a torch stream of that device, or a handle of
+    one as an int) is given."""
 
     def __init__(self, pages, kind: str, kv_heads: int, head_dim: int, page_tokens: int):
         torch = _torch()
@@ -401,6 +402,8 @@ _stream_now = getattr(getattr(_th, "_C", None), "_cuda_getCurrentRawStream", Non
 def _on(pool, stream):
     """The pool's device current and `stream` (None: that device's current one) torch's current
     stream, so that what a call allocates inside belongs to the stream it runs on."""
+    if stream is not None and not isinstance(stream, int) and stream.device != pool.device:
+        raise ValueError(f"stream must be one of {pool.device}")       # entering it would switch the device
     with _th.cuda.device(pool._index):
         if stream is None:
             yield
