@@ -392,10 +392,11 @@ class KVPool:
 
 
 # torch's own accessors behind torch.cuda.current_device and current_stream, which cost a decode
-# step's launch time each
+# step's launch time each; the public ones where a torch does not have them
 _th = sys.modules.get("torch")
-_device_now = getattr(getattr(_th, "_C", None), "_cuda_getDevice", None)
-_stream_now = getattr(getattr(_th, "_C", None), "_cuda_getCurrentRawStream", None)
+_device_now = getattr(getattr(_th, "_C", None), "_cuda_getDevice", None) or (lambda: _th.cuda.current_device())
+_stream_now = (getattr(getattr(_th, "_C", None), "_cuda_getCurrentRawStream", None)
+               or (lambda index: _th.cuda.current_stream(index).cuda_stream))
 
 
 @contextlib.contextmanager

@@ -1,4 +1,5 @@
-"""The paged-cache binding's streams (on the CPU, with stand-ins for what needs a GPU)."""
+"""The paged-cache binding's streams and devices (on the CPU, with stand-ins for what needs a GPU)."""
+import importlib.util
 import types
 
 import pytest
@@ -19,3 +20,32 @@ def test_stream_of_another_device_is_refused():
                  lambda: qg.kv_compact(pool, x, x, stream=other)):
         with pytest.raises(ValueError, match="stream"):
             call()
+
+
+def _second_copy():
+    """The package's module once more, under another name."""
+    spec = importlib.util.spec_from_file_location("qg_second_copy", qg.__file__)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+def test_torch_without_the_short_accessors(monkeypatch):
+    """The binding uses torch's private accessors of the current device and stream where they are, and
+    the public ones where a torch does not have them."""
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    mod = _second_copy()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: types.SimpleNamespace(cuda_stream=1000 + index))
+    assert mod._device_now() == 3 and mod._stream_now(2) == 1002
+
+
+@pytest.mark.gpu
+def test_short_and_public_accessors_agree():
+    torch.zeros(1, device="cuda")
+    side = torch.cuda.Stream()
+    for stream in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(stream):
+            assert qg._device_now() == torch.cuda.current_device()
+            assert qg._stream_now(0) == torch.cuda.current_stream(0).cuda_stream == stream.cuda_stream
