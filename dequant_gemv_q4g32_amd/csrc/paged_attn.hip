@@ -868,7 +868,9 @@ int attn_shape(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max
   if (int st = kv_pool_layout(pool, L)) return st;
   if (batch < 0 || heads < 1 || heads % pool->kv_heads || heads > (1 << 22) || batch > (1 << 22) / heads) return QG_ERR_SHAPE;
   if (max_len < 0 || max_len > (1 << 30)) return QG_ERR_SHAPE;
-  if (batch * heads * (attn_tiles(max_len, 0) + 1) > 0x7FFFFFFF) return QG_ERR_SHAPE;   // the line fits 31 bits
+  // The line fits 31 bits. Its extra units take nothing: a head tile has one below 16 tiles only (16 units
+  // at most then), and there is a line only where the longest has more than 16 tiles (attn_whole).
+  if (batch * heads * attn_tiles(max_len, 0) > 0x7FFFFFFF) return QG_ERR_SHAPE;
   return QG_OK;
 }
 
