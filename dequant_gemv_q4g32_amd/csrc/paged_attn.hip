@@ -421,7 +421,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? (HT == 1 ? 4 : 3) : D == 128 ? 
   using T = Tile<D, Q8>;
   constexpr int VJ = T::VJ;
   constexpr int kPad = D + 4;                        // LDS rows of neighbouring heads start in other banks
-  extern __shared__ float sums[];                    // [kWaves][rows][kPad], rows = heads of a tile
+  extern __shared__ __align__(16) float sums[];      // [kWaves][rows][kPad], rows = heads of a tile; in 16-byte accesses
   __shared__ uint32_t scan[kWaves], found[3][kWaves];
   __shared__ float wave_m[kWaves][16 * HT], wave_l[kWaves][16 * HT], run_m[kWaves][16 * HT];
   const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), c = lane & 15, g = lane >> 4;
