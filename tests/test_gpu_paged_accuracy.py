@@ -1,4 +1,5 @@
-"""GPU tests of how exactly paged decode attention adds up: scores of any size."""
+"""GPU tests of how exactly paged decode attention adds up: scores of any size, every step of a
+long cache counted once, and long caches to what fp32 sums of the kernel's shape allow."""
 import numpy as np
 import pytest
 
@@ -6,6 +7,7 @@ import dequant_gemv_q4g32_amd as qg
 from oracle import paged
 
 from paged_util import attention_tolerance, dev, upload
+from test_gpu_paged_flow import _filled, _torch_reference
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -67,3 +69,105 @@ def test_large_scores(kind, dim, exponent, sign):
             assert torch.isfinite(got).all() and torch.isfinite(got_lse).all()
             assert ((got.double() - ref).abs() <= tol).all(), f"{(got.double() - ref).abs().max():.3g}"
             assert ((got_lse.double() - ref_lse).abs() <= tol_lse).all()
+
+
+# ---- each step once ---------------------------------------------------------------------------------
+
+STEPS = [  # kind, heads, kv heads, dim, page tokens, table pages, lens, window
+    ("q8", 8, 2, 128, 16, 8192, [131072], 0), ("f16", 4, 1, 64, 256, 157, [40000, 7, 13001], 0),
+    ("q8", 16, 1, 256, 64, 313, [9000, 1, 20011], 0), ("f16", 12, 4, 128, 32, 2048, [65536, 0, 65535, 31, 1], 0),
+    ("f16", 16, 2, 256, 128, 256, [32768, 20000, 3, 32737], 0), ("q8", 4, 4, 64, 16, 2048, [32768, 32000, 1025], 1025),
+    ("f16", 40, 2, 128, 16, 1024, [16384, 9999] * 20, 0), ("q8", 64, 2, 64, 64, 256, [16384, 77, 16000] * 15, 0),
+    ("q8", 33, 1, 256, 16, 1250, [20000, 12345] * 8, 0), ("f16", 20, 1, 64, 32, 1000, [32000, 5000] * 20, 4000),
+    ("q8", 16, 4, 128, 16, 600, list(range(1, 9601, 31)), 0), ("f16", 8, 8, 64, 16, 300, list(range(0, 4800, 13)), 0),
+    ("q8", 8, 8, 128, 32, 64, list(range(2048, 0, -9)), 700)]
+
+
+@pytest.mark.parametrize("kind,heads,kv_heads,dim,tokens,pages,lens,window", STEPS)
+def test_every_step_counts_once(kind, heads, kv_heads, dim, tokens, pages, lens, window):
+    """With K = 0 every token has weight 1, so an output is the mean of V and lse is ln of the number of
+    tokens. V marks each token's 32-token step in two elements (their pair names the step), with 1 or 2
+    by the token's parity; one step left out, or counted twice, shows as 32 in a count.
+
+    All sums are exact: the weights are one power of two, their multiples by 0, 1 and 2 whole numbers
+    below 2^24 of it, the factors of the joins 1 (or 0, of parts without a token). What is left is the
+    reciprocal's and its product's rounding, 2^-23 of the value and a bit more; for lse a logarithm of
+    at most 24 good to 2^-21, and its product with ln 2."""
+    n = pages * tokens
+    half, step = dim // 2, np.arange(n) // 32
+    marks = np.zeros((n, dim))
+    value = 1.0 + np.arange(n) % 2
+    marks[np.arange(n), step % half] = value
+    marks[np.arange(n), half + step // half % half] = value
+    c = paged.Cache(kind, 1, pages, kv_heads, dim, tokens)
+    v = np.stack([np.roll(marks, g, axis=1).reshape(pages, tokens, dim) for g in range(kv_heads)], axis=1)[None]
+    rng = np.random.default_rng(n)
+    order = rng.permutation(pages)                        # logical page i lies in page order[i]
+    if kind == "q8":
+        c.codes[1][:, order], c.scales[1][...], c.scales[0][...] = v, 1.0, 0.5
+    else:
+        c.values[1][:, order] = v
+    sums = np.concatenate([np.zeros((1, dim)), np.cumsum(marks, axis=0)])
+    lens = np.array(lens)
+    first = np.maximum(0, lens - window) if window else np.zeros_like(lens)
+    count = lens - first
+    mean = (sums[lens] - sums[first]) / np.maximum(count, 1)[:, None]
+    ref = np.stack([np.roll(mean, h // (heads // kv_heads), axis=1) for h in range(heads)], axis=1)
+    table = dev(np.tile(order, (len(lens), 1)))
+    q = torch.randn((len(lens), heads, dim), generator=torch.Generator("cuda").manual_seed(n), device="cuda").half()
+    out, lse = qg.paged_attention(upload(c), q, table, dev(lens), window=window, out_f32=True, return_lse=True)
+    want = dev(ref, np.float64)
+    off = (out.double() - want).abs() - 1.01 * 2.0 ** -23 * want.abs()
+    assert (off <= 0).all(), f"sequence {int(off.flatten(1).amax(1).argmax())}: off by {float((out.double() - want).abs().max()):.3g}"
+    with np.errstate(divide="ignore"):
+        want = dev(np.log(count), np.float64)[:, None].expand_as(lse)
+    some = dev(count)[:, None].expand_as(lse) > 0
+    assert torch.all(torch.isneginf(lse[~some]))
+    assert ((lse.double() - want).abs()[some] <= 24 * 2.0 ** -21).all(), float((lse.double() - want).abs()[some].max())
+
+
+# ---- long caches closely ----------------------------------------------------------------------------
+
+def _close_tolerance(out, lse, bound, reach, lens, head_tiles, dim):
+    """As paged_util.attention_tolerance, with the roundings of sums counted along the longest chain
+    instead of one for each token. Relative to sum w |V| (out) and to sum w (lse), e = 2^-24:
+    - a wave runs through `steps` steps of 32 tokens: the share of the 32-token tiles of all head
+      tiles (one more for short ones) that falls to each of 1024 waves, which are fewer than the kernel has
+      wherever there are tiles enough, and one more;
+    - a step adds 32 products twice (the weights are pairs) to a sum of V and 8 weights to the
+      denominator, and may scale both: at most 2 * 33 + 1 and 9 roundings;
+    - joins: 4 waves, then at most 81 parts one after the other at 3 roundings each, and the quotient:
+      fewer than 260;
+    - a weight as a pair of fp16 numbers is off by 2^-22 of itself, or 2^-32 of the largest."""
+    e = 2.0 ** -24
+    total = sum(-(-n // 32) + 1 for n in lens) * head_tiles
+    steps = -(-total // 1024) + 1
+    score = (dim + 8) * e * reach
+    rel = 2 * (score + 2.0 ** -21) + (76 * steps + 520) * e + 2 * max(lens) * 2.0 ** -32
+    with np.errstate(invalid="ignore"):
+        size = np.where(np.isfinite(lse), np.abs(lse), 0.0)
+    return rel[..., None] * bound + 1e-30, rel + 4 * e * (size + reach) + 4 * e
+
+
+@pytest.mark.parametrize("kind,heads,kv_heads,dim,tokens,lens", [
+    ("q8", 8, 2, 128, 16, [20011]), ("f16", 4, 1, 64, 256, [40000, 7, 13001]), ("q8", 16, 1, 256, 64, [9000, 1]),
+    ("f16", 8, 8, 128, 32, [5000] * 3), ("q8", 4, 1, 64, 64, [40001, 39999, 20000]), ("f16", 4, 2, 128, 16, [30000, 11])])
+def test_long_caches_closely(kind, heads, kv_heads, dim, tokens, lens):
+    """fp32 output over long random caches, to a bound that a lost 32-token step of average weight
+    passes: lse's is below half of such a step's share (asserted)."""
+    pages = sum(-(-n // tokens) for n in lens)
+    pool, values, gen = _filled(kind, kv_heads, dim, tokens, pages, dim + len(lens))
+    order, table, at = torch.randperm(pages, generator=gen, device="cuda").int(), [], 0
+    for n in lens:
+        held = -(-n // tokens)
+        table.append(torch.nn.functional.pad(order[at:at + held], (0, -(-max(lens) // tokens) - held), value=-1))
+        at += held
+    table = torch.stack(table)
+    q = (torch.randn((len(lens), heads, dim), generator=gen, device="cuda") * 1.5).half()
+    out, lse = qg.paged_attention(pool, q, table, dev(lens), out_f32=True, return_lse=True)
+    ref = _torch_reference(*values, table, lens, q, dim ** -0.5, 0)
+    tol, tol_lse = _close_tolerance(*ref, lens, kv_heads, dim)
+    assert max(lens) < 16000 or (tol_lse[int(np.argmax(lens))] < 16 / max(lens)).all()
+    got, got_lse = out.cpu().double().numpy(), lse.cpu().double().numpy()
+    assert (np.abs(got - ref[0]) <= tol).all(), float((np.abs(got - ref[0]) / tol).max())
+    assert (np.abs(got_lse - ref[1]) <= tol_lse).all(), float((np.abs(got_lse - ref[1]) / tol_lse).max())
