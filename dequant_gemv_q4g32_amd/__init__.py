@@ -485,7 +485,7 @@ def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: 
     tokens only. Returns out [batch, heads, head_dim] (fp16, or fp32 with out_f32), or (out, lse)
     with return_lse or when lse (fp32 [batch, heads]) is given. A sequence without tokens gets zeros and
     lse -inf. workspace: uint8 of paged_attention_bytes(...), used by one call at a time; allocated
-    here when None."""
+    here when None. out, lse and workspace overlap nothing that the call reads, q among it."""
     if stream is not None or _device_now() != pool._index:
         with _on(pool, stream):
             return paged_attention(pool, q, table, lens, max_len, scale, window, out, out_f32, lse, return_lse, workspace, layer)
@@ -536,8 +536,9 @@ def kv_copy_pages(pool, src, dst, stream=None) -> None:
 
 def kv_fork(pool, table, lens, refs, src_rows, dst_rows, new_pages, stream=None) -> None:
     """Table rows dst_rows become second holders of src_rows' tokens: whole pages are shared (refs
-    counts them), a partly filled last page is copied to new_pages[i]. table, lens and refs are
-    updated in place; free the destination rows first if they hold anything."""
+    counts them), a partly filled last page is copied to new_pages[i] (a free page, left free where
+    there is nothing to copy). table, lens and refs are updated in place; free the destination rows
+    first if they hold anything."""
     if stream is not None or _device_now() != pool._index:
         with _on(pool, stream):
             return kv_fork(pool, table, lens, refs, src_rows, dst_rows, new_pages)
@@ -563,9 +564,9 @@ def kv_free(pool, table, lens, refs, rows, stream=None) -> None:
 def kv_compact(pool, table, refs, table_out=None, refs_out=None, remap=None, live=None, stream=None):
     """Move the held pages of the pool to its first pages, in every layer. Returns (table_out,
     refs_out, remap, live): the table and the counts for the moved pages (pass table and refs
-    themselves to update them in place), each page's new index (-1: free), and the number of
-    held pages (int32 [1] on the device). What is not given is allocated, the last three as views of
-    one buffer when none of them is."""
+    themselves to update them in place, else they must not overlap), each page's new index (-1: free),
+    and the number of held pages (int32 [1] on the device). What is not given is allocated, the last
+    three as views of one buffer when none of them is."""
     if stream is not None or _device_now() != pool._index:
         with _on(pool, stream):
             return kv_compact(pool, table, refs, table_out, refs_out, remap, live)

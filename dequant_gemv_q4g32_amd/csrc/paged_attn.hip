@@ -15,13 +15,15 @@
 // as hi + lo fp16 pairs, 22 bits.
 //
 // What bounds it: each cached byte is read once, so HBM, and for int8 also instruction issue (about
-// 380 vector and 130 scalar instructions a step of 8.7 KB; a wave alone needs 1.3 us for it). The
+// 372 vector and 130 scalar instructions a step of 8.7 KB; a wave alone needs 1.3 us for it). The
 // next step's K is on its way while the softmax and the products with V run, its V from then on.
 // Measured (GPU time; a plain stream of reads reaches 6.8 TB/s here): 64 sequences of 8192 tokens,
-// 64 heads on 8 of 128: fp16 319 us = 6.7 TB/s, int8 186 us = 6.1 TB/s; one of 131072 tokens, int8,
+// 64 heads on 8 of 128: fp16 320 us = 6.7 TB/s, int8 186 us = 6.1 TB/s; one of 131072 tokens, int8,
 // 54 us = 5.3 TB/s; 32 of up to 8192, int8, 47 us = 4.9 TB/s; 48 of up to 6007 with one KV head of
-// 256, int8, 28 us; one of 1000 tokens 9.5 us, of 100 tokens 6 us (a launch and four dependent
+// 256, int8, 27 us; one of 1000 tokens 9.5 us, of 100 tokens 6 us (a launch and four dependent
 // memory latencies: length, page, K, and the first step). HBM reads are the algorithm's bytes.
+// The scalar registers do not hold all of a wave's places: 34 to 61 spill to vector lanes, none in the
+// blocks with matrix instructions.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -799,10 +801,14 @@ int64_t attn_resident(int64_t dim, int64_t tile_heads) { return dim == 64 ? (til
 // Heads of a head tile. More than 16 heads of a KV head in two tiles of 16 read and decode its K and V
 // twice, so a tile takes 32 where the waves have steps enough for that to count; with few steps
 // the larger parts cost more than this gains. 16 against 32 heads a tile, us: 32 sequences of 8192 tokens
-// and 8 KV heads of 128 with 32 heads each, fp16 298 : 178, int8 168 : 113; 48 and 4 KV heads with 20
-// each, int8, 141 : 93; 32 of 8000 and 2 of 256 with 32 each, fp16 (15 registers spilled) 166 : 123; but
-// 16 of up to 8000 and 2 KV heads with 32 each 24.5 : 26, one sequence of
-// 4000 and 71 heads of 64 9.9 : 11.6.
+// and 8 KV heads of 128 with 32 heads each, fp16 303 : 187, int8 172 : 117; of 6000 and 4 KV heads with
+// 20 each, int8, 76 : 53; 32 of 8000 and 2 of 256 with 32 each, fp16 (17 registers spilled) 172 : 124; but
+// 16 of up to 8000 and 2 KV heads with 32 each 24.4 : 25.0, one sequence of 4000 and 71 heads of 64
+// 9.7 : 11.2. The steps are counted by max_len, since the lengths are on the device, so a ragged batch
+// of short ones can get 32 and lose: int8, 32 sequences of up to 8192 (40% of that on average) and one KV
+// head of 256 with 32 heads 35.6 : 38.7, with 20 33.4 : 34.5; of up to 4096 and 2 of 128 with 32 23.4 : 24.5;
+// 64 of up to 4000 and 71 heads of 64 26.7 : 27.3. With more work ragged ones gain too (32 of up to 8192 and 2
+// of 128 with 20 heads, int8 30.5 : 26.6, fp16 41.7 : 30.1).
 int32_t attn_tile_heads(int64_t group, int64_t kv_heads, int64_t batch, int64_t tiles, int64_t dim) {
   const int64_t steps = batch * kv_heads * ((group + 15) / 16) * tiles;
   return group > 16 && steps >= 8 * kWaves * attn_resident(dim, 16) ? 32 : 16;

@@ -438,8 +438,8 @@ int qg_kv_gather(const qg_kv_pool *pool, int64_t layer, const int32_t *table, in
  * fp32 rounding, at most 2 (head_dim + 8) 2^-24 max_j scale sum |q K_j|, and by the sums': 76
  * roundings (2^-24 each) for a step of 32 tokens of one wave, the steps of all head tiles shared
  * out over at least 1024 waves, and 520 for the joins. Both are bounds: 8000 to 131072 tokens of
- * random values measured 4e-7 at most with scale sum |q K_j| up to 20, 6e-6 up to 80 (lse 2e-6 and
- * 5e-6). fp16 out adds its one rounding.
+ * random values measured 4e-7 at most with scale sum |q K_j| up to 21, 6e-6 up to 84 (lse 2e-6 and
+ * 6e-6). fp16 out adds its one rounding.
  *
  * The cache's length is split over the workgroups, whose partial results go through
  * `workspace` (device, 16-byte aligned, at least qg_paged_attention_bytes, which is 0, and NULL will
