@@ -1,12 +1,13 @@
 """GPU tests of how exactly paged decode attention adds up: scores of any size, every step of a
-long cache counted once, and long caches to what fp32 sums of the kernel's shape allow."""
+long cache counted once, long caches to what fp32 sums of the kernel's shape allow, and the smallest
+values."""
 import numpy as np
 import pytest
 
 import dequant_gemv_q4g32_amd as qg
 from oracle import paged
 
-from paged_util import attention_tolerance, dev, upload
+from paged_util import attention_tolerance, check_attention, dev, upload
 from test_gpu_paged_flow import _filled, _torch_reference
 
 torch = pytest.importorskip("torch")
@@ -171,3 +172,32 @@ def test_long_caches_closely(kind, heads, kv_heads, dim, tokens, lens):
     got, got_lse = out.cpu().double().numpy(), lse.cpu().double().numpy()
     assert (np.abs(got - ref[0]) <= tol).all(), float((np.abs(got - ref[0]) / tol).max())
     assert (np.abs(got_lse - ref[1]) <= tol_lse).all(), float((np.abs(got_lse - ref[1]) / tol_lse).max())
+
+
+# ---- small values -----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind,dim", [("f16", 64), ("f16", 128), ("f16", 256), ("q8", 64), ("q8", 128), ("q8", 256)])
+@pytest.mark.parametrize("what", ["k", "v", "q", "all"])
+def test_subnormal_values(kind, dim, what):
+    """K, V or q of fp16 subnormals (int8 pages: with subnormal scales), exact like any others. The scale
+    makes up for them, so that the scores differ by far more than the tolerance: taken as zeros they
+    would not pass, nor V, whose tolerance is relative."""
+    lens, tokens, heads = [300, 33, 1], 16, 8
+    rng = np.random.default_rng(dim)
+    c = paged.Cache(kind, 1, 25, 2, dim, tokens)
+    small = {"k": what in ("k", "all"), "v": what in ("v", "all"), "q": what in ("q", "all")}
+    for i, name in enumerate("kv"):
+        if kind == "q8":
+            c.codes[i][...] = rng.integers(-127, 128, c.codes[i].shape)
+            steps = rng.integers(1, 9, c.scales[i].shape)
+            c.scales[i][...] = steps * (2.0 ** -24 if small[name] else 2.0 ** -8)
+        else:
+            c.values[i][...] = rng.integers(-1023, 1024, c.values[i].shape) * (2.0 ** -24 if small[name] else 2.0 ** -9)
+    q = (rng.integers(-1023, 1024, (3, heads, dim)) * (2.0 ** -24 if small["q"] else 2.0 ** -9)).astype(np.float16)
+    scale = float(np.float32(0.5 * (2.0 ** 15 if small["k"] else 1.0) * (2.0 ** 15 if small["q"] else 1.0) / dim))
+    table = rng.integers(0, 25, (3, 19)).astype(np.int32)
+    ref = paged.attention(c, 0, q, table, lens, 10 ** 6, scale)
+    assert ref[0].any() and (ref[3][0] > 0.25).all()      # the size of the scores' terms
+    for f32 in (True, False):
+        out, lse = qg.paged_attention(upload(c), dev(q, np.float16), dev(table), dev(lens), scale=scale, out_f32=f32, return_lse=True)
+        check_attention(out, lse, ref, max(lens), dim)
