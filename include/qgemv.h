@@ -433,13 +433,14 @@ int qg_kv_gather(const qg_kv_pool *pool, int64_t layer, const int32_t *table, in
  * heads dense; out: fp16, or fp32 with out_f32 != 0, row b at out + b * ldo, heads dense; lse:
  * fp32 [batch][heads], or NULL. The new token's own K and V are in the cache before the call
  * (qg_kv_append) and counted by lens. Products, the softmax and its sums are fp32; the weights
- * e^(s_j - max) meet V as a pair of fp16 numbers (their rounding and its remainder, 22 bits). fp32
- * out, relative to sum_j w_j |V_j| with w_j the weights' shares, and lse are off by the scores'
- * fp32 rounding, at most 2 (head_dim + 8) 2^-24 max_j scale sum |q K_j|, and by the sums': 76
- * roundings (2^-24 each) for a step of 32 tokens of one wave, the steps of all head tiles shared
- * out over at least 1024 waves, and 520 for the joins. Both are bounds: 8000 to 131072 tokens of
- * random values measured 4e-7 at most with scale sum |q K_j| up to 21, 6e-6 up to 84 (lse 2e-6 and
- * 6e-6). fp16 out adds its one rounding.
+ * e^(s_j - max) meet V as a pair of fp16 numbers (their rounding and its remainder, 22 bits).
+ * Bounds of the error, relative to sum_j w_j |V_j| with w_j the weights' shares for fp32 out and
+ * absolute for lse: 2 (head_dim + 8) 2^-24 max_j |scale| sum |q K_j| for the scores' fp32 rounding, 2^-20
+ * and 2^-31 a token for the weights' pairs, 2^-24 for each of the sums' roundings: 76 a step of 32
+ * tokens of a wave (at most 16 steps, or a wave's share if all head tiles' steps are shared out over
+ * 1024 waves) and 520 for the joins; lse also has 2^-22 of its own and the scores' size. 8000 to
+ * 131072 tokens of random values measured 4e-7 at most with |scale| sum |q K_j| up to 21, 6e-6 up to
+ * 84 (lse 2e-6 and 6e-6). fp16 out adds its one rounding.
  *
  * The cache's length is split over the workgroups, whose partial results go through
  * `workspace` (device, 16-byte aligned, at least qg_paged_attention_bytes, which is 0, and NULL will
