@@ -27,7 +27,7 @@ HOST_ONLY_LIB = os.environ.get("QGEMV_HOST_ONLY_LIBRARY")
 LIB_PATH = HOST_ONLY_LIB or os.path.join(_HERE, "libqgemv.so")
 # exported by the host code (host.cpp); everything else is device code
 HOST_FUNCTIONS = ("qg_abi_version", "qg_strerror", "qg_canonical_bytes", "qg_device_layout",
-                  "qg_packed_bytes", "qg_kv_page_bytes", "qg_pack_bits", "qg_unpack_bits", "qg_quantize", "qg_to_device_layout",
+                  "qg_packed_bytes", "qg_kv_page_bytes", "qg_rope_freqs", "qg_pack_bits", "qg_unpack_bits", "qg_quantize", "qg_to_device_layout",
                   "qg_from_device_layout")
 HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "qgemv.h")
 
@@ -64,6 +64,12 @@ class _Pool(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("layers", ctypes.c_int64),
                 ("layer_stride", ctypes.c_int64), ("kind", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32)]
+
+
+class _Rotary(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("factor", ctypes.c_float), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 def _load() -> ctypes.CDLL:
@@ -110,6 +116,12 @@ def _load() -> ctypes.CDLL:
         "qg_kv_free": ([vp, vp, i64, i64, i64, vp, vp, vp, i64, vp], i32),
         "qg_kv_compact_bytes": ([vp, ctypes.POINTER(i64)], i32),
         "qg_kv_compact": ([vp, vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp], i32),
+        "qg_kv_extend_bytes": ([vp, i64, ctypes.POINTER(i64)], i32),
+        "qg_kv_extend": ([vp, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp], i32),
+        "qg_kv_trim": ([vp, vp, i64, i64, i64, vp, vp, vp, vp], i32),
+        "qg_rope_freqs": ([i32, i64] + [ctypes.c_double] * 5 + [vp], i32),
+        "qg_qk_rope": ([vp, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp], i32),
+        "qg_kv_append_rope": ([vp, i64, vp, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp], i32),
         "qg_dequantize": ([i32, vp, vp, vp, i64, i64, vp], i32),
         "qg_read_probe": ([vp, i64, vp, vp], i32),
     }
@@ -380,6 +392,7 @@ class KVPool:
         self._ref = ctypes.addressof(self._c)
         # workspace sizes, kept by the sizes they follow from: asking the library takes 1 us of a call's 15
         self._attention_bytes = functools.lru_cache(256)(functools.partial(_workspace, "qg_paged_attention_bytes", self._c))
+        self._extend_bytes = functools.lru_cache(256)(functools.partial(_workspace, "qg_kv_extend_bytes", self._c))
         self._compact_bytes = functools.lru_cache(1)(functools.partial(_workspace, "qg_kv_compact_bytes", self._c))
 
     @classmethod
@@ -590,6 +603,174 @@ def kv_compact(pool, table, refs, table_out=None, refs_out=None, remap=None, liv
                               _ints(pool, "remap", remap, pool.num_pages), _ints(pool, "live", live, 1),
                               workspace.data_ptr(), need, _stream_now(pool._index)), "qg_kv_compact")
     return table_out, refs_out, remap, live
+
+
+def kv_extend(pool, table, lens, refs, add, slots: int, granted=None, starts=None, seqs=None, positions=None, stream=None):
+    """Places for a step's new tokens: row r of the table asks for add[r] more (int32 on the device, 0
+    or less: none), and gets the free pages that it lacks for them. Returns (granted, seqs, positions):
+    the tokens that each row got (add[r], or 0), and the slot map of `slots` places that kv_append
+    takes, row after row with the tokens asked for; the places of a row that got none hold -1, as do
+    those past the last row's. table, lens and refs are updated in place. A row gets none when the slots,
+    its table entries or the free pages (the rows before it come first) do not suffice, or when other rows hold the
+    partly filled page that its tokens would go to. starts, int32 [rows + 1], receives each row's first slot
+    if given; what else is not given is allocated as views of one buffer when none of it is."""
+    if stream is not None or _device_now() != pool._index:
+        with _on(pool, stream):
+            return kv_extend(pool, table, lens, refs, add, slots, granted, starts, seqs, positions)
+    at, ld, rows, pages = _table(pool, table)
+    if slots < 0:
+        raise ValueError("slots must not be negative")
+    need = pool._extend_bytes(rows)
+    if granted is None and seqs is None and positions is None:
+        granted, seqs, positions, workspace = refs.new_empty(rows + 2 * slots + need // 4).split_with_sizes(
+            (rows, slots, slots, need // 4))
+    else:
+        granted = refs.new_empty(rows) if granted is None else granted
+        seqs = refs.new_empty(slots) if seqs is None else seqs
+        positions = refs.new_empty(slots) if positions is None else positions
+        workspace = refs.new_empty(need // 4)
+    _check(_lib.qg_kv_extend(pool._ref, at, ld, rows, pages, _ints(pool, "lens", lens, rows),
+                             _ints(pool, "refs", refs, pool.num_pages), _ints(pool, "add", add, rows),
+                             _ints(pool, "granted", granted, rows),
+                             None if starts is None else _ints(pool, "starts", starts, rows + 1),
+                             _ints(pool, "seqs", seqs, slots), _ints(pool, "positions", positions, slots), slots,
+                             workspace.data_ptr(), need, _stream_now(pool._index)), "qg_kv_extend")
+    return granted, seqs, positions
+
+
+def kv_trim(pool, table, lens, refs, to, stream=None) -> None:
+    """The way back: a row r with 0 <= to[r] < lens[r] keeps its first to[r] tokens (int32 [rows] on
+    the device) and gives up the pages past them. table, lens and refs are updated in place."""
+    if stream is not None or _device_now() != pool._index:
+        with _on(pool, stream):
+            return kv_trim(pool, table, lens, refs, to)
+    at, ld, rows, pages = _table(pool, table)
+    _check(_lib.qg_kv_trim(pool._ref, at, ld, rows, pages, _ints(pool, "lens", lens, rows),
+                           _ints(pool, "refs", refs, pool.num_pages), _ints(pool, "to", to, rows),
+                           _stream_now(pool._index)), "qg_kv_trim")
+
+
+ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "turns": 3, "parts": 4}
+
+
+def rope_freqs(rotary_dim: int, base: float = 10000.0, kind: str = "plain", scale: float = 1.0, context: float = 0.0,
+               low: float = 1.0, high: float = 32.0) -> np.ndarray:
+    """Radians a token of each rotated pair (fp64 [rotary_dim / 2], on the host). kind scales them for
+    contexts longer than the trained one: "linear" divides all by scale, "base" raises the base,
+    "turns" and "parts" slow the pairs that turn less than `low` times in the trained `context` tokens and
+    keep those of over `high` turns (include/qgemv.h has the formulas)."""
+    out = np.empty(max(0, rotary_dim // 2), dtype=np.float64)
+    _check(_lib.qg_rope_freqs(ROPE_KINDS[kind], rotary_dim, base, scale, context, low, high, _ptr(out)), "qg_rope_freqs")
+    return out
+
+
+class Rotary:
+    """What kv_append_rope and qk_rope do to a head of head_dim elements: the norm, if there are
+    weights (fp16 [head_dim]), then the rotation of its first 2 * len(freqs) elements by position * freqs
+    (fp64, radians a token: an array such as rope_freqs gives, copied to `device`, or a tensor there;
+    None: no rotation). interleaved: pairs are neighbours instead of halves apart. factor scales the
+    rotated elements. Keeps its tensors alive."""
+
+    def __init__(self, head_dim: int, freqs=None, interleaved: bool = False, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 factor: float = 1.0, device="cuda"):
+        torch = _torch()
+        if freqs is not None and not isinstance(freqs, torch.Tensor):
+            freqs = torch.from_numpy(np.ascontiguousarray(freqs, dtype=np.float64)).to(device)
+        if freqs is not None and (freqs.dtype != torch.float64 or freqs.dim() != 1 or not freqs.is_contiguous()):
+            raise ValueError("freqs must be a dense fp64 vector")
+        held = [t for t in (freqs, q_weight, k_weight) if t is not None]
+        for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if t is not None and (t.dtype != torch.float16 or t.shape != (head_dim,) or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a dense fp16 vector of {head_dim}")
+        if len({t.device for t in held}) > 1 or not all(t.is_cuda for t in held):
+            raise ValueError("freqs and weights must be on one GPU")
+        self.head_dim, self.rotary_dim = head_dim, 0 if freqs is None else 2 * freqs.numel()
+        self.freqs, self.q_weight, self.k_weight = freqs, q_weight, k_weight
+        self._index = held[0].get_device() if held else None
+        address = [None if t is None else t.data_ptr() for t in (freqs, q_weight, k_weight)]
+        self._c = _Rotary(*address, eps, factor, self.rotary_dim, bool(interleaved))
+        self._ref = ctypes.addressof(self._c)
+
+
+class _Where:
+    """What a pool says of its place, for calls without one."""
+    __slots__ = ("device", "_index")
+
+    def __init__(self, t):
+        self.device, self._index = t.device, t.get_device()
+
+
+def _head_rows(index, what: str, t, count: int, head_dim: int):
+    """(address, leading dimension, heads) of fp16 rows [count, heads * head_dim], or [count, heads, head_dim]
+    with dense heads."""
+    shape, ok = t.shape, t.dtype is _th.float16 and t.get_device() == index and t.dim() in (2, 3) and t.shape[0] == count
+    if ok and t.dim() == 3:
+        ok = shape[2] == head_dim and (t.is_contiguous() or (t.stride(2) == 1 and (shape[1] < 2 or t.stride(1) == head_dim)))
+        heads = shape[1]
+    elif ok:
+        ok = shape[1] % head_dim == 0 and (t.is_contiguous() or t.stride(1) == 1)
+        heads = shape[1] // head_dim
+    if not ok:
+        raise ValueError(f"{what} must be fp16 [{count}, heads * {head_dim}] or [{count}, heads, {head_dim}] with dense rows "
+                         f"on cuda:{index}")
+    return t.data_ptr(), t.stride(0), heads
+
+
+def qk_rope(rotary, q, k, positions, q_out=None, k_out=None, stream=None):
+    """Norm and rotate queries and keys: fp16 [count, heads * head_dim] (or [count, heads, head_dim]) with any
+    row stride, row i at positions[i] (int32 on the device; below 0: the row of the output stays as it
+    is). Returns (q_out, k_out), dense where they are allocated here; q and k themselves may be given. k may be
+    None (then so is k_out)."""
+    if not q.is_cuda:
+        raise ValueError("q must be on a GPU")
+    where = _Where(q)
+    index = where._index
+    if stream is not None or _device_now() != index:
+        with _on(where, stream):
+            return qk_rope(rotary, q, k, positions, q_out, k_out)
+    if rotary._index not in (None, index):
+        raise ValueError(f"the rotary's tensors are on cuda:{rotary._index}, q on {q.device}")
+    count, dim = q.shape[0], rotary.head_dim
+    at, ld, heads = _head_rows(index, "q", q, count, dim)
+    kat, ldk, kv_heads = (None, 0, 0) if k is None else _head_rows(index, "k", k, count, dim)
+    q_out = q.new_empty(q.shape) if q_out is None else q_out
+    to, ldo, out_heads = _head_rows(index, "q_out", q_out, count, dim)
+    kto, ldko, k_out_heads = None, 0, 0
+    if k is not None:
+        k_out = k.new_empty(k.shape) if k_out is None else k_out
+        kto, ldko, k_out_heads = _head_rows(index, "k_out", k_out, count, dim)
+    if out_heads != heads or k_out_heads != kv_heads:
+        raise ValueError("outputs must have their inputs' heads")
+    _check(_lib.qg_qk_rope(rotary._ref, dim, heads, kv_heads, at, ld, kat, ldk, _ints(where, "positions", positions, count), count,
+                           to, ldo, kto, ldko, _stream_now(index)), "qg_qk_rope")
+    return q_out, k_out
+
+
+def kv_append_rope(pool, table, rotary, q, k, v, positions, seqs=None, q_out=None, layer: int = 0, stream=None):
+    """qk_rope and kv_append in one pass: the normed and rotated queries are returned (q_out, dense where it
+    is allocated here; q itself may be given), the keys and v go into the cache as token positions[i] of table
+    row seqs[i] (row i when seqs is None). q: fp16 [count, heads * head_dim] or [count, heads, head_dim],
+    or None; k, v: fp16 [count, kv_heads * head_dim]; any row strides. A row with position -1 is
+    skipped, its row of q_out stays as it is; one without a page gives its queries only."""
+    if stream is not None or _device_now() != pool._index:
+        with _on(pool, stream):
+            return kv_append_rope(pool, table, rotary, q, k, v, positions, seqs, q_out, layer)
+    if rotary._index not in (None, pool._index) or rotary.head_dim != pool.head_dim:
+        raise ValueError(f"the rotary must be for heads of {pool.head_dim}, its tensors on {pool.device}")
+    count, dim = positions.numel(), pool.head_dim
+    at, ld, heads, to, ldo = None, 0, 0, None, 0
+    if q is not None:
+        at, ld, heads = _head_rows(pool._index, "q", q, count, dim)
+        q_out = q.new_empty(q.shape) if q_out is None else q_out
+        to, ldo, out_heads = _head_rows(pool._index, "q_out", q_out, count, dim)
+        if out_heads != heads:
+            raise ValueError("q_out must have q's heads")
+    _check(_lib.qg_kv_append_rope(pool._ref, layer, *_table(pool, table), rotary._ref, heads, at, ld,
+                                  *_rows16(pool, "k", k, count), *_rows16(pool, "v", v, count),
+                                  None if seqs is None else _ints(pool, "seqs", seqs, count),
+                                  _ints(pool, "positions", positions), count, to, ldo, _stream_now(pool._index)),
+           "qg_kv_append_rope")
+    return q_out
 
 
 def dequantize(fmt, w, n: int, k: int, values: bool = True, codes: bool = True, stream=None):

@@ -700,7 +700,7 @@ const char *qg_strerror(int status) {
     case QG_ERR_SHAPE: return "n, k or m out of range (k must be a multiple of 256 for the super-block formats, of 32 for q4g32, 64 for q4g16, q4g64, q4a32, q4g32h, q3g32 and q5g32, 128 for q4g128)";
     case QG_ERR_ALIGN: return "misaligned device pointer or leading dimension";
     case QG_ERR_NONFINITE: return "a weight is NaN or infinite";
-    case QG_ERR_RANGE: return "a super-block scale does not fit fp16 (or bf16), or an fp16 group scale overflows, or a code does not fit its width";
+    case QG_ERR_RANGE: return "a super-block scale does not fit fp16 (or bf16), or an fp16 group scale overflows, or a code does not fit its width, or a scale, factor or epsilon is out of range";
     case QG_ERR_FORMAT: return "unknown format or bit width";
     case QG_ERR_LAUNCH: return "the HIP runtime refused a kernel launch";
     case QG_ERR_DEVICE: return "no usable gfx950 device or HIP runtime error";
@@ -714,6 +714,32 @@ int qg_kv_page_bytes(int kind, int64_t kv_heads, int64_t head_dim, int64_t page_
   KvLayout L;
   if (int st = kv_layout(kind, kv_heads, head_dim, page_tokens, &L)) return st;
   *bytes = L.page_bytes;
+  return QG_OK;
+}
+
+int qg_rope_freqs(int kind, int64_t rotary_dim, double base, double scale, double context, double low, double high,
+                  double *freqs) {
+  if (!freqs) return QG_ERR_NULL;
+  if (kind < QG_ROPE_PLAIN || kind > QG_ROPE_PARTS) return QG_ERR_FORMAT;
+  if (rotary_dim < 2 || rotary_dim % 2 || (kind == QG_ROPE_BASE && rotary_dim < 4)) return QG_ERR_SHAPE;
+  const bool bands = kind == QG_ROPE_TURNS || kind == QG_ROPE_PARTS;
+  if (!(std::isfinite(base) && base > 1)) return QG_ERR_RANGE;
+  if (kind != QG_ROPE_PLAIN && !(std::isfinite(scale) && scale > 0)) return QG_ERR_RANGE;
+  if (bands && !(std::isfinite(context) && context > 0 && std::isfinite(high) && low > 0 && low < high)) return QG_ERR_RANGE;
+  const double r = (double)rotary_dim, turn = 2 * 3.14159265358979323846;
+  if (kind == QG_ROPE_BASE) base *= std::pow(scale, r / (r - 2));
+  // the pair, as a real number, that makes t turns in the context
+  const auto pair = [&](double t) { return r * std::log(context / (t * turn)) / (2 * std::log(base)); };
+  const double a = bands ? std::max(std::floor(pair(high)), 0.0) : 0, b = bands ? std::min(std::ceil(pair(low)), r - 1) : 0;
+  for (int64_t j = 0; j < rotary_dim / 2; ++j) {
+    const double f = std::pow(base, -2.0 * (double)j / r);
+    double g = 1;                                            // the part that keeps its frequency
+    if (kind == QG_ROPE_LINEAR) g = 0;
+    if (kind == QG_ROPE_TURNS) g = (context * f / turn - low) / (high - low);
+    if (kind == QG_ROPE_PARTS) g = 1 - ((double)j - a) / std::max(b - a, 0.001);
+    g = std::min(std::max(g, 0.0), 1.0);
+    freqs[j] = g == 1 ? f : f * (g + (1 - g) / scale);
+  }
   return QG_OK;
 }
 

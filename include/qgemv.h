@@ -501,6 +501,96 @@ int qg_kv_compact(const qg_kv_pool *pool, const int32_t *table, int64_t ld_table
                   int64_t table_rows, int64_t table_pages, const int32_t *refs, int32_t *refs_out, int32_t *remap,
                   int32_t *live, void *workspace, int64_t workspace_bytes, void *stream);
 
+/* Extend: places for a step's new tokens. Row r of the table asks for add[r] tokens (int32 [table_rows] on the
+ * device; 0 or less: none) after its lens[r], and for the pages that it lacks for them. With N_r the tokens asked
+ * by rows 0 to r, its tokens are the places N_(r-1) to N_r - 1 of the slot map seqs, positions (int32
+ * [slots]), whether it gets them or not: the order in which the caller's batch holds them. A row is served
+ * unless
+ *   N_r exceeds slots, or lens[r] + add[r] the row's table_pages * T tokens, or
+ *   its last page is partly filled and not held by this row alone (refs 1): appending would write into
+ *     another row's tokens (qg_kv_fork copies such a page), or
+ *   it lacks pages and these, with those lacked by the rows before it that none of this refuses, are more
+ *     than there are free pages (refs 0 or less).
+ * A served row's new entries name free pages, in ascending order over all rows, whose refs become 1; lens[r] grows
+ * by add[r], granted[r] (int32 [table_rows]) is add[r], and slot i of its tokens holds seqs r and
+ * positions the token's place in the row: what qg_kv_append takes. A row that is not served stays as it was,
+ * granted is 0, its slots hold -1 and -1, and so do the slots past the last row's. starts (int32 [table_rows + 1], or
+ * NULL) receives N_(r-1) at r, at most slots. The entries past a row's pages are overwritten whatever they
+ * hold (-1 by convention).
+ * workspace (4-byte aligned): at least qg_kv_extend_bytes, as for qg_paged_attention. add, granted, starts, the
+ * slot map and the workspace overlap nothing else. table_rows is at most 65536, num_pages 2^24, slots
+ * 2^26 here. Errors: also QG_ERR_WORKSPACE. */
+int qg_kv_extend_bytes(const qg_kv_pool *pool, int64_t table_rows, int64_t *bytes);
+int qg_kv_extend(const qg_kv_pool *pool, int32_t *table, int64_t ld_table, int64_t table_rows, int64_t table_pages,
+                 int32_t *lens, int32_t *refs, const int32_t *add, int32_t *granted, int32_t *starts, int32_t *seqs,
+                 int32_t *positions, int64_t slots, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Trim, the way back: a row r with 0 <= to[r] < lens[r] (int32 [table_rows] on the device) keeps its first to[r]
+ * tokens; its entries past their pages give up their page (refs - 1) and become -1. Other rows stay as they
+ * are. A last page that is then partly filled and held by other rows too is not copied (qg_kv_extend refuses to
+ * add to it). table_rows is at most 65536. */
+int qg_kv_trim(const qg_kv_pool *pool, int32_t *table, int64_t ld_table, int64_t table_rows, int64_t table_pages,
+               int32_t *lens, int32_t *refs, const int32_t *to, void *stream);
+
+/* ---- norm and rotation of queries and keys ---------------------------------------------------
+ * Between the projections and the attention, a head x of D = head_dim elements becomes
+ *   y = x / sqrt(mean(x^2) + eps) * w     with q_weight for queries and k_weight for keys (fp16 [D],
+ *                                         16-byte aligned), or y = x where that is NULL; then
+ *   (y_i, y_k) -> factor * (y_i cos t - y_k sin t, y_k cos t + y_i sin t),  t = position * freqs[j]
+ * for the pairs j < rotary_dim / 2: (i, k) = (j, j + rotary_dim / 2), or (2 j, 2 j + 1) with interleaved
+ * != 0. Elements from rotary_dim on are not rotated. freqs, fp64 [rotary_dim / 2] on the device (8-byte
+ * aligned), are radians a token: qg_rope_freqs makes them, scaled for long contexts if need be, and factor (1 where
+ * nothing is to be changed) is the factor of the attention's logits that goes with some scalings. The angle
+ * is fp64 and right at any position, the rest fp32 with one rounding to fp16. rotary_dim is a multiple of 16,
+ * at most head_dim; head_dim is 64, 128 or 256; eps is at least the smallest normal fp32 (read where there is
+ * a weight), factor finite, else QG_ERR_RANGE. */
+typedef struct qg_rotary {
+  const double *freqs;
+  const uint16_t *q_weight;
+  const uint16_t *k_weight;
+  float eps;
+  float factor;
+  int32_t rotary_dim;
+  int32_t interleaved;
+} qg_rotary;
+
+/* Frequencies (host): freqs[j], j < rotary_dim / 2, for the given base (10000 by habit), with f_j = base^(-2 j /
+ * rotary_dim) and t_j = context * f_j / (2 pi), the turns of pair j in the `context` tokens of training:
+ *   QG_ROPE_PLAIN   f_j
+ *   QG_ROPE_LINEAR  f_j / scale: all positions closer together
+ *   QG_ROPE_BASE    f_j of the base base * scale^(rotary_dim / (rotary_dim - 2)): the slowest pair
+ *                   `scale` times slower, the fastest as it was
+ *   QG_ROPE_TURNS   f_j (g + (1 - g) / scale), g = clamp((t_j - low) / (high - low), 0, 1): pairs of less than
+ *                   `low` turns in training slowed, of more than `high` as they were
+ *   QG_ROPE_PARTS   the same with 1 - g = clamp((j - a) / (b - a), 0, 1), a and b the pairs (as real numbers, rounded
+ *                   down and up, at least 0 and at most rotary_dim - 1) that make `high` and `low` turns; b - a at least 0.001
+ * scale is read by all but QG_ROPE_PLAIN, context, low and high by the last two; base > 1, scale > 0, context > 0 and
+ * 0 < low < high, all finite, else QG_ERR_RANGE. rotary_dim is a positive even number, above 2 for QG_ROPE_BASE.
+ * Errors: QG_ERR_NULL, QG_ERR_FORMAT (kind), QG_ERR_SHAPE, QG_ERR_RANGE. */
+typedef enum qg_rope_kind { QG_ROPE_PLAIN = 0, QG_ROPE_LINEAR = 1, QG_ROPE_BASE = 2, QG_ROPE_TURNS = 3, QG_ROPE_PARTS = 4 } qg_rope_kind;
+int qg_rope_freqs(int kind, int64_t rotary_dim, double base, double scale, double context, double low, double high,
+                  double *freqs);
+
+/* Queries [count][heads * head_dim] and keys [count][kv_heads * head_dim] (fp16, rows at q + i * ldq and k + i *
+ * ldk) into q_out and k_out, row i at positions[i] (int32 [count] on the device). A row with a position below 0
+ * is skipped: its output stays as it was. q_out may be q with the same leading dimension, and k_out k; else outputs
+ * overlap nothing that the call reads. All rows 16-byte aligned, leading dimensions multiples of 8 and at least
+ * the row's elements when count > 1. heads or kv_heads may be 0 (its pointers are not read then); both are at
+ * most 65536, count is at most 2^23. Errors: QG_ERR_NULL, QG_ERR_SHAPE, QG_ERR_ALIGN, QG_ERR_RANGE, QG_ERR_LAUNCH. */
+int qg_qk_rope(const qg_rotary *rotary, int64_t head_dim, int64_t heads, int64_t kv_heads, const uint16_t *q, int64_t ldq,
+               const uint16_t *k, int64_t ldk, const int32_t *positions, int64_t count, uint16_t *q_out, int64_t ld_q_out,
+               uint16_t *k_out, int64_t ld_k_out, void *stream);
+
+/* qg_qk_rope and qg_kv_append in one pass: the queries into q_out, the keys (rounded to fp16) and the values v into
+ * `layer` of the pool, the same bytes as by the two calls. A row with a position below 0 is skipped, one whose
+ * place is no page (see qg_kv_append) gives its queries only. What is cached, rotated keys among it, is finite.
+ * heads may be 0. q_out may be q as above, and overlaps nothing else that the call reads. Sizes and alignment of
+ * qg_qk_rope for q and q_out, of qg_kv_append for k and v; errors of both. */
+int qg_kv_append_rope(const qg_kv_pool *pool, int64_t layer, const int32_t *table, int64_t ld_table, int64_t table_rows,
+                      int64_t table_pages, const qg_rotary *rotary, int64_t heads, const uint16_t *q, int64_t ldq,
+                      const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int32_t *seqs,
+                      const int32_t *positions, int64_t count, uint16_t *q_out, int64_t ld_q_out, void *stream);
+
 /* ---- decode to memory (device; for verification, not for inference) ----------------------
  * Writes W_hat as fp32 [n][k] to w_out (if non-NULL) and the integer codes as uint8 [n][k]
  * to codes_out (if non-NULL; q4g32 writes the unsigned nibble u = q + 8, q4a32 the code c).
