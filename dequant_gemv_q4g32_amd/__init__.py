@@ -116,6 +116,9 @@ def _load() -> ctypes.CDLL:
         "qg_kv_free": ([vp, vp, i64, i64, i64, vp, vp, vp, i64, vp], i32),
         "qg_kv_compact_bytes": ([vp, ctypes.POINTER(i64)], i32),
         "qg_kv_compact": ([vp, vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp], i32),
+        "qg_prefix_attention_bytes": ([vp, i64, i64, i64, i64, i64, ctypes.POINTER(i64)], i32),
+        "qg_prefix_attention": ([vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, i64, i64, i64, i64, ctypes.c_float, vp, i64, i32,
+                                 vp, vp, i64, vp], i32),
         "qg_kv_extend_bytes": ([vp, i64, ctypes.POINTER(i64)], i32),
         "qg_kv_extend": ([vp, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp], i32),
         "qg_kv_trim": ([vp, vp, i64, i64, i64, vp, vp, vp, vp], i32),
@@ -392,6 +395,7 @@ class KVPool:
         self._ref = ctypes.addressof(self._c)
         # workspace sizes, kept by the sizes they follow from: asking the library takes 1 us of a call's 15
         self._attention_bytes = functools.lru_cache(256)(functools.partial(_workspace, "qg_paged_attention_bytes", self._c))
+        self._prefix_bytes = functools.lru_cache(256)(functools.partial(_workspace, "qg_prefix_attention_bytes", self._c))
         self._extend_bytes = functools.lru_cache(256)(functools.partial(_workspace, "qg_kv_extend_bytes", self._c))
         self._compact_bytes = functools.lru_cache(1)(functools.partial(_workspace, "qg_kv_compact_bytes", self._c))
 
@@ -488,20 +492,8 @@ def paged_attention_bytes(pool, batch: int, heads: int, max_len: int) -> int:
     return pool._attention_bytes(batch, heads, max_len)
 
 
-def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: Optional[float] = None, window: int = 0,
-                    out=None, out_f32: bool = False, lse=None, return_lse: bool = False, workspace=None, layer: int = 0,
-                    stream=None):
-    """Attention of one new token a sequence over its cached tokens. q: fp16 [batch, heads, head_dim]
-    (row stride q.stride(0), heads dense); table: int32 [batch, pages]; lens: int32 [batch], each
-    sequence's tokens, the new one's K and V (kv_append) among them. max_len bounds lens (default:
-    what the table holds); scale defaults to head_dim ** -0.5; window > 0 sees the last `window`
-    tokens only. Returns out [batch, heads, head_dim] (fp16, or fp32 with out_f32), or (out, lse)
-    with return_lse or when lse (fp32 [batch, heads]) is given. A sequence without tokens gets zeros and
-    lse -inf. workspace: uint8 of paged_attention_bytes(...), used by one call at a time; allocated
-    here when None. out, lse and workspace overlap nothing that the call reads, q among it."""
-    if stream is not None or _device_now() != pool._index:
-        with _on(pool, stream):
-            return paged_attention(pool, q, table, lens, max_len, scale, window, out, out_f32, lse, return_lse, workspace, layer)
+def _attention_args(pool, q, table, max_len, scale, out, out_f32, lse, return_lse):
+    """What the attentions over the cache take in common, checked, with its defaults and outputs."""
     if q.dtype is not _th.float16 or q.get_device() != pool._index or q.dim() != 3:
         raise ValueError(f"q must be fp16 [batch, heads, head_dim] on {pool.device}")
     shape = batch, heads, dim = q.shape
@@ -524,6 +516,24 @@ def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: 
             raise ValueError(f"lse must be dense fp32 [{batch}, {heads}] on {pool.device}")
     elif return_lse:
         lse = q.new_empty((batch, heads), dtype=_th.float32)
+    return batch, heads, at, ld, max_len, scale, out, lse
+
+
+def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: Optional[float] = None, window: int = 0,
+                    out=None, out_f32: bool = False, lse=None, return_lse: bool = False, workspace=None, layer: int = 0,
+                    stream=None):
+    """Attention of one new token a sequence over its cached tokens. q: fp16 [batch, heads, head_dim]
+    (row stride q.stride(0), heads dense); table: int32 [batch, pages]; lens: int32 [batch], each
+    sequence's tokens, the new one's K and V (kv_append) among them. max_len bounds lens (default:
+    what the table holds); scale defaults to head_dim ** -0.5; window > 0 sees the last `window`
+    tokens only. Returns out [batch, heads, head_dim] (fp16, or fp32 with out_f32), or (out, lse)
+    with return_lse or when lse (fp32 [batch, heads]) is given. A sequence without tokens gets zeros and
+    lse -inf. workspace: uint8 of paged_attention_bytes(...), used by one call at a time; allocated
+    here when None. out, lse and workspace overlap nothing that the call reads, q among it."""
+    if stream is not None or _device_now() != pool._index:
+        with _on(pool, stream):
+            return paged_attention(pool, q, table, lens, max_len, scale, window, out, out_f32, lse, return_lse, workspace, layer)
+    batch, heads, at, ld, max_len, scale, out, lse = _attention_args(pool, q, table, max_len, scale, out, out_f32, lse, return_lse)
     if workspace is None:
         need = pool._attention_bytes(batch, heads, max_len)
         workspace = q.new_empty(need, dtype=_th.uint8) if need else None
@@ -534,6 +544,41 @@ def paged_attention(pool, q, table, lens, max_len: Optional[int] = None, scale: 
                                    out.dtype is _th.float32, None if lse is None else lse.data_ptr(),
                                    *((None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())),
                                    _stream_now(pool._index)), "qg_paged_attention")
+    return out if lse is None else (out, lse)
+
+
+def prefix_attention_bytes(pool, batch: int, heads: int, groups: int, max_len: int, max_tail: int) -> int:
+    """Workspace bytes of prefix_attention for these sizes."""
+    return pool._prefix_bytes(batch, heads, groups, max_len, max_tail)
+
+
+def prefix_attention(pool, q, table, lens, starts, prefix, max_len: Optional[int] = None, max_tail: Optional[int] = None,
+                     scale: Optional[float] = None, out=None, out_f32: bool = False, lse=None, return_lse: bool = False,
+                     workspace=None, layer: int = 0, stream=None):
+    """paged_attention of rows that share their first tokens in groups (forks of one prompt, say): the
+    shared tokens are read and multiplied once a group. Group g is the rows starts[g] to starts[g + 1] - 1
+    (int32 [groups + 1], ascending); the first prefix[g] tokens (int32 [groups]) of its rows are the same and are
+    read through the table's row starts[g]. Rows in no group, and what follows a prefix, are read as by
+    paged_attention. max_tail bounds the tokens that a row does not share (default: max_len); more of them are slower,
+    no less right. The other arguments and the results are paged_attention's, without a window; fp16 results
+    carry one more rounding of the shared tokens' weights to fp16."""
+    if stream is not None or _device_now() != pool._index:
+        with _on(pool, stream):
+            return prefix_attention(pool, q, table, lens, starts, prefix, max_len, max_tail, scale, out, out_f32, lse, return_lse,
+                                    workspace, layer)
+    batch, heads, at, ld, max_len, scale, out, lse = _attention_args(pool, q, table, max_len, scale, out, out_f32, lse, return_lse)
+    groups = prefix.numel()
+    if max_tail is None:
+        max_tail = max_len
+    if workspace is None:
+        workspace = q.new_empty(pool._prefix_bytes(batch, heads, groups, max_len, max_tail), dtype=_th.uint8)
+    elif workspace.dtype != _th.uint8 or workspace.device != pool.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be dense uint8 on {pool.device}")
+    _check(_lib.qg_prefix_attention(pool._ref, layer, q.data_ptr(), q.stride(0), at, ld, _ints(pool, "lens", lens, batch),
+                                    _ints(pool, "starts", starts, groups + 1), _ints(pool, "prefix", prefix), groups, batch, heads,
+                                    max_len, max_tail, scale, out.data_ptr(), out.stride(0), out.dtype is _th.float32,
+                                    None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                    _stream_now(pool._index)), "qg_prefix_attention")
     return out if lse is None else (out, lse)
 
 

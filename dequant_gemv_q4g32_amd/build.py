@@ -26,7 +26,7 @@ LIB = os.path.join(PKG, "libqgemv.so")
 
 HOST_SOURCES = ["host.cpp"]
 DEVICE_SOURCES = ["gemv.hip", "prefill.hip", "skinny.hip", "kvcache.hip", "paged_kv.hip", "paged_attn.hip",
-                  "paged_extend.hip", "rope.hip"] + sorted(
+                  "paged_extend.hip", "rope.hip", "prefix_attn.hip"] + sorted(
     f for f in os.listdir(CSRC) if f.startswith("mv_") and f.endswith(".hip"))   # streaming launchers per format
 ARCH = "gfx950"
 

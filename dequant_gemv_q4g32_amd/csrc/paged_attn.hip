@@ -29,6 +29,7 @@
 #include <cmath>
 
 #include "../../include/qgemv.h"
+#include "attn_common.h"
 #include "device_common.h"
 #include "kv_pages.h"
 #include "launch.h"
@@ -45,6 +46,7 @@ struct AttnArgs {
   const int32_t *table;
   int64_t ld_table;
   const int32_t *lens;
+  const int32_t *from;           // tokens before from[b] of sequence b are not seen (NULL: all are)
   int32_t batch, heads, group;   // group = heads / kv_heads
   int32_t tile_heads;            // heads of a head tile: 16, or 32 where a KV head has more than 16
   int32_t tiles_per_kv, head_tiles;   // head tiles of a KV head, and of all of them
@@ -53,38 +55,19 @@ struct AttnArgs {
   float scale_log2;              // scale * log2(e)
   void *out;
   int64_t ldo;
-  int32_t out_f32;
+  int32_t out_f32;               // 0: fp16, 1: fp32, kRaw: the sums themselves in fp32, and (reference, denominator) pairs in lse
   float *lse;
   uint32_t *starts;              // workspace: where each sequence starts on the line, and its end;
   const int32_t *starts_in;      // the same for reading
   float *slots;                  // workspace: two parts a wave
 };
 
-typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
-typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
 constexpr int kWaves = 4;                          // waves of a workgroup
 constexpr int kTile = 32;                          // tokens of a wave's step, the grain of the split
 constexpr int kThreads = 64 * kWaves;
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-// Weights are 2^(s - ref) with ref moved to (largest s) - 7 once s - ref passes 15: they stay below
-// fp16's 65504 and small ones lose nothing above 2^-31 of the largest, while most steps find ref good
-// as it is. The difference itself is compared, as the weights use it: ref + 15 rounds up to ref + 16
-// for scores of 2^24 to 2^28.
-constexpr float kLow = 7.0f, kHigh = 15.0f;
+constexpr int32_t kRaw = 2;
 
-template <typename T>
-__device__ __forceinline__ T uniform(T v) { return __builtin_amdgcn_readfirstlane(v); }
-
-// Read-only memory at a uniform address, through the scalar cache.
-__device__ __forceinline__ int32_t scalar_load(const int32_t *p) {
-  return *(const __attribute__((address_space(4))) int32_t *)(uintptr_t)p;
-}
-
-// What of sequence b is seen: tokens [first, len), in tiles from base = first rounded down.
+// What of a sequence is seen: tokens [first, len), in tiles from base = first rounded down.
 // On the line (below) a head tile of few tiles counts one unit more: its start costs a wave about as
 // much as half a tile, which a wave with many short sequences would be late by (32 sequences of up to
 // 8192 tokens, some of none or one: 56 us without the unit, 51 with it).
@@ -94,16 +77,18 @@ struct Seen {
 };
 constexpr int32_t kShort = 16;                       // tiles below which a head tile has that unit
 template <bool WHOLE>
-__device__ __forceinline__ Seen seen_of(const AttnArgs &a, int32_t raw) {
+__device__ __forceinline__ Seen seen_of(const AttnArgs &a, int32_t raw, int32_t from) {
   Seen s;
   s.len = min(max(raw, 0), a.max_len);
-  s.first = a.window ? max(0, s.len - a.window) : 0;
+  s.first = a.window ? max(0, s.len - a.window) : min(from, s.len);
   s.base = s.first & ~(kTile - 1);
   s.tiles = max(1, (s.len - s.base + kTile - 1) / kTile);      // an empty sequence still gets its zeros written
   s.lead = !WHOLE && s.tiles < kShort ? 1 : 0;
   s.units = (uint32_t)s.tiles + s.lead;
   return s;
 }
+
+__device__ __forceinline__ int32_t from_of(const AttnArgs &a, int32_t b) { return a.from ? scalar_load(a.from + b) : 0; }
 
 // The split. The units of all sequences and head tiles, sequence by sequence and head tile by head
 // tile, are one line of `total` units (below 2^31), of which wave v of `waves` takes the v-th part:
@@ -114,35 +99,6 @@ __device__ __forceinline__ Seen seen_of(const AttnArgs &a, int32_t raw) {
 // parts of a head tile are: one for each workgroup with such waves (named by the first of them,
 // the leader), and one for a wave that goes on past u1. A workgroup for each head tile instead would
 // put one long sequence on as many CUs as it has KV heads, and wait for the longest of ragged ones.
-struct Line {
-  uint32_t total, waves, quota, extra, first;
-  __device__ __forceinline__ uint32_t start(uint32_t v) const { return first + v * quota + min(v, extra); }
-  // the wave that holds unit u
-  __device__ __forceinline__ uint32_t holder(uint32_t u) const {
-    const uint32_t big = extra * (quota + 1);
-    return u < big ? u / (quota + 1) : extra + (u - big) / quota;
-  }
-};
-__device__ __forceinline__ Line make_line(uint32_t total, uint32_t waves) {
-  Line l;
-  l.total = total;
-  l.first = 0;
-  l.waves = min(total, waves);
-  l.quota = total / l.waves;
-  l.extra = total - l.quota * l.waves;
-  return l;
-}
-
-// Sum of `v` over this lane and those before it: within rows of 16, then over the rows.
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
-  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false);   // row_shr:1
-  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false);   // row_shr:2
-  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false);   // row_shr:4
-  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false);   // row_shr:8
-  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);   // row_bcast:15
-  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);   // row_bcast:31
-  return v;
-}
 
 // Sum of `v` over the threads before this one; total: over all. lds: a value for each wave.
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *lds, uint32_t &total) {
@@ -158,17 +114,6 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *lds, uint32
   total = uniform(all);
   return before + scan - v;
 }
-
-// 16 codes of one group to 16 fp16 values: code + 128 under the exponent of 1024 (a byte permute
-// and an exact subtraction for two), times the scale, rounded to fp16 as qg_kv_dequantize does.
-// MODE.FP16_OVFL (set at the start of the kernel) saturates the product at +-65504: without it the
-// one scale that can pass it (516) would need two more operations for every pair.
-__device__ __forceinline__ uint32_t scaled_pair(uint32_t magic_pair, uint32_t scale) {
-  const h2_t off = __builtin_bit_cast(h2_t, 0x64806480u);       // 1152 = 1024 + 128
-  return __builtin_bit_cast(uint32_t, (__builtin_bit_cast(h2_t, magic_pair) - off) * __builtin_bit_cast(h2_t, scale));
-}
-constexpr uint32_t kMagicBytes = 0x64646464u;
-constexpr uint32_t kSelLow = 0x04010400u, kSelHigh = 0x04030402u;   // bytes 0, 1 and 2, 3 of the second operand under 0x64
 
 template <int D, bool Q8>
 struct Tile {
@@ -274,21 +219,6 @@ __device__ __forceinline__ void scores(const Tile<D, Q8> &t, int st, const half8
   }
 }
 
-// Whether the lane's part of q holds a NaN or an infinity. FP16_OVFL makes the matrix units take
-// either as a finite number, so with int8 pages such a head is marked instead: its scores are
-// infinite or NaN against any finite K, and its softmax is NaN as soon as it sees a token.
-template <int KD>
-__device__ __forceinline__ bool nonfinite(const half8_t *q) {
-  uint32_t bad = 0;
-#pragma unroll
-  for (int i = 0; i < KD; ++i) {
-    const u32x4 x = __builtin_bit_cast(u32x4, q[i]);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) bad |= (x[j] & 0x7C007C00u) + 0x04000400u;   // an exponent of ones carries into bit 15
-  }
-  return (bad & 0x80008000u) != 0;
-}
-
 // O^T += V^T P^T with the weights as hi + lo fp16 pairs. Column c of V^T's block j is element
 // VJ * c + j, so O^T's lane holds head c and elements VJ * (4 g + i) + j.
 template <int D, bool Q8, int HT>
@@ -367,11 +297,11 @@ template <bool WHOLE>
 __device__ __forceinline__ Segment segment_at(const AttnArgs &a, uint32_t at, uint32_t end, int32_t b, uint32_t seq_at,
                                               int32_t len) {
   Segment g;
-  Seen s = seen_of<WHOLE>(a, len);
+  Seen s = seen_of<WHOLE>(a, len, from_of(a, b));
   while (at - seq_at >= s.units * a.head_tiles) {
     seq_at += s.units * a.head_tiles;
     ++b;
-    s = seen_of<WHOLE>(a, scalar_load(a.lens + b));
+    s = seen_of<WHOLE>(a, scalar_load(a.lens + b), from_of(a, b));
   }
   g.ht = (int32_t)((at - seq_at) / s.units);
   g.u0 = seq_at + (uint32_t)g.ht * s.units;
@@ -403,6 +333,11 @@ __device__ __forceinline__ void store_result(const AttnArgs &a, int32_t b, int32
   }
   const int32_t h = h0 + r;
   const int64_t at = b * a.ldo + (int64_t)h * D + d;
+  if (a.out_f32 == kRaw) {
+    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = o;
+    if (d == 0) *reinterpret_cast<f32x2 *>(a.lse + 2 * ((int64_t)b * a.heads + h)) = f32x2{m, l};
+    return;
+  }
   const float inv = l > 0.f ? 1.0f / l : l;          // no token: 0; NaN sums stay NaN
   o *= inv;
   if (a.out_f32) {
@@ -437,7 +372,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? (HT == 1 ? 4 : 3) : D == 128 ? 
   if constexpr (WHOLE) {
     from_b = blockIdx.x / a.head_tiles;
     from_len = scalar_load(a.lens + from_b);
-    const uint32_t tiles = seen_of<true>(a, from_len).units;
+    const uint32_t tiles = seen_of<true>(a, from_len, from_of(a, (int32_t)from_b)).units;
     line = make_line(tiles, blockDim.x / 64);
     line.first = (blockIdx.x - from_b * a.head_tiles) * tiles;
     from_at = 0;
@@ -453,7 +388,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? (HT == 1 ? 4 : 3) : D == 128 ? 
       if (my_b + i < a.batch) {
         const int32_t len = a.lens[my_b + i];
         if (i == 0) my_len = len;
-        mine += seen_of<false>(a, len).units * a.head_tiles;
+        mine += seen_of<false>(a, len, a.from ? a.from[my_b + i] : 0).units * a.head_tiles;
       }
     uint32_t total, before;
     if (one) {
@@ -468,7 +403,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? (HT == 1 ? 4 : 3) : D == 128 ? 
       for (int32_t i = 0; i < per; ++i)
         if (my_b + i < a.batch) {
           a.starts[my_b + i] = at;
-          at += seen_of<false>(a, a.lens[my_b + i]).units * a.head_tiles;
+          at += seen_of<false>(a, a.lens[my_b + i], a.from ? a.from[my_b + i] : 0).units * a.head_tiles;
         }
       if (threadIdx.x == 0) a.starts[a.batch] = total;
     }
@@ -728,7 +663,7 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(AttnArgs a, uint32_t
   __shared__ f32x4 sums[kSplit][kLanes];
   const int32_t b = blockIdx.x / a.head_tiles, ht = blockIdx.x - b * a.head_tiles;
   const Line line = make_line((uint32_t)scalar_load(a.starts_in + a.batch), waves);
-  const Seen s = seen_of<false>(a, scalar_load(a.lens + b));
+  const Seen s = seen_of<false>(a, scalar_load(a.lens + b), from_of(a, b));
   const uint32_t u0 = (uint32_t)scalar_load(a.starts_in + b) + (uint32_t)ht * s.units;
   const uint32_t u1 = u0 + s.units, w0 = line.holder(u0), w1 = line.holder(u1 - 1);
   if (w0 == w1) return;
@@ -880,7 +815,82 @@ int attn_shape(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max
   return QG_OK;
 }
 
+int64_t attn_workspace(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t tiles) {
+  const int64_t group = heads / pool->kv_heads, dim = pool->head_dim;
+  const int64_t tile = attn_tile_heads(group, pool->kv_heads, batch, tiles, dim);
+  // a window only shortens the head tiles: what needs no join without one needs none with one, and
+  // a call that is left with tiles of 16 heads has no more waves than counted here, nor larger parts
+  if (batch == 0 || attn_whole(batch * pool->kv_heads * ((group + tile - 1) / tile), tiles, dim)) return 0;
+  const int64_t slots = 2 * kWaves * attn_grid(batch, (group + 15) / 16 * pool->kv_heads, tiles, dim, 16);
+  return starts_bytes(batch) + 4 * slots * slot_floats((int32_t)(group < tile ? group : tile), (int32_t)dim);
+}
+
+// Launches for checked arguments. likely: the longest sequence's tokens that are seen, as far as the host can
+// say; it chooses the launch's shape only, and the workspace's size follows from it.
+int launch_checked(const qg_kv_pool *pool, const KvLayout &L, int64_t layer, const uint16_t *q, int64_t ldq, const int32_t *table,
+                   int64_t ld_table, const int32_t *lens, const int32_t *from, int64_t batch, int64_t heads, int64_t max_len,
+                   int64_t likely, int64_t window, float scale_log2, void *out, int64_t ldo, int32_t out_f32, float *lse,
+                   void *workspace, void *stream) {
+  AttnArgs a;
+  a.window = (int32_t)(window > max_len ? 0 : window);
+  const int64_t tiles = attn_tiles(likely, a.window), cols = heads * pool->head_dim;
+  a.pool = static_cast<const uint8_t *>(pool->pages) + (layer ? layer * pool->layer_stride : 0);
+  a.page_bytes = L.page_bytes;
+  a.head_bytes = L.head_bytes;
+  a.v_off = L.v_off;
+  a.ks_off = L.ks_off;
+  a.vs_off = L.vs_off;
+  a.num_pages = (int32_t)pool->num_pages;
+  a.tok_shift = __builtin_ctz(pool->page_tokens);
+  a.q = q;
+  a.ldq = batch > 1 ? ldq : cols;
+  a.table = table;
+  a.ld_table = ld_table;
+  a.lens = lens;
+  a.from = from;
+  a.batch = (int32_t)batch;
+  a.heads = (int32_t)heads;
+  a.group = (int32_t)(heads / pool->kv_heads);
+  a.tile_heads = attn_tile_heads(a.group, pool->kv_heads, batch, tiles, pool->head_dim);
+  a.tiles_per_kv = (a.group + a.tile_heads - 1) / a.tile_heads;
+  a.head_tiles = a.tiles_per_kv * pool->kv_heads;
+  a.rows = a.group < a.tile_heads ? a.group : a.tile_heads;
+  a.max_len = (int32_t)max_len;
+  a.scale_log2 = scale_log2;
+  a.out = out;
+  a.ldo = batch > 1 ? ldo : cols;
+  a.out_f32 = out_f32;
+  a.lse = lse;
+  a.starts = static_cast<uint32_t *>(workspace);
+  a.starts_in = static_cast<const int32_t *>(workspace);
+  a.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + starts_bytes(batch));
+  const bool q8 = pool->kind == QG_KV_Q8;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (pool->head_dim) {
+    case 64: return launch_dim<64>(a, tiles, q8, s);
+    case 128: return launch_dim<128>(a, tiles, q8, s);
+    default: return launch_dim<256>(a, tiles, q8, s);
+  }
+}
+
 }  // namespace
+
+int attn_shape_check(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_len) {
+  KvLayout L;
+  return attn_shape(pool, batch, heads, max_len, &L);
+}
+
+int64_t attn_tail_bytes(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_tail) {
+  return attn_workspace(pool, batch, heads, attn_tiles(max_tail, 0));
+}
+
+int launch_attn_tail(const qg_kv_pool *pool, const KvLayout &L, int64_t layer, const uint16_t *q, int64_t ldq,
+                     const int32_t *table, int64_t ld_table, const int32_t *lens, const int32_t *from, int64_t batch,
+                     int64_t heads, int64_t max_len, int64_t max_tail, float scale_log2, float *sums, float *ml, void *workspace,
+                     void *stream) {
+  return launch_checked(pool, L, layer, q, ldq, table, ld_table, lens, from, batch, heads, max_len, max_tail, 0, scale_log2, sums,
+                        heads * pool->head_dim, kRaw, ml, workspace, stream);
+}
 
 }  // namespace qg
 
@@ -892,14 +902,7 @@ int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t head
   if (!bytes) return QG_ERR_NULL;
   KvLayout L;
   if (int st = attn_shape(pool, batch, heads, max_len, &L)) return st;
-  const int64_t group = heads / pool->kv_heads, tiles = attn_tiles(max_len, 0), dim = pool->head_dim;
-  const int64_t tile = attn_tile_heads(group, pool->kv_heads, batch, tiles, dim);
-  // a window only shortens the head tiles: what needs no join without one needs none with one, and
-  // a call that is left with tiles of 16 heads has no more waves than counted here, nor larger parts
-  *bytes = 0;
-  if (batch == 0 || attn_whole(batch * pool->kv_heads * ((group + tile - 1) / tile), tiles, dim)) return QG_OK;
-  const int64_t slots = 2 * kWaves * attn_grid(batch, (group + 15) / 16 * pool->kv_heads, tiles, dim, 16);
-  *bytes = starts_bytes(batch) + 4 * slots * slot_floats((int32_t)(group < tile ? group : tile), (int32_t)dim);
+  *bytes = attn_workspace(pool, batch, heads, attn_tiles(max_len, 0));
   return QG_OK;
 }
 
@@ -922,45 +925,8 @@ int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q,
       attn_misaligned(workspace, 16) || (batch > 1 && (ldq % 8 || ldo % (out_f32 ? 4 : 8))))
     return QG_ERR_ALIGN;
   if (workspace_bytes < need) return QG_ERR_WORKSPACE;
-  AttnArgs a;
-  a.window = (int32_t)(window > max_len ? 0 : window);
-  const int64_t tiles = attn_tiles(max_len, a.window);
-  a.pool = static_cast<const uint8_t *>(pool->pages) + (layer ? layer * pool->layer_stride : 0);
-  a.page_bytes = L.page_bytes;
-  a.head_bytes = L.head_bytes;
-  a.v_off = L.v_off;
-  a.ks_off = L.ks_off;
-  a.vs_off = L.vs_off;
-  a.num_pages = (int32_t)pool->num_pages;
-  a.tok_shift = __builtin_ctz(pool->page_tokens);
-  a.q = q;
-  a.ldq = batch > 1 ? ldq : cols;
-  a.table = table;
-  a.ld_table = ld_table;
-  a.lens = lens;
-  a.batch = (int32_t)batch;
-  a.heads = (int32_t)heads;
-  a.group = (int32_t)(heads / pool->kv_heads);
-  a.tile_heads = attn_tile_heads(a.group, pool->kv_heads, batch, tiles, pool->head_dim);
-  a.tiles_per_kv = (a.group + a.tile_heads - 1) / a.tile_heads;
-  a.head_tiles = a.tiles_per_kv * pool->kv_heads;
-  a.rows = a.group < a.tile_heads ? a.group : a.tile_heads;
-  a.max_len = (int32_t)max_len;
-  a.scale_log2 = scale * kLog2e;
-  a.out = out;
-  a.ldo = batch > 1 ? ldo : cols;
-  a.out_f32 = out_f32 != 0;
-  a.lse = lse;
-  a.starts = static_cast<uint32_t *>(workspace);
-  a.starts_in = static_cast<const int32_t *>(workspace);
-  a.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + starts_bytes(batch));
-  const bool q8 = pool->kind == QG_KV_Q8;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  switch (pool->head_dim) {
-    case 64: return launch_dim<64>(a, tiles, q8, s);
-    case 128: return launch_dim<128>(a, tiles, q8, s);
-    default: return launch_dim<256>(a, tiles, q8, s);
-  }
+  return launch_checked(pool, L, layer, q, ldq, table, ld_table, lens, nullptr, batch, heads, max_len, max_len, window,
+                        scale * kLog2e, out, ldo, out_f32 != 0, lse, workspace, stream);
 }
 
 }  // extern "C"

@@ -501,6 +501,31 @@ int qg_kv_compact(const qg_kv_pool *pool, const int32_t *table, int64_t ld_table
                   int64_t table_rows, int64_t table_pages, const int32_t *refs, int32_t *refs_out, int32_t *remap,
                   int32_t *live, void *workspace, int64_t workspace_bytes, void *stream);
 
+/* Attention of one new token a sequence where neighbouring sequences share their first tokens (forks of one
+ * prompt, many requests after one long instruction): the shared tokens are read and multiplied once for
+ * all of them. Group g < groups is the rows starts[g] to starts[g + 1] - 1 of the batch (int32 [groups + 1] on the
+ * device; rows before starts[0] and from starts[groups] on are in no group), and the first prefix[g] tokens
+ * (int32 [groups] on the device) of each of its rows are the same: they are read through the table's
+ * row starts[g] only, as far as they fill whole pages and that row has them (a prefix below 0 counts as 0,
+ * past lens[starts[g]] as that). Further tokens, and all of a group of one row, are read through each
+ * row's own entries. A row that is shorter than the prefix sees its lens tokens.
+ * Values of starts outside [0, batch] count as the nearest of these, one below an earlier one as that one.
+ * The result is defined as qg_paged_attention's with window 0, with these bounds of the error: with fp32
+ * out the same; with fp16 out the weights e^(s_j - max) of shared tokens meet V as one fp16 number, 2^-11 of
+ * each weight, rounded to nearest, on top (the denominators add the unrounded weights).
+ *
+ * max_tail bounds the tokens that a row reads by itself and chooses the launch's shape only: a row with more of
+ * them is slower, no less right. Arguments, alignment, limits and errors otherwise as qg_paged_attention;
+ * groups is at most 4095 and at most batch. The workspace, at least qg_prefix_attention_bytes, is always needed;
+ * what is said of qg_paged_attention's holds for it. */
+int qg_prefix_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t groups, int64_t max_len,
+                              int64_t max_tail, int64_t *bytes);
+int qg_prefix_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q, int64_t ldq, const int32_t *table,
+                        int64_t ld_table, const int32_t *lens, const int32_t *starts, const int32_t *prefix,
+                        int64_t groups, int64_t batch, int64_t heads, int64_t max_len, int64_t max_tail, float scale,
+                        void *out, int64_t ldo, int out_f32, float *lse, void *workspace, int64_t workspace_bytes,
+                        void *stream);
+
 /* Extend: places for a step's new tokens. Row r of the table asks for add[r] tokens (int32 [table_rows] on the
  * device; 0 or less: none) after its lens[r], and for the pages that it lacks for them. With N_r the tokens asked
  * by rows 0 to r, its tokens are the places N_(r-1) to N_r - 1 of the slot map seqs, positions (int32
