@@ -3,7 +3,6 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/qgemv.h"
-#include "kv_pages.h"
 
 namespace qg {
 
@@ -40,17 +39,5 @@ int launch_skinny(int fmt, const void *w, const uint16_t *X, int64_t ldx, void *
 // Estimated duration in microseconds of one launch_skinny of m <= 32 rows (a huge value for
 // shapes it does not take).
 double skinny_us(int fmt, int64_t m, int64_t n, int64_t k);
-
-// Attention over the tokens from[b] to lens[b] - 1 of each sequence (paged_attn.hip; prefix_attn.hip sends it what
-// the sequences do not share): for row b and head h, the sums of 2^(s - m) V [heads * head_dim] a row, and the pairs (m, sum
-// of 2^(s - m)) with scores s in units of log2 (m -inf and zeros where there is no token). max_tail is the likely number of
-// tokens of the longest; it chooses the launch's shape, and its workspace is attn_tail_bytes. Arguments are validated
-// by the caller; attn_shape_check checks the sizes that all attention over the cache has.
-int attn_shape_check(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_len);
-int64_t attn_tail_bytes(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_tail);
-int launch_attn_tail(const qg_kv_pool *pool, const KvLayout &L, int64_t layer, const uint16_t *q, int64_t ldq,
-                     const int32_t *table, int64_t ld_table, const int32_t *lens, const int32_t *from, int64_t batch,
-                     int64_t heads, int64_t max_len, int64_t max_tail, float scale_log2, float *sums, float *ml, void *workspace,
-                     void *stream);
 
 }  // namespace qg

@@ -46,7 +46,6 @@ struct AttnArgs {
   const int32_t *table;
   int64_t ld_table;
   const int32_t *lens;
-  const int32_t *from;           // tokens before from[b] of sequence b are not seen (NULL: all are)
   int32_t batch, heads, group;   // group = heads / kv_heads
   int32_t tile_heads;            // heads of a head tile: 16, or 32 where a KV head has more than 16
   int32_t tiles_per_kv, head_tiles;   // head tiles of a KV head, and of all of them
@@ -55,7 +54,7 @@ struct AttnArgs {
   float scale_log2;              // scale * log2(e)
   void *out;
   int64_t ldo;
-  int32_t out_f32;               // 0: fp16, 1: fp32, kRaw: the sums themselves in fp32, and (reference, denominator) pairs in lse
+  int32_t out_f32;
   float *lse;
   uint32_t *starts;              // workspace: where each sequence starts on the line, and its end;
   const int32_t *starts_in;      // the same for reading
@@ -63,11 +62,9 @@ struct AttnArgs {
 };
 
 constexpr int kWaves = 4;                          // waves of a workgroup
-constexpr int kTile = 32;                          // tokens of a wave's step, the grain of the split
 constexpr int kThreads = 64 * kWaves;
-constexpr int32_t kRaw = 2;
 
-// What of a sequence is seen: tokens [first, len), in tiles from base = first rounded down.
+// What of sequence b is seen: tokens [first, len), in tiles from base = first rounded down.
 // On the line (below) a head tile of few tiles counts one unit more: its start costs a wave about as
 // much as half a tile, which a wave with many short sequences would be late by (32 sequences of up to
 // 8192 tokens, some of none or one: 56 us without the unit, 51 with it).
@@ -77,18 +74,16 @@ struct Seen {
 };
 constexpr int32_t kShort = 16;                       // tiles below which a head tile has that unit
 template <bool WHOLE>
-__device__ __forceinline__ Seen seen_of(const AttnArgs &a, int32_t raw, int32_t from) {
+__device__ __forceinline__ Seen seen_of(const AttnArgs &a, int32_t raw) {
   Seen s;
   s.len = min(max(raw, 0), a.max_len);
-  s.first = a.window ? max(0, s.len - a.window) : min(from, s.len);
+  s.first = a.window ? max(0, s.len - a.window) : 0;
   s.base = s.first & ~(kTile - 1);
   s.tiles = max(1, (s.len - s.base + kTile - 1) / kTile);      // an empty sequence still gets its zeros written
   s.lead = !WHOLE && s.tiles < kShort ? 1 : 0;
   s.units = (uint32_t)s.tiles + s.lead;
   return s;
 }
-
-__device__ __forceinline__ int32_t from_of(const AttnArgs &a, int32_t b) { return a.from ? scalar_load(a.from + b) : 0; }
 
 // The split. The units of all sequences and head tiles, sequence by sequence and head tile by head
 // tile, are one line of `total` units (below 2^31), of which wave v of `waves` takes the v-th part:
@@ -113,159 +108,6 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *lds, uint32
   }
   total = uniform(all);
   return before + scan - v;
-}
-
-template <int D, bool Q8>
-struct Tile {
-  static constexpr int KD = D / 32;                 // matrix steps along the head
-  static constexpr int VJ = D / 16;                 // elements of one token's V a lane holds
-  static constexpr int KR = Q8 ? D / 64 : D / 32;   // 16-byte loads of a K row a lane takes part in
-  static constexpr int VW = Q8 ? VJ / 4 : VJ / 2;   // dwords of a V row a lane holds
-  u32x4 k[2][KR];
-  uint32_t ks[2][Q8 ? D / 64 : 1];
-  uint32_t v[8][VW];
-  u32x2 vs[2];
-};
-
-// A 16-token block in memory: its KV head's part of a page as a buffer resource, and the block's
-// first place in the page. A block without a page has an empty range, whose loads give zeros.
-struct Block {
-  rsrc_t r;
-  uint32_t place;
-};
-
-// Cache policy: V's codes past the caches (each line is one instruction's), K cached, since two or
-// four instructions share each of its lines, and the scales, whose lines many lanes share. 64
-// sequences of 8192 tokens: all cached 361 us (fp16) and 205 us (int8), all past the caches 316 and
-// 192, this way 322 and 187, and the ragged and short cases all fastest.
-template <int N, int AUX>
-__device__ __forceinline__ void load_words(rsrc_t r, uint32_t voff, uint32_t soff, uint32_t *w) {
-  if constexpr (N == 1) {
-    w[0] = bldx1<AUX>(r, voff, soff);
-  } else if constexpr (N == 2) {
-    const u32x2 t = bldx2<AUX>(r, voff, soff);
-    w[0] = t.x;
-    w[1] = t.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const u32x4 t = bldx4<AUX>(r, voff + 16 * i, soff);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[4 * i + j] = t[j];
-    }
-  }
-}
-
-// K of a tile: lane (c = lane % 16, g = lane / 16) takes token c of each 16-token block; of every 64
-// elements of its row the 16 at 16 g, eight for each of two matrix steps. The lane's part of an
-// address never changes: what does (page, place) is scalar.
-template <int D, bool Q8>
-__device__ __forceinline__ void load_k(const AttnArgs &a, const Block *blk, Tile<D, Q8> &t) {
-  const uint32_t lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int st = 0; st < 2; ++st) {
-#pragma unroll
-    for (int i = 0; i < Tile<D, Q8>::KR; ++i)
-      t.k[st][i] = Q8 ? bldx4<0>(blk[st].r, c * D + 16 * g + 64 * i, blk[st].place * D)
-                      : bldx4<0>(blk[st].r, c * 2 * D + 32 * g + 128 * (i >> 1) + 16 * (i & 1), blk[st].place * 2 * D);
-    if constexpr (Q8) load_words<D / 64, 0>(blk[st].r, c * (D / 16), a.ks_off + blk[st].place * (D / 16), t.ks[st]);
-  }
-}
-
-// V of a tile: a lane takes the VJ elements at VJ * c of the tokens 4 g .. 4 g + 3 of each block.
-template <int D, bool Q8>
-__device__ __forceinline__ void load_v(const AttnArgs &a, const Block *blk, uint32_t vs_lane, Tile<D, Q8> &t) {
-  constexpr uint32_t VJ = Tile<D, Q8>::VJ, VW = Tile<D, Q8>::VW, kElem = Q8 ? 1 : 2;
-  const uint32_t lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-#pragma unroll
-  for (int st = 0; st < 2; ++st) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      load_words<VW, kNT>(blk[st].r, (4 * g * D + VJ * c) * kElem + i * D * kElem, a.v_off + blk[st].place * (D * kElem),
-                     t.v[4 * st + i]);
-    if constexpr (Q8) t.vs[st] = bldx2<0>(blk[st].r, vs_lane, a.vs_off + 2 * blk[st].place);
-  }
-}
-
-// Scores of a block against each 16 heads: S^T [16 tokens x 16 heads] = K Q^T. Lane: head c, tokens 4 g + i.
-template <int D, bool Q8, int HT>
-__device__ __forceinline__ void scores(const Tile<D, Q8> &t, int st, const half8_t (*q)[D / 32], f32x4 *s) {
-#pragma unroll
-  for (int u = 0; u < HT; ++u) s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if constexpr (Q8) {
-    const uint32_t pick = (threadIdx.x & 32) ? 0x03020302u : 0x01000100u;   // the group of the lane's 16 elements
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const uint32_t d = __builtin_amdgcn_perm(t.ks[st][i], t.ks[st][i], pick);
-      u32x4 w[2];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t x = t.k[st][i][j] ^ 0x80808080u;
-        w[j >> 1][2 * (j & 1)] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, x, kSelLow), d);
-        w[j >> 1][2 * (j & 1) + 1] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, x, kSelHigh), d);
-      }
-#pragma unroll
-      for (int u = 0; u < HT; ++u) {
-        s[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w[0]), q[u][2 * i], s[u], 0, 0, 0);
-        s[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, w[1]), q[u][2 * i + 1], s[u], 0, 0, 0);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-      for (int u = 0; u < HT; ++u)
-        s[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, t.k[st][i]), q[u][i], s[u], 0, 0, 0);
-  }
-}
-
-// O^T += V^T P^T with the weights as hi + lo fp16 pairs. Column c of V^T's block j is element
-// VJ * c + j, so O^T's lane holds head c and elements VJ * (4 g + i) + j.
-template <int D, bool Q8, int HT>
-__device__ __forceinline__ void accumulate(const Tile<D, Q8> &t, const half8_t *hi, const half8_t *lo, f32x4 (*o)[D / 16]) {
-  constexpr int VW = Tile<D, Q8>::VW;
-#pragma unroll
-  for (int w = 0; w < VW; ++w) {
-    if constexpr (Q8) {
-      // two tokens' dwords interleave to bytes (t0 d, t1 d, t0 d+1, t1 d+1), then to fp16 pairs
-      u32x4 e[4];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint32_t x0 = t.v[2 * p][w] ^ 0x80808080u, x1 = t.v[2 * p + 1][w] ^ 0x80808080u;
-        const uint32_t d = t.vs[p >> 1][p & 1];
-        const uint32_t a = __builtin_amdgcn_perm(x1, x0, 0x05010400u), b = __builtin_amdgcn_perm(x1, x0, 0x07030602u);
-        e[0][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, a, kSelLow), d);
-        e[1][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, a, kSelHigh), d);
-        e[2][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, b, kSelLow), d);
-        e[3][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, b, kSelHigh), d);
-      }
-#pragma unroll
-      for (int u = 0; u < HT; ++u) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          o[u][4 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), hi[u], o[u][4 * w + j], 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          o[u][4 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), lo[u], o[u][4 * w + j], 0, 0, 0);
-      }
-    } else {
-      u32x4 e[2];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        e[0][p] = __builtin_amdgcn_perm(t.v[2 * p + 1][w], t.v[2 * p][w], 0x05040100u);
-        e[1][p] = __builtin_amdgcn_perm(t.v[2 * p + 1][w], t.v[2 * p][w], 0x07060302u);
-      }
-#pragma unroll
-      for (int u = 0; u < HT; ++u) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          o[u][2 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), hi[u], o[u][2 * w + j], 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          o[u][2 * w + j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, e[j]), lo[u], o[u][2 * w + j], 0, 0, 0);
-      }
-    }
-  }
 }
 
 // A part in the workspace: [rows][D] sums, then each row's reference and denominator, in whole 16
@@ -297,11 +139,11 @@ template <bool WHOLE>
 __device__ __forceinline__ Segment segment_at(const AttnArgs &a, uint32_t at, uint32_t end, int32_t b, uint32_t seq_at,
                                               int32_t len) {
   Segment g;
-  Seen s = seen_of<WHOLE>(a, len, from_of(a, b));
+  Seen s = seen_of<WHOLE>(a, len);
   while (at - seq_at >= s.units * a.head_tiles) {
     seq_at += s.units * a.head_tiles;
     ++b;
-    s = seen_of<WHOLE>(a, scalar_load(a.lens + b), from_of(a, b));
+    s = seen_of<WHOLE>(a, scalar_load(a.lens + b));
   }
   g.ht = (int32_t)((at - seq_at) / s.units);
   g.u0 = seq_at + (uint32_t)g.ht * s.units;
@@ -333,11 +175,6 @@ __device__ __forceinline__ void store_result(const AttnArgs &a, int32_t b, int32
   }
   const int32_t h = h0 + r;
   const int64_t at = b * a.ldo + (int64_t)h * D + d;
-  if (a.out_f32 == kRaw) {
-    *reinterpret_cast<f32x4 *>(static_cast<float *>(a.out) + at) = o;
-    if (d == 0) *reinterpret_cast<f32x2 *>(a.lse + 2 * ((int64_t)b * a.heads + h)) = f32x2{m, l};
-    return;
-  }
   const float inv = l > 0.f ? 1.0f / l : l;          // no token: 0; NaN sums stay NaN
   o *= inv;
   if (a.out_f32) {
@@ -372,7 +209,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? (HT == 1 ? 4 : 3) : D == 128 ? 
   if constexpr (WHOLE) {
     from_b = blockIdx.x / a.head_tiles;
     from_len = scalar_load(a.lens + from_b);
-    const uint32_t tiles = seen_of<true>(a, from_len, from_of(a, (int32_t)from_b)).units;
+    const uint32_t tiles = seen_of<true>(a, from_len).units;
     line = make_line(tiles, blockDim.x / 64);
     line.first = (blockIdx.x - from_b * a.head_tiles) * tiles;
     from_at = 0;
@@ -388,7 +225,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? (HT == 1 ? 4 : 3) : D == 128 ? 
       if (my_b + i < a.batch) {
         const int32_t len = a.lens[my_b + i];
         if (i == 0) my_len = len;
-        mine += seen_of<false>(a, len, a.from ? a.from[my_b + i] : 0).units * a.head_tiles;
+        mine += seen_of<false>(a, len).units * a.head_tiles;
       }
     uint32_t total, before;
     if (one) {
@@ -403,7 +240,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? (HT == 1 ? 4 : 3) : D == 128 ? 
       for (int32_t i = 0; i < per; ++i)
         if (my_b + i < a.batch) {
           a.starts[my_b + i] = at;
-          at += seen_of<false>(a, a.lens[my_b + i], a.from ? a.from[my_b + i] : 0).units * a.head_tiles;
+          at += seen_of<false>(a, a.lens[my_b + i]).units * a.head_tiles;
         }
       if (threadIdx.x == 0) a.starts[a.batch] = total;
     }
@@ -663,7 +500,7 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(AttnArgs a, uint32_t
   __shared__ f32x4 sums[kSplit][kLanes];
   const int32_t b = blockIdx.x / a.head_tiles, ht = blockIdx.x - b * a.head_tiles;
   const Line line = make_line((uint32_t)scalar_load(a.starts_in + a.batch), waves);
-  const Seen s = seen_of<false>(a, scalar_load(a.lens + b), from_of(a, b));
+  const Seen s = seen_of<false>(a, scalar_load(a.lens + b));
   const uint32_t u0 = (uint32_t)scalar_load(a.starts_in + b) + (uint32_t)ht * s.units;
   const uint32_t u1 = u0 + s.units, w0 = line.holder(u0), w1 = line.holder(u1 - 1);
   if (w0 == w1) return;
@@ -815,82 +652,7 @@ int attn_shape(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max
   return QG_OK;
 }
 
-int64_t attn_workspace(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t tiles) {
-  const int64_t group = heads / pool->kv_heads, dim = pool->head_dim;
-  const int64_t tile = attn_tile_heads(group, pool->kv_heads, batch, tiles, dim);
-  // a window only shortens the head tiles: what needs no join without one needs none with one, and
-  // a call that is left with tiles of 16 heads has no more waves than counted here, nor larger parts
-  if (batch == 0 || attn_whole(batch * pool->kv_heads * ((group + tile - 1) / tile), tiles, dim)) return 0;
-  const int64_t slots = 2 * kWaves * attn_grid(batch, (group + 15) / 16 * pool->kv_heads, tiles, dim, 16);
-  return starts_bytes(batch) + 4 * slots * slot_floats((int32_t)(group < tile ? group : tile), (int32_t)dim);
-}
-
-// Launches for checked arguments. likely: the longest sequence's tokens that are seen, as far as the host can
-// say; it chooses the launch's shape only, and the workspace's size follows from it.
-int launch_checked(const qg_kv_pool *pool, const KvLayout &L, int64_t layer, const uint16_t *q, int64_t ldq, const int32_t *table,
-                   int64_t ld_table, const int32_t *lens, const int32_t *from, int64_t batch, int64_t heads, int64_t max_len,
-                   int64_t likely, int64_t window, float scale_log2, void *out, int64_t ldo, int32_t out_f32, float *lse,
-                   void *workspace, void *stream) {
-  AttnArgs a;
-  a.window = (int32_t)(window > max_len ? 0 : window);
-  const int64_t tiles = attn_tiles(likely, a.window), cols = heads * pool->head_dim;
-  a.pool = static_cast<const uint8_t *>(pool->pages) + (layer ? layer * pool->layer_stride : 0);
-  a.page_bytes = L.page_bytes;
-  a.head_bytes = L.head_bytes;
-  a.v_off = L.v_off;
-  a.ks_off = L.ks_off;
-  a.vs_off = L.vs_off;
-  a.num_pages = (int32_t)pool->num_pages;
-  a.tok_shift = __builtin_ctz(pool->page_tokens);
-  a.q = q;
-  a.ldq = batch > 1 ? ldq : cols;
-  a.table = table;
-  a.ld_table = ld_table;
-  a.lens = lens;
-  a.from = from;
-  a.batch = (int32_t)batch;
-  a.heads = (int32_t)heads;
-  a.group = (int32_t)(heads / pool->kv_heads);
-  a.tile_heads = attn_tile_heads(a.group, pool->kv_heads, batch, tiles, pool->head_dim);
-  a.tiles_per_kv = (a.group + a.tile_heads - 1) / a.tile_heads;
-  a.head_tiles = a.tiles_per_kv * pool->kv_heads;
-  a.rows = a.group < a.tile_heads ? a.group : a.tile_heads;
-  a.max_len = (int32_t)max_len;
-  a.scale_log2 = scale_log2;
-  a.out = out;
-  a.ldo = batch > 1 ? ldo : cols;
-  a.out_f32 = out_f32;
-  a.lse = lse;
-  a.starts = static_cast<uint32_t *>(workspace);
-  a.starts_in = static_cast<const int32_t *>(workspace);
-  a.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + starts_bytes(batch));
-  const bool q8 = pool->kind == QG_KV_Q8;
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  switch (pool->head_dim) {
-    case 64: return launch_dim<64>(a, tiles, q8, s);
-    case 128: return launch_dim<128>(a, tiles, q8, s);
-    default: return launch_dim<256>(a, tiles, q8, s);
-  }
-}
-
 }  // namespace
-
-int attn_shape_check(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_len) {
-  KvLayout L;
-  return attn_shape(pool, batch, heads, max_len, &L);
-}
-
-int64_t attn_tail_bytes(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t max_tail) {
-  return attn_workspace(pool, batch, heads, attn_tiles(max_tail, 0));
-}
-
-int launch_attn_tail(const qg_kv_pool *pool, const KvLayout &L, int64_t layer, const uint16_t *q, int64_t ldq,
-                     const int32_t *table, int64_t ld_table, const int32_t *lens, const int32_t *from, int64_t batch,
-                     int64_t heads, int64_t max_len, int64_t max_tail, float scale_log2, float *sums, float *ml, void *workspace,
-                     void *stream) {
-  return launch_checked(pool, L, layer, q, ldq, table, ld_table, lens, from, batch, heads, max_len, max_tail, 0, scale_log2, sums,
-                        heads * pool->head_dim, kRaw, ml, workspace, stream);
-}
 
 }  // namespace qg
 
@@ -902,7 +664,14 @@ int qg_paged_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t head
   if (!bytes) return QG_ERR_NULL;
   KvLayout L;
   if (int st = attn_shape(pool, batch, heads, max_len, &L)) return st;
-  *bytes = attn_workspace(pool, batch, heads, attn_tiles(max_len, 0));
+  const int64_t group = heads / pool->kv_heads, tiles = attn_tiles(max_len, 0), dim = pool->head_dim;
+  const int64_t tile = attn_tile_heads(group, pool->kv_heads, batch, tiles, dim);
+  // a window only shortens the head tiles: what needs no join without one needs none with one, and
+  // a call that is left with tiles of 16 heads has no more waves than counted here, nor larger parts
+  *bytes = 0;
+  if (batch == 0 || attn_whole(batch * pool->kv_heads * ((group + tile - 1) / tile), tiles, dim)) return QG_OK;
+  const int64_t slots = 2 * kWaves * attn_grid(batch, (group + 15) / 16 * pool->kv_heads, tiles, dim, 16);
+  *bytes = starts_bytes(batch) + 4 * slots * slot_floats((int32_t)(group < tile ? group : tile), (int32_t)dim);
   return QG_OK;
 }
 
@@ -925,8 +694,45 @@ int qg_paged_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q,
       attn_misaligned(workspace, 16) || (batch > 1 && (ldq % 8 || ldo % (out_f32 ? 4 : 8))))
     return QG_ERR_ALIGN;
   if (workspace_bytes < need) return QG_ERR_WORKSPACE;
-  return launch_checked(pool, L, layer, q, ldq, table, ld_table, lens, nullptr, batch, heads, max_len, max_len, window,
-                        scale * kLog2e, out, ldo, out_f32 != 0, lse, workspace, stream);
+  AttnArgs a;
+  a.window = (int32_t)(window > max_len ? 0 : window);
+  const int64_t tiles = attn_tiles(max_len, a.window);
+  a.pool = static_cast<const uint8_t *>(pool->pages) + (layer ? layer * pool->layer_stride : 0);
+  a.page_bytes = L.page_bytes;
+  a.head_bytes = L.head_bytes;
+  a.v_off = L.v_off;
+  a.ks_off = L.ks_off;
+  a.vs_off = L.vs_off;
+  a.num_pages = (int32_t)pool->num_pages;
+  a.tok_shift = __builtin_ctz(pool->page_tokens);
+  a.q = q;
+  a.ldq = batch > 1 ? ldq : cols;
+  a.table = table;
+  a.ld_table = ld_table;
+  a.lens = lens;
+  a.batch = (int32_t)batch;
+  a.heads = (int32_t)heads;
+  a.group = (int32_t)(heads / pool->kv_heads);
+  a.tile_heads = attn_tile_heads(a.group, pool->kv_heads, batch, tiles, pool->head_dim);
+  a.tiles_per_kv = (a.group + a.tile_heads - 1) / a.tile_heads;
+  a.head_tiles = a.tiles_per_kv * pool->kv_heads;
+  a.rows = a.group < a.tile_heads ? a.group : a.tile_heads;
+  a.max_len = (int32_t)max_len;
+  a.scale_log2 = scale * kLog2e;
+  a.out = out;
+  a.ldo = batch > 1 ? ldo : cols;
+  a.out_f32 = out_f32 != 0;
+  a.lse = lse;
+  a.starts = static_cast<uint32_t *>(workspace);
+  a.starts_in = static_cast<const int32_t *>(workspace);
+  a.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + starts_bytes(batch));
+  const bool q8 = pool->kind == QG_KV_Q8;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  switch (pool->head_dim) {
+    case 64: return launch_dim<64>(a, tiles, q8, s);
+    case 128: return launch_dim<128>(a, tiles, q8, s);
+    default: return launch_dim<256>(a, tiles, q8, s);
+  }
 }
 
 }  // extern "C"

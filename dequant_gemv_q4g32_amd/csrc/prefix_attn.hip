@@ -1,16 +1,13 @@
 // Attention of one new token a sequence where neighbouring sequences share their first tokens, gfx950.
 //
-// A group's rows with the heads of a KV head are one block of queries against the shared tokens: unlike a
-// single sequence's few heads, enough of them to keep the matrix cores busy. Three steps: the shared tokens,
-// once a group, as a flash attention of up to 128 query rows a workgroup; what the rows do not share, by the
-// one-token kernel (paged_attn.hip); the join of both.
-//
-// Shared tokens: S^T = K Q^T and O^T += V^T P^T on v_mfma_f32_32x32x16_f16. A wave takes 32 query rows, and
-// a lane of S^T holds one row and 16 of 32 tokens, which is the operand that P^T has to be: the softmax stays in the
-// registers. K and V go through LDS as fp16, decoded and V turned once for the four waves, in two buffers: while
-// one tile is multiplied the next one is written and the one after that is on its way from memory.
+// A group's rows with the heads of a KV head are one block of queries against the shared tokens: unlike a single
+// sequence's few heads, enough of them to keep the matrix cores busy. One launch does both kinds of work, each on its
+// share of the workgroups: the shared tokens, once a group, as a flash attention of up to 256 query rows a workgroup
+// (bound by the matrix and vector instructions), and the tokens that a row has for itself, as paged_attn.hip does
+// them, a wave for up to 16 heads (bound by HBM). A second launch joins the parts.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 
 #include "../../include/qgemv.h"
@@ -23,17 +20,37 @@ namespace qg {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kPrefixThreads = 256;
-constexpr int kRows = 128;                         // query rows of a workgroup, 32 a wave
-constexpr int kElems = 8192;                       // elements of K (and of V) a tile: 128 tokens of 64, 64 of 128, 32 of 256
+// Waves of a workgroup, each with 32 query rows of the shared tokens: two on every SIMD, so that one's vector
+// instructions run beside the other's matrix instructions. Heads of 256 take the registers of two.
+__host__ __device__ constexpr int prefix_waves(int dim) { return dim == 256 ? 4 : 8; }
+// Shared tokens of a tile: 8192 elements of K, and of V.
+__host__ __device__ constexpr int tile_tokens(int dim) { return 8192 / dim; }
+// Heads of a KV head that a wave takes against a row's own tokens.
+constexpr int kHeads = 16;
+constexpr int kMaxGroups = 1023;
 
-// What the plan says of a group. Its query rows are rows * (heads of a KV head), in tiles of kRows a KV head; its
-// tokens are `units` tiles. On the line its segments (KV head, row tile) follow each other, `units` each.
+// What the workgroups find out of a group (of at least two rows). Its query rows are rows * (heads of a KV head), in
+// tiles a KV head; its tokens, whole pages, are tiles too, `units` with the lead. On the line of shared work its
+// segments (KV head, row tile) follow each other, `units` each: the lead, which stands for what the start of a segment
+// costs a worker that comes from another one, then the tiles.
+constexpr int32_t kLead = 4;
+// The same for own work, about 3 us; a step takes what its bytes do, of which the waves of a workgroup together
+// get 42 KB a us.
+__host__ __device__ constexpr double own_step_us(int dim, bool q8) { return prefix_waves(dim) * 32 * (q8 ? 2.125 : 4.0) * dim / 42e3; }
+__host__ __device__ constexpr int32_t own_lead(int dim, bool q8) { return (int32_t)(3.0 / own_step_us(dim, q8) + 0.5); }
 struct GroupPlan {
-  int32_t row0, rows, tokens;
-  int32_t row_tiles, units;
+  int32_t row0, tokens, row_tiles, units;
   uint32_t unit0, seg0;          // units and segments of the groups before
-  int32_t pad;
+};
+// Of a row: its group (-1: it shares nothing), and its own tokens' place on the line of own work: for each head tile in
+// turn `units`, a lead and steps of 32 tokens, or none.
+struct RowPlan {
+  int32_t group;
+  uint32_t unit0, units;
+};
+// Of the call: both lines, and their workers.
+struct Split {
+  uint32_t shared, workers, own, waves;
 };
 
 struct PrefixArgs {
@@ -47,244 +64,316 @@ struct PrefixArgs {
   int64_t ld_table;
   const int32_t *lens, *starts, *prefix;
   int32_t groups, batch, heads, group, kv_heads;   // group = heads / kv_heads
-  int32_t max_len, tile_tokens;
-  float scale_log2;              // |scale| * log2(e)
-  uint32_t flip;                 // sign bits of two fp16 numbers where scale is negative: turned in q
+  int32_t tiles_per_kv, head_tiles;   // own work: head tiles of a KV head, and of all of them
+  int32_t max_len;
+  int32_t part_rows, own_rows;   // query rows that a part of shared work, and of own work, has room for
+  int32_t own_lead;              // of own work's segments
+  uint32_t own_most;             // waves that own work may have: the parts' room
+  float shared_cost;             // of a tile of shared work for a workgroup, in steps of own work of a wave
+  float scale_log2;              // |scale| * log2(e), or 1 where that is not a normal number;
+  uint32_t keep, flip;           // for these, q is taken as zero, or as its negative: masks of two fp16 numbers
   void *out;
   int64_t ldo;
   int32_t out_f32;
   float *lse;
-  uint32_t *total;               // workspace: units in all;
+  Split *split;                  // workspace: what the join has to know,
   GroupPlan *plan;
-  int32_t *from, *group_of;      // of each row: the tokens that it shares, its group (-1: shares none)
-  float *parts;                  // partial results: part w + s is worker w's of segment s
-  float *tail, *tail_ml;         // what launch_attn_tail gives
+  RowPlan *rows;
+  float *parts, *own_parts;      // and the partial results: part w + s is worker w's of segment s
 };
 
-// A part: [kRows][D] sums, then each row's reference and denominator.
-__host__ __device__ __forceinline__ int64_t part_floats(int32_t dim) { return (int64_t)kRows * dim + 2 * kRows; }
+// A part: [rows][D] sums, then each row's reference and denominator.
+__host__ __device__ __forceinline__ int64_t part_floats(int32_t dim, int32_t rows) { return (int64_t)rows * dim + 2 * rows; }
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanGroups = 4;                     // groups a thread
-constexpr int64_t kMaxGroups = kPlanThreads * kPlanGroups - 1;
+// ---- the plan ------------------------------------------------------------------------------------
+//
+// Every workgroup makes the whole plan by itself: it is a chain of three loads and some sums, and a launch of its
+// own took 5 us.
 
-// Sum (or maximum) over the threads up to this one. lds: a value for each wave.
-template <bool MAX>
-__device__ __forceinline__ uint32_t plan_scan(uint32_t v, uint32_t *lds) {
-  auto join = [](uint32_t a, uint32_t b) { return MAX ? max(a, b) : a + b; };
+__device__ __forceinline__ uint32_t scan_max(uint32_t v) {
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const uint32_t up = (uint32_t)__shfl_up((int)v, o);
-    if ((int)(threadIdx.x & 63) >= o) v = join(v, up);
+    if ((int)(threadIdx.x & 63) >= o) v = max(v, up);
   }
-  __syncthreads();
-  if ((threadIdx.x & 63) == 63) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  for (int w = 0; w < (int)(threadIdx.x >> 6); ++w) v = join(v, lds[w]);
   return v;
 }
 
-// One workgroup: the groups' rows and shared tokens, their places on the line, and each row's group.
-__global__ __launch_bounds__(kPlanThreads) void prefix_plan_kernel(PrefixArgs a) {
-  __shared__ uint32_t lds[kPlanThreads / 64];
-  __shared__ int32_t lead[kPlanThreads * kPlanGroups];   // the groups' first rows, made to ascend, and the last one's end
-  __shared__ int32_t shared[kPlanThreads * kPlanGroups];
-  const int32_t g0 = kPlanGroups * (int32_t)threadIdx.x;
-  uint32_t at[kPlanGroups], most = 0;
-#pragma unroll
-  for (int i = 0; i < kPlanGroups; ++i) {
-    const int32_t s = g0 + i <= a.groups ? a.starts[g0 + i] : 0;
-    most = max(most, (uint32_t)min(max(s, 0), a.batch));
-    at[i] = most;
-  }
-  const uint32_t upto = plan_scan<true>(most, lds);
-  // what is before this thread: the scan's value of the thread before
-  __shared__ uint32_t edge[kPlanThreads];
-  edge[threadIdx.x] = upto;
-  __syncthreads();
-  const uint32_t before = threadIdx.x ? edge[threadIdx.x - 1] : 0;
-#pragma unroll
-  for (int i = 0; i < kPlanGroups; ++i) lead[g0 + i] = (int32_t)max(at[i], before);
-  __syncthreads();
-  GroupPlan p[kPlanGroups];
-  uint32_t units = 0, segs = 0;
-#pragma unroll
-  for (int i = 0; i < kPlanGroups; ++i) {
-    const int32_t g = g0 + i;
-    p[i] = GroupPlan{0, 0, 0, 0, 0, 0, 0, 0};
-    if (g >= a.groups) continue;
-    p[i].row0 = lead[g];
-    p[i].rows = lead[g + 1] - lead[g];
-    if (p[i].rows > 1) {
-      const int32_t len = min(max(a.lens[p[i].row0], 0), a.max_len);
-      p[i].tokens = min(max(a.prefix[g], 0), len) >> a.tok_shift << a.tok_shift;   // whole pages
-    }
-    p[i].units = (p[i].tokens + a.tile_tokens - 1) / a.tile_tokens;
-    p[i].row_tiles = p[i].units ? (int32_t)(((int64_t)p[i].rows * a.group + kRows - 1) / kRows) : 0;
-    p[i].unit0 = units;
-    p[i].seg0 = segs;
-    segs += (uint32_t)(p[i].row_tiles * a.kv_heads);
-    units += (uint32_t)(p[i].row_tiles * a.kv_heads) * (uint32_t)p[i].units;
-    shared[g] = p[i].tokens;
-  }
-  const uint32_t all_units = plan_scan<false>(units, lds), all_segs = plan_scan<false>(segs, lds);
-#pragma unroll
-  for (int i = 0; i < kPlanGroups; ++i) {
-    if (g0 + i >= a.groups) continue;
-    p[i].unit0 += all_units - units;
-    p[i].seg0 += all_segs - segs;
-    a.plan[g0 + i] = p[i];
-  }
-  if (threadIdx.x == kPlanThreads - 1) *a.total = all_units;
-  __syncthreads();
-  for (int32_t b = threadIdx.x; b < a.batch; b += kPlanThreads) {
-    int32_t lo = 0, hi = a.groups + 1;               // the last g with lead[g] <= b is lo - 1
+struct Plan {
+  int32_t lead[kMaxGroups + 1];  // the groups' first rows, made to ascend, and the last one's end
+  GroupPlan g[kMaxGroups];
+  uint32_t red[2][8];
+  uint32_t found[3][8];
+
+  // the group of row b, -1: none
+  __device__ __forceinline__ int32_t group_of(int32_t b, int32_t groups) const {
+    int32_t lo = 0, hi = groups + 1;                 // the last lead <= b is lo - 1
     while (lo < hi) {
       const int32_t mid = (lo + hi) >> 1;
       if (lead[mid] <= b) lo = mid + 1; else hi = mid;
     }
-    const int32_t g = lo - 1;
-    const int32_t n = g >= 0 && g < a.groups ? shared[g] : 0;
-    a.from[b] = n;
-    a.group_of[b] = n ? g : -1;
+    return lo > groups || lo == 0 || g[lo - 1].tokens == 0 ? -1 : lo - 1;
   }
+};
+
+// Sums over the threads before this one, and in all, of two values at once.
+template <int W>
+__device__ __forceinline__ void scan_two(uint32_t &x, uint32_t &y, uint32_t &all_x, uint32_t &all_y, Plan &p) {
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, sx = wave_scan(x), sy = wave_scan(y);
+  __syncthreads();
+  if (lane == 63) {
+    p.red[0][wave] = sx;
+    p.red[1][wave] = sy;
+  }
+  __syncthreads();
+  uint32_t bx = 0, by = 0, tx = 0, ty = 0;
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    const uint32_t rx = p.red[0][k], ry = p.red[1][k];
+    bx += k < (int)wave ? rx : 0;
+    by += k < (int)wave ? ry : 0;
+    tx += rx;
+    ty += ry;
+  }
+  x = bx + sx - x;
+  y = by + sy - y;
+  all_x = uniform(tx);
+  all_y = uniform(ty);
+}
+
+// What of a row's tokens is its own: [first, len), in steps of 32 from base = first rounded down, and the units
+// that a head tile of it has on the line.
+struct Own {
+  int32_t first, len, base;
+  uint32_t units;
+};
+__device__ __forceinline__ Own own_of(const PrefixArgs &a, int32_t raw, int32_t shared) {
+  Own o;
+  o.len = min(max(raw, 0), a.max_len);
+  o.first = min(shared, o.len);
+  o.base = o.first & ~(kTile - 1);
+  o.units = o.first < o.len ? (uint32_t)(o.len - o.base + kTile - 1) / kTile + a.own_lead : 0;
+  return o;
 }
 
 // ---- the shared tokens ---------------------------------------------------------------------------
 
+// What a tile is to a workgroup. K is fetched 16 bytes a thread and load, V in pieces of four tokens by four
+// elements, so that the 64 lanes of a load lie in one block of 16 tokens: its page is scalar. In LDS a row has 16
+// bytes more than it needs: 16 neighbouring lanes read the same place of neighbouring rows at once, which so lie
+// in different banks, and all places of a lane are constants away from one address. K is [T][D], V^T [D][T] with
+// each 16 bytes the eight tokens of a lane's operand (16 s + 4 h + {0..3, 8..11} for step s, lane half h: place 2 s + h).
 template <int D, bool Q8>
 struct Shape {
-  static constexpr int T = kElems / D;              // tokens of a tile
-  static constexpr int TB = T / 32;                 // blocks of 32 of them
+  static constexpr int NT = 64 * prefix_waves(D);
+  static constexpr int T = tile_tokens(D);
+  static constexpr int TB = T / 32;                 // blocks of 32 tokens
   static constexpr int KS = D / 16;                 // matrix steps along the head
   static constexpr int DB = D / 32;                 // blocks of 32 elements of the head
-  static constexpr int KL = Q8 ? 2 : 4;             // 16-byte loads of K a thread
-  static constexpr int KPer = Q8 ? D / 16 : D / 8;  // such loads a token
-  static constexpr int VPer = D / 4;                // threads that share eight tokens of V, four elements each
+  static constexpr int KBytes = Q8 ? D : 2 * D;     // bytes of a token's K
+  static constexpr int KPer = KBytes / 16;          // loads of a token's K
+  static constexpr int KL = T * KPer / NT;          // such loads a thread
+  static constexpr int VPer = D / 4;                // pieces of four tokens' V
+  static constexpr int VL = T / 4 * VPer / NT;      // pieces a thread
+  static constexpr uint32_t KRow = D / 8 + 1, VRow = T / 8 + 1;   // 16-byte places of a row in LDS
+  static constexpr uint32_t KTile = T * KRow, VTile = D * VRow;   // and of a tile
+  static constexpr uint32_t kLds = 16 * 3 * (KTile + VTile);      // bytes of three tiles
 };
 
-// Places in LDS, in units of 16 bytes: neighbouring lanes read the same place of neighbouring rows, so a row's
-// places are exchanged by its number to spread them over the banks. K is [T][D], V^T [D][T] with each
-// place eight tokens of a lane's operand (16 s + 4 h + {0..3, 8..11} for step s, lane half h: place 2 s + h).
-template <int D>
-__device__ __forceinline__ uint32_t k_place(uint32_t tok, uint32_t c) { return tok * (D / 8) + (c ^ (tok & 7)); }
-template <int D>
-__device__ __forceinline__ uint32_t v_place(uint32_t d, uint32_t c) {
-  constexpr uint32_t kPer = kElems / D / 8;          // places of a row: 16, 8, 4
-  return d * kPer + (c ^ (kPer >= 8 ? (d ^ (d >> 3)) & 7 : ((d >> 1) ^ (d >> 3)) & 3));
-}
-
-// What a thread holds of the tile on its way.
+// K and V of a tile on its way, and their way into LDS. A page that is none has an empty range, whose loads
+// give zeros.
 template <int D, bool Q8>
-struct Staged {
-  u32x4 k[Shape<D, Q8>::KL];
-  uint16_t ks[Shape<D, Q8>::KL];
-  u32x2 v[8];                                        // int8: one dword each
-  u32x2 vs[2];
-  bool fine;                                         // the thread's tokens of V are in a page
-};
-
-template <int D, bool Q8>
-__device__ __forceinline__ void write_tile(const Staged<D, Q8> &t, u32x4 *lds) {
+struct StagedK {
   using S = Shape<D, Q8>;
-  const uint32_t tid = threadIdx.x;
+  u32x4 k[S::KL];
+  uint32_t s[S::KL];
+  __device__ __forceinline__ void write(u32x4 *lds) const {
+    const uint32_t at = threadIdx.x / S::KPer * S::KRow + threadIdx.x % S::KPer * (Q8 ? 2 : 1);
 #pragma unroll
-  for (int i = 0; i < S::KL; ++i) {
-    const uint32_t id = tid + kPrefixThreads * i, tok = id / S::KPer, c = id % S::KPer;
-    if constexpr (Q8) {
-      const uint32_t d = t.ks[i] * 0x00010001u;
-      u32x4 w[2];
+    for (int i = 0; i < S::KL; ++i) {
+      u32x4 *to = lds + at + i * (S::NT / S::KPer) * S::KRow;
+      if constexpr (Q8) {
+        const uint32_t d = s[i] * 0x00010001u;
+        u32x4 w[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t x = t.k[i][j] ^ 0x80808080u;
-        w[j >> 1][2 * (j & 1)] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, x, kSelLow), d);
-        w[j >> 1][2 * (j & 1) + 1] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, x, kSelHigh), d);
-      }
-      lds[k_place<D>(tok, 2 * c)] = w[0];
-      lds[k_place<D>(tok, 2 * c + 1)] = w[1];
-    } else {
-      lds[k_place<D>(tok, c)] = t.k[i];
-    }
-  }
-  const uint32_t c = tid / S::VPer, d0 = 4 * (tid % S::VPer);
-  u32x4 e[4];                                        // elements d0 .. d0 + 3, eight tokens each
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    if constexpr (Q8) {
-      const uint32_t x0 = t.v[2 * p].x ^ 0x80808080u, x1 = t.v[2 * p + 1].x ^ 0x80808080u, d = t.vs[p >> 1][p & 1];
-      const uint32_t a = __builtin_amdgcn_perm(x1, x0, 0x05010400u), b = __builtin_amdgcn_perm(x1, x0, 0x07030602u);
-      e[0][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, a, kSelLow), d);
-      e[1][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, a, kSelHigh), d);
-      e[2][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, b, kSelLow), d);
-      e[3][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, b, kSelHigh), d);
-    } else {
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        e[2 * w][p] = __builtin_amdgcn_perm(t.v[2 * p + 1][w], t.v[2 * p][w], 0x05040100u);
-        e[2 * w + 1][p] = __builtin_amdgcn_perm(t.v[2 * p + 1][w], t.v[2 * p][w], 0x07060302u);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = k[i][j] ^ 0x80808080u;
+          w[j >> 1][2 * (j & 1)] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, x, kSelLow), d);
+          w[j >> 1][2 * (j & 1) + 1] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, x, kSelHigh), d);
+        }
+        to[0] = w[0];
+        to[1] = w[1];
+      } else {
+        to[0] = k[i];
       }
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)                        // what is in no page may be anything, and zero times NaN is NaN
-    lds[kElems / 8 + v_place<D>(d0 + i, c)] = t.fine ? e[i] : u32x4{0, 0, 0, 0};
-}
+};
 
-// Workgroup `bid` takes its part of the line, segment by segment. PAIRS: weights as hi + lo fp16 pairs (22
+template <int D, bool Q8>
+struct StagedV {
+  using S = Shape<D, Q8>;
+  u32x2 v[S::VL][4];                               // int8: one dword each
+  u32x2 s[S::VL];
+  __device__ __forceinline__ void write(u32x4 *lds) const {
+    const uint32_t d0 = 4 * (threadIdx.x % S::VPer), run = threadIdx.x / S::VPer;   // of four tokens
+    const uint32_t at = d0 * S::VRow + 2 * (run >> 2) + (run & 1), half = (run >> 1) & 1;
+#pragma unroll
+    for (int i = 0; i < S::VL; ++i) {
+      u32x2 e[4];                                   // elements d0 .. d0 + 3, four tokens each
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        if constexpr (Q8) {
+          const uint32_t x0 = v[i][2 * p].x ^ 0x80808080u, x1 = v[i][2 * p + 1].x ^ 0x80808080u, d = s[i][p];
+          const uint32_t a = __builtin_amdgcn_perm(x1, x0, 0x05010400u), b = __builtin_amdgcn_perm(x1, x0, 0x07030602u);
+          e[0][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, a, kSelLow), d);
+          e[1][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, a, kSelHigh), d);
+          e[2][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, b, kSelLow), d);
+          e[3][p] = scaled_pair(__builtin_amdgcn_perm(kMagicBytes, b, kSelHigh), d);
+        } else {
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            e[2 * w][p] = __builtin_amdgcn_perm(v[i][2 * p + 1][w], v[i][2 * p][w], 0x05040100u);
+            e[2 * w + 1][p] = __builtin_amdgcn_perm(v[i][2 * p + 1][w], v[i][2 * p][w], 0x07060302u);
+          }
+        }
+      }
+      constexpr uint32_t kStep = S::NT / S::VPer / 2;   // places between a thread's pieces: their runs are a multiple of 4 apart
+      static_assert(S::VL == 1 || S::NT / S::VPer % 4 == 0, "the pieces' halves agree");
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *(reinterpret_cast<u32x2 *>(lds + at + j * S::VRow + i * kStep) + half) = e[j];
+    }
+  }
+};
+
+// A worker's part [at, end) of the line of shared work, segment by segment. PAIRS: weights as hi + lo fp16 pairs (22
 // bits), for fp32 results; else as one fp16 number, whose rounding, 2^-12 of a weight on average and
 // independent from token to token, is of the size of an fp16 result's own.
+//
+// The work is in steps of 32 tokens, three of which are under way at once, each independent of the others: the
+// scores of the next, the softmax of this one, the products with V of the one before. So matrix and vector
+// instructions alternate throughout. K and V lie in three buffers of a tile each: a tile's writing, its scores'
+// reading and its products' reading go on between the same two barriers.
+//
+// S^T = K Q^T and O^T += V^T P^T on v_mfma_f32_32x32x16_f16: a lane of S^T holds one query row and 16 of 32
+// tokens, which is the operand that P^T has to be, so the softmax stays in the registers.
 template <int D, bool Q8, bool PAIRS>
-__global__ __launch_bounds__(kPrefixThreads, D == 256 ? 1 : 2) void prefix_kernel(PrefixArgs a) {
+__device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &plan, u32x4 *tiles, uint32_t w, uint32_t at, uint32_t end) {
   using S = Shape<D, Q8>;
-  constexpr int T = S::T, TB = S::TB, KS = S::KS, DB = S::DB, kBlocks = T / 16;
-  extern __shared__ __align__(16) u32x4 tiles[];     // [2][K, V^T]
+  constexpr int T = S::T, TB = S::TB, KS = S::KS, DB = S::DB, kBlocks = T / 16, kRows = S::NT / 2, NT = S::NT;
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), n = lane & 31, h = lane >> 5;
-  if constexpr (Q8) __builtin_amdgcn_s_setreg(1 | (23 << 6) | (0 << 11), 1);   // hwreg(MODE, 23, 1): FP16_OVFL
-  const uint32_t total = (uint32_t)scalar_load(reinterpret_cast<const int32_t *>(a.total));
-  if (total == 0) return;
-  const Line line = make_line(total, gridDim.x);
-  const uint32_t w = blockIdx.x;
-  if (w >= line.waves) return;
-  const uint32_t end = line.start(w + 1);
-  uint32_t at = line.start(w);
+  u32x4 *const lds_k = tiles, *const lds_v = tiles + 3 * S::KTile;
+  const uint32_t k_at = n * S::KRow + h, v_at = n * S::VRow + h;   // a lane's places of K and V
+  // a lane's part of an address of K and V, beside the wave's first rows
+  const uint32_t k_lane = (lane / S::KPer) * S::KBytes + 16 * (lane % S::KPer);
+  const uint32_t ks_lane = Q8 ? (lane / S::KPer) * (D / 16) + 2 * (lane % S::KPer / 2) : 0;
+  const uint32_t v_run = lane / S::VPer, v_lane = 4 * v_run * S::KBytes + (Q8 ? 4 : 8) * (tid % S::VPer);
+  const uint32_t vs_lane = 2 * (((4 * (tid % S::VPer) / 32) << a.tok_shift) + 4 * v_run);
   int32_t g = 0;
-  {                                                  // the last group with unit0 <= at that has units
+  {                                                  // the last group with unit0 <= at
     int32_t lo = 0, hi = a.groups;
     while (lo < hi) {
       const int32_t mid = (lo + hi) >> 1;
-      if ((uint32_t)scalar_load(reinterpret_cast<const int32_t *>(&a.plan[mid].unit0)) <= at) lo = mid + 1; else hi = mid;
+      if (uniform(plan.g[mid].unit0) <= at) lo = mid + 1; else hi = mid;
     }
     g = lo - 1;
   }
   while (at < end) {
-    const int32_t *said = reinterpret_cast<const int32_t *>(a.plan + g);
-    const GroupPlan p{scalar_load(said), scalar_load(said + 1), scalar_load(said + 2), scalar_load(said + 3), scalar_load(said + 4),
-                      (uint32_t)scalar_load(said + 5), (uint32_t)scalar_load(said + 6), 0};
+    const GroupPlan p{uniform(plan.g[g].row0), uniform(plan.g[g].tokens), uniform(plan.g[g].row_tiles), uniform(plan.g[g].units),
+                      uniform(plan.g[g].unit0), uniform(plan.g[g].seg0)};
+    const int32_t rows = (uniform(plan.lead[g + 1]) - p.row0) * a.group;
     const uint32_t segs = (uint32_t)(p.row_tiles * a.kv_heads);
     if (p.units == 0 || at - p.unit0 >= segs * (uint32_t)p.units) {
       ++g;
       continue;
     }
-    const uint32_t seg = (at - p.unit0) / (uint32_t)p.units, first = at - p.unit0 - seg * (uint32_t)p.units;
-    const uint32_t last = min(first + (end - at), (uint32_t)p.units);   // tiles [first, last) of the group's tokens
+    const uint32_t seg = (at - p.unit0) / (uint32_t)p.units, u = at - p.unit0 - seg * (uint32_t)p.units;
+    const uint32_t until = min(u + (end - at), (uint32_t)p.units);
+    at += until - u;
+    if (until <= kLead) continue;
+    const uint32_t first = max(u, (uint32_t)kLead) - kLead, last = until - kLead;   // tiles of the group's tokens
     const int32_t kvh = (int32_t)(seg / (uint32_t)p.row_tiles), rt = (int32_t)seg - kvh * p.row_tiles;
     const int32_t *row = a.table + (int64_t)p.row0 * a.ld_table;
     const uint8_t *kv = a.pool + kvh * a.head_bytes;
-    // the lane's query row
-    const int32_t m = rt * kRows + (int32_t)(32 * wave + n), rows = p.rows * a.group;
+
+    // The pages of 64 blocks of 16 tokens, a block a lane (-1: none, or not this worker's); those of the next 64
+    // on their way.
+    const uint32_t blocks = min(last * kBlocks, (uint32_t)p.tokens / 16);
+    auto pages_at = [&](uint32_t blk) { return blk + lane < blocks ? row[(int64_t)(blk + lane) * 16 >> a.tok_shift] : -1; };
+    auto in_pool = [&](int32_t page) { return page < a.num_pages ? max(page, -1) : -1; };
+    uint32_t base = first * kBlocks;                 // of the blocks in ids
+    int32_t ids = in_pool(pages_at(base)), ids_next = pages_at(base + 64);
+    auto block = [&](int32_t page) {
+      return make_rsrc(kv + (uint64_t)(uint32_t)max(page, 0) * (uint64_t)a.page_bytes, page < 0 ? 0u : (uint32_t)a.head_bytes);
+    };
+    const uint32_t mask = (1u << a.tok_shift) - 1;
+    int32_t v_page[S::VL];                           // of the tile whose K was fetched last: for its V
+    uint32_t fine = 0;                               // that tile's blocks that are in a page
+    auto fetch_k = [&](uint32_t tile, StagedK<D, Q8> &t) {
+      if (tile * kBlocks >= base + 64) {
+        base += 64;
+        ids = in_pool(ids_next);
+        ids_next = pages_at(base + 64);
+      }
+      const uint32_t b0 = tile * kBlocks - base;
+      fine = (uint32_t)(__ballot(ids >= 0) >> b0) & ((1u << kBlocks) - 1);
+#pragma unroll
+      for (int i = 0; i < S::KL; ++i) {
+        const uint32_t r = (64 * wave + NT * i) / S::KPer;   // the load's first token, a lane's others in k_lane
+        const rsrc_t rs = block(__builtin_amdgcn_readlane(ids, b0 + r / 16));
+        const uint32_t place = (tile * T + r) & mask;
+        t.k[i] = bldx4<0>(rs, k_lane, place * S::KBytes);
+        if constexpr (Q8) t.s[i] = bldh(rs, ks_lane, a.ks_off + place * (D / 16));
+      }
+#pragma unroll
+      for (int i = 0; i < S::VL; ++i) v_page[i] = __builtin_amdgcn_readlane(ids, b0 + (64 * wave + NT * i) / S::VPer / 4);
+    };
+    auto fetch_v = [&](uint32_t tile, const int32_t *pages, StagedV<D, Q8> &t) {
+#pragma unroll
+      for (int i = 0; i < S::VL; ++i) {
+        const uint32_t r = 4 * ((64 * wave + NT * i) / S::VPer);
+        const rsrc_t rs = block(pages[i]);
+        const uint32_t place = (tile * T + r) & mask;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (Q8) t.v[i][j].x = bldx1<0>(rs, v_lane + j * S::KBytes, a.v_off + place * S::KBytes);
+          else t.v[i][j] = bldx2<0>(rs, v_lane + j * S::KBytes, a.v_off + place * S::KBytes);
+        }
+        if constexpr (Q8) t.s[i] = bldx2<0>(rs, vs_lane, a.vs_off + 2 * place);
+      }
+    };
+
+    StagedK<D, Q8> kt, kt1;
+    StagedV<D, Q8> vt;
+    int32_t pages[S::VL];                            // of V of the tile after the one in vt
+    fetch_k(first, kt);
+    uint32_t cur = fine;
+#pragma unroll
+    for (int i = 0; i < S::VL; ++i) pages[i] = v_page[i];
+    fetch_v(first, pages, vt);
+    fetch_k(first + 1, kt1);
+    uint32_t next_fine = fine;
+#pragma unroll
+    for (int i = 0; i < S::VL; ++i) pages[i] = v_page[i];
+    // the lane's query row; one that is not finite is taken as zeros, and marked
+    const int32_t m = rt * kRows + (int32_t)(32 * wave + n);
     const bool active = rt * kRows + (int32_t)(32 * wave) < rows;
     const int32_t b = p.row0 + min(m, rows - 1) / a.group, hd = kvh * a.group + min(m, rows - 1) % a.group;
     half8_t q[KS];
 #pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      u32x4 x = *reinterpret_cast<const u32x4 *>(a.q + b * a.ldq + (int64_t)hd * D + 16 * i + 8 * h);
+    for (int i = 0; i < KS; ++i)
+      q[i] = *reinterpret_cast<const half8_t *>(a.q + b * a.ldq + (int64_t)hd * D + 16 * i + 8 * h);
+    const int32_t limit = min(max(a.lens[b], 0), p.tokens);   // the tokens that the row sees
+    const bool whole = !__any(limit < p.tokens);
+    bool bad = nonfinite<KS>(q);
+    bad = __shfl_xor((int)bad, 32) || bad;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = m < rows ? x[j] ^ a.flip : 0u;
+    for (int i = 0; i < KS; ++i) {
+      u32x4 x = __builtin_bit_cast(u32x4, q[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = m < rows && !bad ? (x[j] & a.keep) ^ a.flip : 0u;
       q[i] = __builtin_bit_cast(half8_t, x);
     }
-    const int32_t limit = min(max(a.lens[b], 0), p.tokens);   // the tokens that the row sees
-    bool whole = !__any(limit < p.tokens);
-    const bool bad = Q8 && nonfinite<KS>(q);
     f32x16 o[DB];
 #pragma unroll
     for (int i = 0; i < DB; ++i)
@@ -292,177 +381,485 @@ __global__ __launch_bounds__(kPrefixThreads, D == 256 ? 1 : 2) void prefix_kerne
       for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
     float ref = -INFINITY, l = 0.f;
 
-    // The pages of 64 blocks of 16 tokens, a block a lane; those of the next 64 on their way.
-    auto pages_at = [&](uint32_t blk) {
-      const int64_t tok = (int64_t)(blk + lane) * 16;
-      int32_t page = -1;
-      if (tok < p.tokens) page = row[tok >> a.tok_shift];
-      return page;
-    };
-    uint32_t base = first * kBlocks;                 // of the blocks in ids
-    int32_t ids = pages_at(base), ids_next = pages_at(base + 64);
-    Staged<D, Q8> t;
-    uint32_t fine = 0;                               // blocks of the tile in t that are in a page
-    auto fetch = [&](uint32_t tile) {
-      if (tile * kBlocks >= base + 64) {
-        base += 64;
-        ids = ids_next;
-        ids_next = pages_at(base + 64);
-      }
-      const uint32_t b0 = tile * kBlocks - base;
-      const bool ok = ids >= 0 && ids < a.num_pages;
-      fine = (uint32_t)(__ballot(ok) >> b0) & ((1u << kBlocks) - 1);
-      const int32_t safe = ok ? ids : 0;
-      const uint32_t mask = (1u << a.tok_shift) - 1;
-#pragma unroll
-      for (int i = 0; i < S::KL; ++i) {
-        const uint32_t id = tid + kPrefixThreads * i, r = id / S::KPer, c = id % S::KPer;
-        const uint32_t place = (tile * T + r) & mask;
-        const uint8_t *at = kv + (uint64_t)(uint32_t)__shfl(safe, (int)(b0 + r / 16)) * (uint64_t)a.page_bytes;
-        t.k[i] = *reinterpret_cast<const u32x4 *>(at + place * (Q8 ? D : 2 * D) + 16 * c);
-        if constexpr (Q8) t.ks[i] = *reinterpret_cast<const uint16_t *>(at + a.ks_off + 2 * (place * (D / 32) + c / 2));
-      }
-      const uint32_t c = tid / S::VPer, d0 = 4 * (tid % S::VPer), r = 16 * (c >> 1) + 4 * (c & 1);
-      const uint32_t place = (tile * T + r) & mask;
-      const uint8_t *at = kv + (uint64_t)(uint32_t)__shfl(safe, (int)(b0 + c / 2)) * (uint64_t)a.page_bytes;
-      t.fine = (fine >> (c / 2)) & 1;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t tok = place + (j & 3) + 8 * (j >> 2);
-        if constexpr (Q8) t.v[j].x = *reinterpret_cast<const uint32_t *>(at + a.v_off + tok * D + d0);
-        else t.v[j] = *reinterpret_cast<const u32x2 *>(at + a.v_off + tok * (2 * D) + 2 * d0);
-      }
-      if constexpr (Q8) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          t.vs[j] = *reinterpret_cast<const u32x2 *>(at + a.vs_off + 2 * (((d0 / 32) << a.tok_shift) + place + 8 * j));
-      }
-    };
-
-    fetch(first);
     __syncthreads();                                 // the segment before is done with LDS
-    write_tile<D, Q8>(t, tiles);
-    uint32_t cur = fine;
-    if (first + 1 < last) fetch(first + 1);
+    kt.write(lds_k);
+    vt.write(lds_v);
+    kt1.write(lds_k + S::KTile);
+    fetch_k(first + 2, kt);
+    fetch_v(first + 1, pages, vt);
+#pragma unroll
+    for (int i = 0; i < S::VL; ++i) pages[i] = v_page[i];
+    uint32_t after = fine;
     __syncthreads();
+
+    // Between two steps: the scores of the step to come, and the weights of the one done (none before the first).
+    f32x16 s;
+    half8_t hi[2], lo[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) hi[k][j] = lo[k][j] = (_Float16)0.f;
+    constexpr int kSlots = KS + 2 * DB, kRing = 4;
+    // The buffers of tiles t - 1, t, t + 1 and t + 2 (that of t + 2 is that of t - 1). Before the first tile there are no
+    // weights, and any finite V will do.
+    uint32_t past = 0, now = 0, ahead = 1, spare = 2;
+    if (active) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[j] = 0.f;
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, lds_k[k_at + 2 * i]), q[i], s, 0, 0, 0);
+    }
+    // The way of the next tiles: half of the waves, one on each SIMD, go it before their steps and the others after
+    // them, so that the matrix cores have work meanwhile.
+    auto stage = [&](uint32_t tile) {
+      kt.write(lds_k + spare * S::KTile);
+      vt.write(lds_v + ahead * S::VTile);
+      fetch_k(tile + 3, kt);
+      fetch_v(tile + 2, pages, vt);
+#pragma unroll
+      for (int i = 0; i < S::VL; ++i) pages[i] = v_page[i];
+    };
     for (uint32_t tile = first; tile < last; ++tile) {
-      const u32x4 *lds = tiles + ((tile - first) & 1) * (kElems / 4);
-      uint32_t next = 0;
-      if (tile + 1 < last) {
-        write_tile<D, Q8>(t, tiles + ((tile - first + 1) & 1) * (kElems / 4));
-        next = fine;
-        if (tile + 2 < last) fetch(tile + 2);
-      }
+      if (wave < NT / 128) stage(tile);
       if (active) {
-        f32x16 s[TB];
 #pragma unroll
         for (int tb = 0; tb < TB; ++tb) {
+          if (!(whole && cur == (1u << kBlocks) - 1)) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) s[tb][j] = 0.f;
+            for (int j = 0; j < 16; ++j) {
+              const int32_t tok = 32 * tb + 8 * (j >> 2) + 4 * (int)h + (j & 3);
+              const bool seen = (cur >> (2 * tb + (j >> 3)) & 1) && (int32_t)(tile * T) + tok < limit;
+              s[j] = seen ? s[j] : -INFINITY;
+            }
+          }
+          float top = s[0];
 #pragma unroll
-          for (int i = 0; i < KS; ++i)
-            s[tb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8_t, lds[k_place<D>(32 * tb + n, 2 * i + h)]), q[i],
-                                                           s[tb], 0, 0, 0);
-        }
-        const bool full = whole && cur == (1u << kBlocks) - 1;
-        auto seen = [&](int tb, int j) {             // the token of the lane's score j of block tb is seen by its row
-          const int32_t tok = 32 * tb + 8 * (j >> 2) + 4 * (int)h + (j & 3);
-          return (cur >> (2 * tb + (j >> 3)) & 1) && (int32_t)(tile * T) + tok < limit;
-        };
-        if (!full) {
+          for (int j = 1; j < 16; ++j) top = fmaxf(top, s[j]);
+          top *= a.scale_log2;
+          const bool moves = __any(top - ref > kHigh);   // ref -inf: moves for any score, not for none (NaN)
+          float keep = 1.0f;
+          if (moves) {
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float to = fmaxf(ref, top - kLow);
+            keep = to == ref ? 1.0f : __builtin_amdgcn_exp2f(ref - to);
+            ref = to;
+            l *= keep;
+          }
+          const float off = ref == -INFINITY ? 0.f : -ref;   // no token so far: all weights are 2^-inf
+          // One step in slots, in the order written: a matrix instruction, the read of the operand of the one four
+          // slots on, a part of the softmax. Past the last tile the scores are of what is there, and nobody reads them.
+          const u32x4 *ks = lds_k + (tb + 1 < TB ? now : ahead) * S::KTile + k_at + 32 * ((tb + 1) % TB) * S::KRow;
+          const u32x4 *vs = lds_v + (tb > 0 ? now : past) * S::VTile + v_at + 4 * ((tb + TB - 1) % TB);
+          auto read = [&](int i) { return i < KS ? ks[2 * i] : vs[2 * ((i - KS) / DB) + 32 * ((i - KS) % DB) * S::VRow]; };
+          u32x4 ring[kRing];
+          f32x16 next;
 #pragma unroll
-          for (int tb = 0; tb < TB; ++tb)
+          for (int j = 0; j < 16; ++j) next[j] = 0.f;
+          u32x4 hi_now[2], lo_now[2];                // pairs of weights
+          float y0 = 0.f;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) s[tb][j] = seen(tb, j) ? s[tb][j] : -INFINITY;
-        }
-        float top = s[0][0];
+          for (int i = 0; i < kRing; ++i) ring[i] = read(i);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int tb = 0; tb < TB; ++tb)
+          for (int i = 0; i < kSlots; ++i) {
+            const half8_t x = __builtin_bit_cast(half8_t, ring[i % kRing]);
+            if (i < KS) {
+              next = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, q[i < KS ? i : 0], next, 0, 0, 0);
+            } else {
+              f32x16 &to = o[(i - KS) % DB];
+              to = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, hi[(i - KS) / DB], to, 0, 0, 0);
+              if constexpr (PAIRS) to = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, lo[(i - KS) / DB], to, 0, 0, 0);
+            }
+            if (i + kRing < kSlots) ring[i % kRing] = read(i + kRing);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) top = fmaxf(top, s[tb][j]);
-        top = top > -INFINITY ? top * a.scale_log2 : top;
-        if (__any(top - ref > kHigh)) {              // ref -inf: moves for any score, not for none (NaN)
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const float now = fmaxf(ref, top - kLow);
-          const float keep = now == ref ? 1.0f : __builtin_amdgcn_exp2f(ref - now);
-          ref = now;
-          l *= keep;
-#pragma unroll
-          for (int i = 0; i < DB; ++i) o[i] *= keep;
-        }
-#pragma unroll
-        for (int tb = 0; tb < TB; ++tb) {
-          float y[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            y[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][j], a.scale_log2, -ref));
-            if (!full) y[j] = seen(tb, j) ? y[j] : 0.f;
-            l += y[j];
+            for (int j = 16 * i / kSlots; j < 16 * (i + 1) / kSlots; ++j) {
+              float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], a.scale_log2, off));
+              asm volatile("" : "+v"(y));            // here and not where it is used
+              l += y;
+              asm volatile("" : "+v"(l));
+              if ((j & 1) == 0) {
+                y0 = y;
+                continue;
+              }
+              const h2_t x2 = h2_t{(_Float16)y0, (_Float16)y};
+              uint32_t bits = __builtin_bit_cast(uint32_t, x2);
+              asm volatile("" : "+v"(bits));
+              hi_now[j >> 3][(j & 7) >> 1] = bits;
+              if constexpr (PAIRS) {
+                bits = __builtin_bit_cast(uint32_t, h2_t{(_Float16)(y0 - (float)x2[0]), (_Float16)(y - (float)x2[1])});
+                asm volatile("" : "+v"(bits));
+                lo_now[j >> 3][(j & 7) >> 1] = bits;
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            half8_t hi, lo;
+            hi[k] = __builtin_bit_cast(half8_t, hi_now[k]);
+            if constexpr (PAIRS) lo[k] = __builtin_bit_cast(half8_t, lo_now[k]);
+          }
+          s = next;
+          if (moves) {                               // the products so far belong to the reference of before
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              hi[j] = (_Float16)y[8 * k + j];
-              if constexpr (PAIRS) lo[j] = (_Float16)(y[8 * k + j] - (float)hi[j]);
-            }
-#pragma unroll
-            for (int i = 0; i < DB; ++i) {
-              const half8_t v = __builtin_bit_cast(half8_t, lds[kElems / 8 + v_place<D>(32 * i + n, 2 * (2 * tb + k) + h)]);
-              o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, hi, o[i], 0, 0, 0);
-              if constexpr (PAIRS) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, lo, o[i], 0, 0, 0);
-            }
+            for (int i = 0; i < DB; ++i) o[i] *= keep;
           }
         }
       }
-      cur = next;
+      if (wave >= NT / 128) stage(tile);
+      cur = next_fine;
+      next_fine = after;
+      after = fine;
+      past = now;
+      now = ahead;
+      ahead = spare;
+      spare = past;
       __syncthreads();
     }
-    if (active && m < rows) {
-      float *part = a.parts + (int64_t)(w + p.seg0 + seg) * part_floats(D);
-      const int r = 32 * (int)wave + (int)n;
+    if (active) {                                    // the products of the last block
+      const u32x4 *vs = lds_v + past * S::VTile + v_at + 4 * (TB - 1);
+#pragma unroll
+      for (int i = 0; i < 2 * DB; ++i) {
+        const half8_t x = __builtin_bit_cast(half8_t, vs[2 * (i / DB) + 32 * (i % DB) * S::VRow]);
+        o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, hi[i / DB], o[i % DB], 0, 0, 0);
+        if constexpr (PAIRS) o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, lo[i / DB], o[i % DB], 0, 0, 0);
+      }
+    }
+    l += __shfl_xor(l, 32);
+    if (m < rows) {
+      float *part = a.parts + (int64_t)(w + p.seg0 + seg) * part_floats(D, a.part_rows);
+      const int r = m - rt * kRows;
       if (bad && ref > -INFINITY) l = __builtin_nanf("");
 #pragma unroll
       for (int i = 0; i < DB; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<f32x4 *>(part + r * D + 32 * i + 8 * j + 4 * h) = f32x4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+          *reinterpret_cast<f32x4 *>(part + r * D + 32 * i + 8 * j + 4 * h) =
+              f32x4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+      if (h == 0) *reinterpret_cast<f32x2 *>(part + a.part_rows * D + 2 * r) = f32x2{ref, l};
     }
-    l += __shfl_xor(l, 32);
-    if (active && m < rows && h == 0) {
-      float *part = a.parts + (int64_t)(w + p.seg0 + seg) * part_floats(D);
-      *reinterpret_cast<f32x2 *>(part + kRows * D + 2 * (32 * wave + n)) = f32x2{ref, l};
-    }
-    at += last - first;
   }
+}
+
+// ---- the rows' own tokens ------------------------------------------------------------------------
+
+// A wave's part of one head tile of one row's own tokens.
+struct OwnSegment {
+  uint32_t u0, u1;           // the head tile on the line
+  uint32_t at, end;          // the wave's part of it; at in the lead: a step before the first, all masked
+  int32_t b, ht;
+  Own seen;
+  int32_t h0, rows;          // its first head, heads
+  const uint8_t *kv;         // its KV head's part of page 0
+  const int32_t *row;        // the row's entries
+};
+
+// The segment at unit `at` < end, at or after row b, whose own tokens start at row_at on the line.
+__device__ __forceinline__ OwnSegment own_segment(const PrefixArgs &a, const Plan &plan, uint32_t at, uint32_t end, int32_t b,
+                                                  uint32_t row_at) {
+  OwnSegment s;
+  for (;;) {
+    const int32_t g = uniform(plan.group_of(b, a.groups));
+    s.seen = own_of(a, scalar_load(a.lens + b), g < 0 ? 0 : uniform(plan.g[g].tokens));
+    if (at - row_at < s.seen.units * (uint32_t)a.head_tiles) break;
+    row_at += s.seen.units * (uint32_t)a.head_tiles;
+    ++b;
+  }
+  s.b = b;
+  s.ht = (int32_t)((at - row_at) / s.seen.units);
+  s.u0 = row_at + (uint32_t)s.ht * s.seen.units;
+  s.u1 = s.u0 + s.seen.units;
+  s.end = min(end, s.u1);
+  s.at = at < s.u0 + a.own_lead && s.u0 + a.own_lead < s.end ? s.u0 + a.own_lead : at;
+  const int32_t kvh = s.ht / a.tiles_per_kv, first_head = (s.ht - kvh * a.tiles_per_kv) * kHeads;
+  s.h0 = kvh * a.group + first_head;
+  s.rows = min(kHeads, a.group - first_head);
+  s.kv = a.pool + kvh * a.head_bytes;
+  s.row = a.table + b * a.ld_table;
+  return s;
+}
+
+// Wave v's part [at, end) of the line of own work, as the waves of paged_attn.hip take theirs: the loads are issued in
+// one order everywhere, the next step's K while this one's softmax and products run, its V from then on.
+template <int D, bool Q8>
+__device__ __forceinline__ void own_work(const PrefixArgs &a, const Plan &plan, uint32_t v, uint32_t at, uint32_t end, int32_t from_b,
+                                         uint32_t from_at) {
+  using T = Tile<D, Q8>;
+  constexpr int VJ = T::VJ;
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+  const uint32_t vs_lane = 2 * ((((VJ * (uint32_t)c) / 32) << a.tok_shift) + 4 * g);   // the lane's V scales
+  T t;
+  half8_t q[1][T::KD];
+  Block blk[2];
+  int32_t page[2];                                   // of the step in t; below 0: none
+  OwnSegment cur = own_segment(a, plan, at, end, from_b, from_at), fetch = cur;   // fetch: of the step in t, fetch.at that step
+  auto token = [&](int st) { return fetch.seen.base + ((int32_t)(fetch.at - fetch.u0) - a.own_lead) * kTile + 16 * st; };
+  auto look_up = [&]() {
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      const int32_t tok = token(st);
+      page[st] = fetch.at < end && tok >= 0 && tok < fetch.seen.len ? scalar_load(fetch.row + (tok >> a.tok_shift)) : -1;
+    }
+  };
+  auto locate = [&]() {
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      if (page[st] >= a.num_pages) page[st] = -1;
+      const uint32_t p = (uint32_t)max(page[st], 0);
+      blk[st].r = make_rsrc(fetch.kv + (uint64_t)p * (uint64_t)a.page_bytes, page[st] < 0 ? 0u : (uint32_t)a.head_bytes);
+      blk[st].place = (uint32_t)token(st) & ((1u << a.tok_shift) - 1);
+    }
+  };
+  auto load_q = [&]() {                              // heads past the tile's read as zeros: their lanes' own offsets are out of range
+    const uint16_t *from = a.q + uniform(fetch.b) * a.ldq + (int64_t)uniform(fetch.h0) * D;
+    const rsrc_t r = make_rsrc(from, (uint32_t)uniform(fetch.rows) * D * 2);
+#pragma unroll
+    for (int i = 0; i < T::KD; ++i)
+      q[0][i] = __builtin_bit_cast(half8_t, bldx4<0>(r, c * (2 * D) + 32 * g, 128 * (i >> 1) + 16 * (i & 1)));
+  };
+  look_up();
+  locate();
+  load_q();
+  __builtin_amdgcn_sched_barrier(0);
+  load_k<D, Q8>(a, blk, t);
+  __builtin_amdgcn_sched_barrier(0);
+  load_v<D, Q8>(a, blk, vs_lane, t);
+  __builtin_amdgcn_sched_barrier(0);
+  bool more = true;
+  while (more) {
+    f32x4 o[1][VJ];
+#pragma unroll
+    for (int j = 0; j < VJ; ++j) o[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float ref = -INFINITY, l = 0.f;
+    bool inside = true, fresh = true, bad = false;   // the step in t is of segment cur, and its first; q is not finite
+    while (inside) {
+      const int32_t t0 = token(0);
+      const bool full = t0 >= cur.seen.first && t0 + kTile <= cur.seen.len && page[0] >= 0 && page[1] >= 0;
+      uint32_t valid = 0xFF;                         // of the lane's eight tokens
+      if (!full) {
+        valid = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int32_t tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
+          valid |= (uint32_t)(tok >= cur.seen.first && tok < cur.seen.len && page[i >> 2] >= 0) << i;
+        }
+      }
+      more = fetch.at + 1 < end;
+      if (++fetch.at == fetch.end) {
+        inside = false;
+        if (more) fetch = own_segment(a, plan, fetch.at, end, fetch.b, fetch.u0 - fetch.seen.units * (uint32_t)fetch.ht);
+      }
+      look_up();
+      if (fresh) {                                   // a head that is not finite is taken as zeros, and marked
+        bad = nonfinite<T::KD>(q[0]);
+        bad = __shfl_xor((int)bad, 16) || bad;
+        bad = __shfl_xor((int)bad, 32) || bad;
+#pragma unroll
+        for (int i = 0; i < T::KD; ++i) {
+          u32x4 x = __builtin_bit_cast(u32x4, q[0][i]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = bad ? 0u : (x[j] & a.keep) ^ a.flip;
+          q[0][i] = __builtin_bit_cast(half8_t, x);
+        }
+        fresh = false;
+      }
+      f32x4 x[2][1];
+#pragma unroll
+      for (int st = 0; st < 2; ++st) scores<D, Q8, 1>(t, st, q, x[st]);
+      locate();
+      if (more && !inside) load_q();
+      load_k<D, Q8>(a, blk, t);
+      float y[8], top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = x[i >> 2][0][i & 3] * a.scale_log2;
+      if (!full) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = (valid >> i & 1) ? y[i] : -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
+      if (__any(top - ref > kHigh)) {                // ref -inf: moves for any score, not for none (NaN)
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float to = fmaxf(ref, top - kLow);
+        const float keep = to == ref ? 1.0f : __builtin_amdgcn_exp2f(ref - to);
+        ref = to;
+        l *= keep;
+#pragma unroll
+        for (int j = 0; j < VJ; ++j) o[0][j] *= keep;
+      }
+      half8_t hi[1], lo[1];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_exp2f(y[i] - ref);
+      if (!full) {                                   // masked places may hold anything: zero times NaN is NaN
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = (valid >> i & 1) ? y[i] : 0.f;
+        if constexpr (Q8) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t m = (valid >> i & 1) ? 0u : (i & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+            t.vs[i >> 2][(i & 3) >> 1] &= ~m;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < T::VW; ++k) t.v[i][k] = (valid >> i & 1) ? t.v[i][k] : 0u;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        l += y[i];
+        hi[0][i] = (_Float16)y[i];
+        lo[0][i] = (_Float16)(y[i] - (float)hi[0][i]);
+      }
+      accumulate<D, Q8, 1>(t, hi, lo, o);
+      load_v<D, Q8>(a, blk, vs_lane, t);
+    }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (bad && ref > -INFINITY) l = __builtin_nanf("");
+    if (c < cur.rows) {
+      float *part = a.own_parts + (int64_t)(v + (uint32_t)(cur.b * a.head_tiles + cur.ht)) * part_floats(D, a.own_rows);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < VJ; j += 4)
+          *reinterpret_cast<f32x4 *>(part + c * D + VJ * (4 * g + i) + j) = f32x4{o[0][j][i], o[0][j + 1][i], o[0][j + 2][i], o[0][j + 3][i]};
+      if (g == 0) *reinterpret_cast<f32x2 *>(part + a.own_rows * D + 2 * c) = f32x2{ref, l};
+    }
+    cur = fetch;
+  }
+}
+
+// ---- the launch ----------------------------------------------------------------------------------
+
+template <int D, bool Q8, bool PAIRS>
+__global__ __launch_bounds__(64 * prefix_waves(D), D == 256 ? 1 : 2) void prefix_kernel(PrefixArgs a) {
+  constexpr int W = prefix_waves(D), NT = 64 * W, kRows = NT / 2, kPer = (kMaxGroups + 1) / NT;
+  extern __shared__ __align__(16) u32x4 tiles[];
+  __shared__ Plan plan;
+  const int32_t tid = threadIdx.x, wave = uniform(tid >> 6);
+  if constexpr (Q8) __builtin_amdgcn_s_setreg(1 | (23 << 6) | (0 << 11), 1);   // hwreg(MODE, 23, 1): FP16_OVFL
+
+  // the groups' first rows: a thread's in order, then the largest of the threads before
+  uint32_t lead[kPer], most = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int32_t g = kPer * tid + i, s = g <= a.groups ? a.starts[g] : 0;
+    most = max(most, (uint32_t)min(max(s, 0), a.batch));
+    lead[i] = most;
+  }
+  const uint32_t upto = scan_max(most);
+  if ((tid & 63) == 63) plan.red[0][wave] = upto;
+  __syncthreads();
+  const uint32_t left = (uint32_t)__shfl_up((int)upto, 1);
+  uint32_t before = (tid & 63) ? left : 0;
+  for (int k = 0; k < wave; ++k) before = max(before, plan.red[0][k]);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) plan.lead[kPer * tid + i] = (int32_t)max(lead[i], before);
+  __syncthreads();
+  uint32_t units = 0, segs = 0, shared, all_segs;
+  GroupPlan mine[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int32_t g = kPer * tid + i;
+    mine[i] = GroupPlan{0, 0, 0, 0, units, segs};
+    if (g >= a.groups) continue;
+    GroupPlan &p = mine[i];
+    p.row0 = plan.lead[g];
+    const int32_t rows = plan.lead[g + 1] - p.row0;
+    if (rows > 1) {
+      const int32_t len = min(max(a.lens[p.row0], 0), a.max_len);
+      p.tokens = min(max(a.prefix[g], 0), len) >> a.tok_shift << a.tok_shift;   // whole pages
+    }
+    p.units = p.tokens ? (p.tokens + tile_tokens(D) - 1) / tile_tokens(D) + kLead : 0;
+    p.row_tiles = p.units ? (int32_t)(((int64_t)rows * a.group + kRows - 1) / kRows) : 0;
+    segs += (uint32_t)(p.row_tiles * a.kv_heads);
+    units += (uint32_t)(p.row_tiles * a.kv_heads) * (uint32_t)p.units;
+  }
+  scan_two<W>(units, segs, shared, all_segs, plan);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int32_t g = kPer * tid + i;
+    if (g >= a.groups) continue;
+    mine[i].unit0 += units;
+    mine[i].seg0 += segs;
+    plan.g[g] = mine[i];
+    if (blockIdx.x == 0) a.plan[g] = mine[i];
+  }
+  __syncthreads();
+  // the rows' own tokens, a run of rows for each thread
+  const int32_t per = (a.batch + NT - 1) / NT, my_b = tid * per;
+  uint32_t my_units = 0, unused = 0, own, none;
+  for (int32_t b = my_b; b < min(my_b + per, a.batch); ++b) {
+    const int32_t g = plan.group_of(b, a.groups);
+    my_units += own_of(a, a.lens[b], g < 0 ? 0 : plan.g[g].tokens).units * (uint32_t)a.head_tiles;
+  }
+  uint32_t my_at = my_units;
+  scan_two<W>(my_at, unused, own, none, plan);
+
+  // Both kinds of work get workgroups by their cost.
+  uint32_t workers = 0;
+  if (shared) {
+    const float x = (float)shared * a.shared_cost * W, y = (float)own;
+    workers = (uint32_t)((float)gridDim.x * (x / (x + y)) + 0.5f);
+    workers = min(max(workers, 1u), gridDim.x - (own ? 1u : 0u));
+  }
+  const Split split{shared, workers, own, min((gridDim.x - workers) * W, a.own_most)};
+  if (blockIdx.x == gridDim.x - 1) {
+    if (tid == 0) *a.split = split;
+    uint32_t u = my_at;
+    for (int32_t b = my_b; b < min(my_b + per, a.batch); ++b) {
+      const int32_t g = plan.group_of(b, a.groups);
+      const uint32_t n = own_of(a, a.lens[b], g < 0 ? 0 : plan.g[g].tokens).units;
+      a.rows[b] = RowPlan{g, u, n};
+      u += n * (uint32_t)a.head_tiles;
+    }
+  }
+  if (blockIdx.x < workers) {
+    const Line line = make_line(shared, workers);
+    if (blockIdx.x >= line.waves) return;
+    shared_work<D, Q8, PAIRS>(a, plan, tiles, blockIdx.x, line.start(blockIdx.x), line.start(blockIdx.x + 1));
+    return;
+  }
+  if (own == 0) return;
+  const Line line = make_line(own, split.waves);
+  const uint32_t v0 = (blockIdx.x - workers) * W;
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    const uint32_t at = line.start(v0 + k);
+    if (at >= my_at && at - my_at < my_units) {
+      plan.found[0][k] = (uint32_t)my_b;
+      plan.found[1][k] = my_at;
+    }
+  }
+  __syncthreads();
+  const uint32_t v = v0 + wave;
+  if (v >= line.waves) return;
+  own_work<D, Q8>(a, plan, v, line.start(v), line.start(v + 1), (int32_t)uniform(plan.found[0][wave]), uniform(plan.found[1][wave]));
 }
 
 // ---- the join ------------------------------------------------------------------------------------
 
-// D / 4 threads a row of the output: its tail's sums and the parts of its shared tokens.
+// D / 4 threads a row of the output: the parts of its shared tokens, and of its own.
 template <int D>
-__global__ __launch_bounds__(256) void prefix_join_kernel(PrefixArgs a, uint32_t workers) {
+__global__ __launch_bounds__(256) void prefix_join_kernel(PrefixArgs a) {
   constexpr uint32_t kLanes = D / 4;
   const int64_t row = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
   const uint32_t d = 4 * (threadIdx.x % kLanes);
   if (row >= (int64_t)a.batch * a.heads) return;
-  const int32_t b = (int32_t)(row / a.heads), hd = (int32_t)(row - (int64_t)b * a.heads);
-  f32x4 o = *reinterpret_cast<const f32x4 *>(a.tail + row * D + d);
-  const f32x2 ml = *reinterpret_cast<const f32x2 *>(a.tail_ml + 2 * row);
-  float m = ml[0], l = ml[1];
-  const int32_t g = a.group_of[b];
-  if (g >= 0) {
-    const GroupPlan p = a.plan[g];
-    const Line line = make_line(*a.total, workers);
-    const int32_t kvh = hd / a.group, q = (b - p.row0) * a.group + hd - kvh * a.group, rt = q / kRows, r = q - rt * kRows;
-    const uint32_t seg = (uint32_t)(kvh * p.row_tiles + rt), u0 = p.unit0 + seg * (uint32_t)p.units;
-    const uint32_t w0 = line.holder(u0), w1 = line.holder(u0 + (uint32_t)p.units - 1);
+  const int32_t b = (int32_t)(row / a.heads), hd = (int32_t)(row - (int64_t)b * a.heads), kvh = hd / a.group;
+  const Split split = *a.split;
+  const RowPlan rp = a.rows[b];
+  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+  auto join = [&](const float *parts, uint32_t first, uint32_t last, int32_t rows, int32_t r) {
 #pragma unroll 4
-    for (uint32_t w = w0; w <= w1; ++w) {
-      const float *part = a.parts + (int64_t)(w + p.seg0 + seg) * part_floats(D);
+    for (uint32_t w = first; w <= last; ++w) {
+      const float *part = parts + (int64_t)w * part_floats(D, rows);
       const f32x4 x = *reinterpret_cast<const f32x4 *>(part + r * D + d);
-      const f32x2 y = *reinterpret_cast<const f32x2 *>(part + kRows * D + 2 * r);
+      const f32x2 y = *reinterpret_cast<const f32x2 *>(part + rows * D + 2 * r);
       const float now = fmaxf(m, y[0]);
       const float keep = m == now ? 1.0f : __builtin_amdgcn_exp2f(m - now);
       const float f = y[0] == now ? 1.0f : __builtin_amdgcn_exp2f(y[0] - now);
@@ -470,6 +867,20 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(PrefixArgs a, uint32_t
       l = l * keep + y[1] * f;
       m = now;
     }
+  };
+  if (rp.group >= 0) {
+    constexpr int32_t kRows = 32 * prefix_waves(D);
+    const GroupPlan p = a.plan[rp.group];
+    const Line line = make_line(split.shared, split.workers);
+    const int32_t q = (b - p.row0) * a.group + hd - kvh * a.group, rt = q / kRows;
+    const uint32_t seg = (uint32_t)(kvh * p.row_tiles + rt), u0 = p.unit0 + seg * (uint32_t)p.units;
+    join(a.parts, line.holder(u0 + kLead) + p.seg0 + seg, line.holder(u0 + (uint32_t)p.units - 1) + p.seg0 + seg, a.part_rows, q - rt * kRows);
+  }
+  if (rp.units) {
+    const Line line = make_line(split.own, split.waves);
+    const int32_t head = hd - kvh * a.group, ht = kvh * a.tiles_per_kv + head / kHeads;
+    const uint32_t u0 = rp.unit0 + (uint32_t)ht * rp.units, seg = (uint32_t)(b * a.head_tiles + ht);
+    join(a.own_parts, line.holder(u0) + seg, line.holder(u0 + rp.units - 1) + seg, a.own_rows, head % kHeads);
   }
   o *= l > 0.f ? 1.0f / l : l;                       // no token: 0; NaN sums stay NaN
   const int64_t to = b * a.ldo + (int64_t)hd * D + d;
@@ -488,62 +899,62 @@ namespace {
 
 bool prefix_misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
-// Workgroups that are resident at once.
-int64_t prefix_resident(int64_t dim) { return dim == 256 ? 256 : 512; }
+constexpr int64_t kResident = 256;                 // workgroups that are resident at once
 
-// Where things lie in the workspace, in bytes, and what the host can say of the line: at most `segments` segments
-// (a group's query rows of a KV head fill all their tiles but one) of at most `units` in all.
+// Where things lie in the workspace, in bytes, and the rows of the parts. A group's query rows of a KV head fill
+// all their tiles but one, so there are at most `segments` segments of shared work.
 struct PrefixSpace {
-  int64_t plan, from, group_of, tail, tail_ml, tail_ws, parts, bytes;
-  int64_t segments, units, workers;
+  int64_t plan, rows, parts, own_parts, bytes;
+  int32_t part_rows, own_rows, own_waves;
 };
 
 int prefix_space(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t groups, int64_t max_len, int64_t max_tail,
                  PrefixSpace *s) {
-  const int64_t dim = pool->head_dim, group = heads / pool->kv_heads, tile = kElems / dim;
-  const int64_t whole = batch * group / kRows;       // rows are at most batch * group in all, a group has two rows or more
-  s->segments = pool->kv_heads * (whole + (groups < batch / 2 ? groups : batch / 2));
-  s->units = s->segments * ((max_len + tile - 1) / tile);
-  if (s->units > 0x7FFFFFFF) return QG_ERR_SHAPE;
-  const int64_t most = prefix_resident(dim);
-  s->workers = s->units < most ? s->units : most;
+  const int64_t dim = pool->head_dim, group = heads / pool->kv_heads, waves = prefix_waves((int)dim), rows = 32 * waves;
+  const int64_t whole = batch * group / rows;        // rows are at most batch * group in all, a group has two rows or more
+  const int64_t segments = pool->kv_heads * (whole + (groups < batch / 2 ? groups : batch / 2));
+  const int64_t units = max_len ? segments * ((max_len + tile_tokens((int)dim) - 1) / tile_tokens((int)dim) + kLead) : 0;
+  const int64_t head_tiles = pool->kv_heads * ((group + kHeads - 1) / kHeads);
+  const int64_t lead = own_lead((int)dim, pool->kind == QG_KV_Q8);
+  const auto steps = [lead](int64_t n) { return (n + kTile - 1) / kTile + 1 + lead; };   // from the middle of one on: one more
+  if (units > 0x7FFFFFFF || batch * head_tiles * steps(max_len) > 0x7FFFFFFF) return QG_ERR_SHAPE;
+  // what is past the prefix's last whole page is a row's own, too
+  const int64_t tail = max_tail + pool->page_tokens < max_len ? max_tail + pool->page_tokens : max_len;
+  const int64_t own = batch * head_tiles * steps(tail), workers = units < kResident ? units : kResident;
+  s->own_waves = (int32_t)(own < kResident * waves ? own : kResident * waves);
+  s->part_rows = (int32_t)(batch * group < rows ? batch * group : rows);
+  s->own_rows = (int32_t)(group < kHeads ? group : kHeads);
   const auto up = [](int64_t n) { return (n + 15) / 16 * 16; };
-  s->plan = 16;
-  s->from = s->plan + groups * (int64_t)sizeof(GroupPlan);
-  s->group_of = s->from + up(4 * batch);
-  s->tail = s->group_of + up(4 * batch);
-  s->tail_ml = s->tail + 4 * batch * heads * dim;
-  s->tail_ws = s->tail_ml + up(8 * batch * heads);
-  s->parts = s->tail_ws + up(attn_tail_bytes(pool, batch, heads, max_tail));
-  s->bytes = s->parts + 4 * part_floats((int32_t)dim) * (s->workers ? s->workers + s->segments - 1 : 0);
+  s->plan = up(sizeof(Split));
+  s->rows = s->plan + up(groups * (int64_t)sizeof(GroupPlan));
+  s->parts = s->rows + up(batch * (int64_t)sizeof(RowPlan));
+  s->own_parts = s->parts + up(4 * part_floats((int32_t)dim, s->part_rows) * (workers ? workers + segments - 1 : 0));
+  s->bytes = s->own_parts + 4 * part_floats((int32_t)dim, s->own_rows) * (batch ? s->own_waves + batch * head_tiles - 1 : 0);
   return QG_OK;
 }
 
-// The tail's likely length: what is past the prefix's last whole page too.
-int64_t prefix_tail(const qg_kv_pool *pool, int64_t max_len, int64_t max_tail) {
-  const int64_t n = max_tail + pool->page_tokens;
-  return n < max_len ? n : max_len;
-}
-
 int prefix_shape(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t groups, int64_t max_len, int64_t max_tail) {
-  if (int st = attn_shape_check(pool, batch, heads, max_len)) return st;
+  KvLayout L;
+  if (int st = kv_pool_layout(pool, &L)) return st;
+  if (batch < 0 || heads < 1 || heads % pool->kv_heads || heads > (1 << 22) || batch > (1 << 22) / heads) return QG_ERR_SHAPE;
+  if (max_len < 0 || max_len > (1 << 30)) return QG_ERR_SHAPE;
   if (groups < 0 || groups > kMaxGroups || groups > batch || max_tail < 0 || max_tail > (1 << 30)) return QG_ERR_SHAPE;
   return QG_OK;
 }
 
 template <int D, bool Q8>
-int launch_prefix(const PrefixArgs &a, int64_t workers, hipStream_t s) {
-  constexpr size_t kLds = 2 * 2 * kElems * sizeof(uint16_t);
-  const dim3 grid((unsigned)workers), block(kPrefixThreads);
-  if (a.out_f32) return launch(prefix_kernel<D, Q8, true>, grid, block, kLds, s, a);
-  return launch(prefix_kernel<D, Q8, false>, grid, block, kLds, s, a);
+int launch_prefix(const PrefixArgs &a, hipStream_t s) {
+  const dim3 grid(kResident), block(64 * prefix_waves(D));
+  if (a.out_f32) return launch(prefix_kernel<D, Q8, true>, grid, block, Shape<D, Q8>::kLds, s, a);
+  return launch(prefix_kernel<D, Q8, false>, grid, block, Shape<D, Q8>::kLds, s, a);
 }
 
 template <int D>
-int launch_join(const PrefixArgs &a, int64_t workers, hipStream_t s) {
+int launch_dim(const PrefixArgs &a, bool q8, hipStream_t s) {
+  if (int st = q8 ? launch_prefix<D, true>(a, s) : launch_prefix<D, false>(a, s)) return st;
   constexpr int64_t kPer = 256 / (D / 4);
   const int64_t rows = (int64_t)a.batch * a.heads;
-  return launch(prefix_join_kernel<D>, dim3((unsigned)((rows + kPer - 1) / kPer)), dim3(256), 0, s, a, (uint32_t)workers);
+  return launch(prefix_join_kernel<D>, dim3((unsigned)((rows + kPer - 1) / kPer)), dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -559,7 +970,7 @@ int qg_prefix_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t hea
   if (!bytes) return QG_ERR_NULL;
   if (int st = prefix_shape(pool, batch, heads, groups, max_len, max_tail)) return st;
   PrefixSpace w;
-  if (int st = prefix_space(pool, batch, heads, groups, max_len, prefix_tail(pool, max_len, max_tail), &w)) return st;
+  if (int st = prefix_space(pool, batch, heads, groups, max_len, max_tail, &w)) return st;
   *bytes = w.bytes;
   return QG_OK;
 }
@@ -576,9 +987,8 @@ int qg_prefix_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q
   if (layer < 0 || layer >= pool->layers || (batch > 1 && (ldq < cols || ldo < cols))) return QG_ERR_SHAPE;
   if (!std::isfinite(scale * kLog2e)) return QG_ERR_RANGE;   // scores are kept in units of log2
   if (batch == 0) return QG_OK;
-  const int64_t tail = prefix_tail(pool, max_len, max_tail);
   PrefixSpace w;
-  if (int st = prefix_space(pool, batch, heads, groups, max_len, tail, &w)) return st;
+  if (int st = prefix_space(pool, batch, heads, groups, max_len, max_tail, &w)) return st;
   if (!q || !lens || !out || !workspace || !starts || (groups && !prefix)) return QG_ERR_NULL;
   if (prefix_misaligned(q, 16) || prefix_misaligned(out, 16) || prefix_misaligned(lens, 4) || prefix_misaligned(lse, 4) ||
       prefix_misaligned(starts, 4) || prefix_misaligned(prefix, 4) || prefix_misaligned(workspace, 16) ||
@@ -607,40 +1017,34 @@ int qg_prefix_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q
   a.heads = (int32_t)heads;
   a.kv_heads = pool->kv_heads;
   a.group = (int32_t)(heads / pool->kv_heads);
+  a.tiles_per_kv = (a.group + kHeads - 1) / kHeads;
+  a.head_tiles = a.tiles_per_kv * pool->kv_heads;
   a.max_len = (int32_t)max_len;
-  a.tile_tokens = kElems / pool->head_dim;
-  a.scale_log2 = std::fabs(scale * kLog2e);
-  a.flip = std::signbit(scale) ? 0x80008000u : 0;
+  a.part_rows = w.part_rows;
+  a.own_rows = w.own_rows;
+  a.own_most = (uint32_t)w.own_waves;
+  // a tile of shared work takes 2.3 us, 1.3 times that with weights as pairs
+  a.own_lead = own_lead(pool->head_dim, pool->kind == QG_KV_Q8);
+  a.shared_cost = (float)((out_f32 ? 3.0 : 2.3) / own_step_us(pool->head_dim, pool->kind == QG_KV_Q8));
+  const float size = std::fabs(scale * kLog2e);
+  a.scale_log2 = size < FLT_MIN ? 1.0f : size;
+  a.keep = size < FLT_MIN ? 0 : 0xFFFFFFFFu;
+  a.flip = scale < 0 ? 0x80008000u : 0;
   a.out = out;
   a.ldo = batch > 1 ? ldo : cols;
   a.out_f32 = out_f32 != 0;
   a.lse = lse;
-  a.total = reinterpret_cast<uint32_t *>(ws);
+  a.split = reinterpret_cast<Split *>(ws);
   a.plan = reinterpret_cast<GroupPlan *>(ws + w.plan);
-  a.from = reinterpret_cast<int32_t *>(ws + w.from);
-  a.group_of = reinterpret_cast<int32_t *>(ws + w.group_of);
-  a.tail = reinterpret_cast<float *>(ws + w.tail);
-  a.tail_ml = reinterpret_cast<float *>(ws + w.tail_ml);
+  a.rows = reinterpret_cast<RowPlan *>(ws + w.rows);
   a.parts = reinterpret_cast<float *>(ws + w.parts);
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (int st = launch(prefix_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a)) return st;
+  a.own_parts = reinterpret_cast<float *>(ws + w.own_parts);
   const bool q8 = pool->kind == QG_KV_Q8;
-  if (w.workers) {
-    int st;
-    switch (pool->head_dim) {
-      case 64: st = q8 ? launch_prefix<64, true>(a, w.workers, s) : launch_prefix<64, false>(a, w.workers, s); break;
-      case 128: st = q8 ? launch_prefix<128, true>(a, w.workers, s) : launch_prefix<128, false>(a, w.workers, s); break;
-      default: st = q8 ? launch_prefix<256, true>(a, w.workers, s) : launch_prefix<256, false>(a, w.workers, s);
-    }
-    if (st) return st;
-  }
-  if (int st = launch_attn_tail(pool, L, layer, q, ldq, table, ld_table, lens, a.from, batch, heads, max_len, tail,
-                                scale * kLog2e, a.tail, a.tail_ml, ws + w.tail_ws, stream))
-    return st;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
   switch (pool->head_dim) {
-    case 64: return launch_join<64>(a, w.workers, s);
-    case 128: return launch_join<128>(a, w.workers, s);
-    default: return launch_join<256>(a, w.workers, s);
+    case 64: return launch_dim<64>(a, q8, s);
+    case 128: return launch_dim<128>(a, q8, s);
+    default: return launch_dim<256>(a, q8, s);
   }
 }
 

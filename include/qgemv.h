@@ -514,10 +514,11 @@ int qg_kv_compact(const qg_kv_pool *pool, const int32_t *table, int64_t ld_table
  * out the same; with fp16 out the weights e^(s_j - max) of shared tokens meet V as one fp16 number, 2^-11 of
  * each weight, rounded to nearest, on top (the denominators add the unrounded weights).
  *
- * max_tail bounds the tokens that a row reads by itself and chooses the launch's shape only: a row with more of
- * them is slower, no less right. Arguments, alignment, limits and errors otherwise as qg_paged_attention;
- * groups is at most 4095 and at most batch. The workspace, at least qg_prefix_attention_bytes, is always needed;
- * what is said of qg_paged_attention's holds for it. */
+ * max_tail bounds the tokens that a row does not share and chooses the workspace and the shares of the work only: a
+ * row with more of them is slower, no less right. Arguments, alignment, limits and errors otherwise as
+ * qg_paged_attention; groups is at most 1023 and at most batch, and the sizes are refused (QG_ERR_SHAPE) where the
+ * work could pass 2^31 units. The workspace, at least qg_prefix_attention_bytes, is always needed; what is said of
+ * qg_paged_attention's holds for it. */
 int qg_prefix_attention_bytes(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t groups, int64_t max_len,
                               int64_t max_tail, int64_t *bytes);
 int qg_prefix_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q, int64_t ldq, const int32_t *table,

@@ -249,9 +249,9 @@ def test_max_tail_chooses_the_launch_only(max_tail):
 
 
 def test_many_groups():
-    """More groups than a wave, and than the plan's threads, has lanes for; sizes 0 to 3."""
+    """More groups than a wave has lanes, and than a workgroup has threads; sizes 0 to 3."""
     rng = np.random.default_rng(7)
-    for groups in (70, 1500):
+    for groups in (70, 1023):
         sizes = rng.integers(0, 4, groups).tolist()
         prefixes = rng.integers(0, 50, groups).tolist()
         owner = [g for g, n in enumerate(sizes) for _ in range(n)]

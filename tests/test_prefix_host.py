@@ -58,13 +58,13 @@ def test_arguments(bad, status):
 def test_sizes():
     status, size = need(pool())
     assert status == 0 and call(pool(), size=size - 1) == WORK
-    assert need(pool(), batch=5000, groups=4096)[0] == SHAPE and need(pool(), batch=5000, groups=4095)[0] == 0
+    assert need(pool(), batch=5000, groups=1024)[0] == SHAPE and need(pool(), batch=5000, groups=1023)[0] == 0
     # the line of tiles stays below 2^31
     assert need(pool(kv_heads=1, num_pages=2 ** 31 - 1, layers=1), batch=2 ** 16, heads=64, groups=1, max_len=2 ** 20)[0] == SHAPE
     # more of anything never needs less
     for name, values in [("batch", (2, 6, 40, 300)), ("max_len", (16, 100, 3000, 8192)), ("max_tail", (0, 10, 1000, 8192))]:
         sizes = [need(pool(), **{name: v})[1] for v in values]
-        assert name == "max_tail" or sizes == sorted(sizes), (name, sizes)
+        assert sizes == sorted(sizes), (name, sizes)
     assert call(pool(), batch=0, groups=0, q=None, out=None, lens=None, table=None, starts=None) == 0
 
 
