@@ -35,8 +35,11 @@ constexpr int kMaxGroups = 1023;
 // costs a worker that comes from another one, then the tiles.
 constexpr int32_t kLead = 4;
 // The same for own work, about 3 us; a step takes what its bytes do, of which the waves of a workgroup together
-// get 42 KB a us.
-__host__ __device__ constexpr double own_step_us(int dim, bool q8) { return prefix_waves(dim) * 32 * (q8 ? 2.125 : 4.0) * dim / 42e3; }
+// get 38 KB a us, or 30 where they are decoded. (64 rows after 8192 fp16 tokens take 46 us at 30 and 44 at 36 to 42,
+// 128 after 16384 int8 ones 80 us at 24 and at 42 and 76 to 77 at 28 to 30.)
+__host__ __device__ constexpr double own_step_us(int dim, bool q8) {
+  return prefix_waves(dim) * 32 * dim * (q8 ? 2.125 / 30e3 : 4.0 / 38e3);
+}
 __host__ __device__ constexpr int32_t own_lead(int dim, bool q8) { return (int32_t)(3.0 / own_step_us(dim, q8) + 0.5); }
 struct GroupPlan {
   int32_t row0, tokens, row_tiles, units;
