@@ -845,30 +845,41 @@ __global__ __launch_bounds__(64 * prefix_waves(D), D == 256 ? 1 : 2) void prefix
 
 // ---- the join ------------------------------------------------------------------------------------
 
-// D / 4 threads a row of the output: the parts of its shared tokens, and of its own.
-template <int D>
+// With few rows (query heads of the batch) the parts are many: most workgroups hold one of each row. A workgroup a row
+// then takes 8 to 10 us where a team of it takes 15 to 26 (40 to 568 rows after 6000 to 20000 tokens); with many rows
+// there are few parts, and it takes 12 us where a team a row takes 7 (2048 rows of 128).
+constexpr int64_t kFewRows = 1024;
+
+// D / 4 threads, a team, take every TEAMS-th part of a row's shared tokens and of its own; the teams of a row meet in LDS.
+template <int D, int TEAMS>
 __global__ __launch_bounds__(256) void prefix_join_kernel(PrefixArgs a) {
-  constexpr uint32_t kLanes = D / 4;
-  const int64_t row = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
-  const uint32_t d = 4 * (threadIdx.x % kLanes);
-  if (row >= (int64_t)a.batch * a.heads) return;
+  constexpr uint32_t kLanes = D / 4, kAll = 256 / kLanes;
+  static_assert(kAll % TEAMS == 0);
+  __shared__ f32x4 team_o[256];
+  __shared__ f32x2 team_ml[kAll];
+  const uint32_t team = threadIdx.x / kLanes, turn = team % TEAMS, d = 4 * (threadIdx.x % kLanes);
+  const int64_t all = (int64_t)a.batch * a.heads, at_row = (int64_t)blockIdx.x * (kAll / TEAMS) + team / TEAMS;
+  const int64_t row = min(at_row, all - 1);
   const int32_t b = (int32_t)(row / a.heads), hd = (int32_t)(row - (int64_t)b * a.heads), kvh = hd / a.group;
   const Split split = *a.split;
   const RowPlan rp = a.rows[b];
   f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;
+  auto add = [&](const f32x4 &x, const f32x2 &y) {
+    const float now = fmaxf(m, y[0]);
+    const float keep = m == now ? 1.0f : __builtin_amdgcn_exp2f(m - now);
+    const float f = y[0] == now ? 1.0f : __builtin_amdgcn_exp2f(y[0] - now);
+    o = o * keep + x * f;
+    l = l * keep + y[1] * f;
+    m = now;
+  };
   auto join = [&](const float *parts, uint32_t first, uint32_t last, int32_t rows, int32_t r) {
 #pragma unroll 4
-    for (uint32_t w = first; w <= last; ++w) {
+    for (uint32_t w = first + turn; w <= last; w += TEAMS) {
       const float *part = parts + (int64_t)w * part_floats(D, rows);
       const f32x4 x = *reinterpret_cast<const f32x4 *>(part + r * D + d);
       const f32x2 y = *reinterpret_cast<const f32x2 *>(part + rows * D + 2 * r);
-      const float now = fmaxf(m, y[0]);
-      const float keep = m == now ? 1.0f : __builtin_amdgcn_exp2f(m - now);
-      const float f = y[0] == now ? 1.0f : __builtin_amdgcn_exp2f(y[0] - now);
-      o = o * keep + x * f;
-      l = l * keep + y[1] * f;
-      m = now;
+      add(x, y);
     }
   };
   if (rp.group >= 0) {
@@ -885,6 +896,15 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(PrefixArgs a) {
     const uint32_t u0 = rp.unit0 + (uint32_t)ht * rp.units, seg = (uint32_t)(b * a.head_tiles + ht);
     join(a.own_parts, line.holder(u0) + seg, line.holder(u0 + rp.units - 1) + seg, a.own_rows, head % kHeads);
   }
+  if constexpr (TEAMS > 1) {
+    team_o[threadIdx.x] = o;
+    team_ml[team] = f32x2{m, l};                     // the same from all of a team
+    __syncthreads();
+    if (turn) return;
+#pragma unroll
+    for (int i = 1; i < TEAMS; ++i) add(team_o[threadIdx.x + i * kLanes], team_ml[team + i]);
+  }
+  if (at_row >= all) return;
   o *= l > 0.f ? 1.0f / l : l;                       // no token: 0; NaN sums stay NaN
   const int64_t to = b * a.ldo + (int64_t)hd * D + d;
   if (a.out_f32) {
@@ -955,9 +975,10 @@ int launch_prefix(const PrefixArgs &a, hipStream_t s) {
 template <int D>
 int launch_dim(const PrefixArgs &a, bool q8, hipStream_t s) {
   if (int st = q8 ? launch_prefix<D, true>(a, s) : launch_prefix<D, false>(a, s)) return st;
-  constexpr int64_t kPer = 256 / (D / 4);
+  constexpr int64_t kAll = 256 / (D / 4);
   const int64_t rows = (int64_t)a.batch * a.heads;
-  return launch(prefix_join_kernel<D>, dim3((unsigned)((rows + kPer - 1) / kPer)), dim3(256), 0, s, a);
+  if (rows <= kFewRows) return launch(prefix_join_kernel<D, kAll>, dim3((unsigned)rows), dim3(256), 0, s, a);
+  return launch(prefix_join_kernel<D, 1>, dim3((unsigned)((rows + kAll - 1) / kAll)), dim3(256), 0, s, a);
 }
 
 }  // namespace
