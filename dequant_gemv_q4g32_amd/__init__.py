@@ -556,9 +556,9 @@ def prefix_attention(pool, q, table, lens, starts, prefix, max_len: Optional[int
                      scale: Optional[float] = None, out=None, out_f32: bool = False, lse=None, return_lse: bool = False,
                      workspace=None, layer: int = 0, stream=None):
     """paged_attention of rows that share their first tokens in groups (forks of one prompt, say): the
-    shared tokens are read and multiplied once a group. Group g is the rows starts[g] to starts[g + 1] - 1
-    (int32 [groups + 1], ascending); the first prefix[g] tokens (int32 [groups]) of its rows are the same and are
-    read through the table's row starts[g]. Rows in no group, and what follows a prefix, are read as by
+    shared tokens are read and multiplied once a group where that is less work than for each row. Group g is the rows
+    starts[g] to starts[g + 1] - 1 (int32 [groups + 1], ascending); the first prefix[g] tokens (int32 [groups]) of its
+    rows are the same, by pages that they share or by equal ones. Rows in no group, and what follows a prefix, are read as by
     paged_attention. max_tail bounds the tokens that a row does not share (default: max_len); more of them are slower,
     no less right. The other arguments and the results are paged_attention's, without a window; fp16 results
     carry one more rounding of the shared tokens' weights to fp16."""

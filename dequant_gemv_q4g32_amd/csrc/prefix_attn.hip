@@ -7,6 +7,7 @@
 // them, a wave for up to 16 heads (bound by HBM). A second launch joins the parts.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 
@@ -72,7 +73,8 @@ struct PrefixArgs {
   int32_t part_rows, own_rows;   // query rows that a part of shared work, and of own work, has room for
   int32_t own_lead;              // of own work's segments
   uint32_t own_most;             // waves that own work may have: the parts' room
-  float shared_cost;             // of a tile of shared work for a workgroup, in steps of own work of a wave
+  float shared_cost, apart;      // of a tile of shared work for a workgroup, in steps of own work of a wave, and in its
+                                 // tokens' own work for a head tile of a row
   float scale_log2;              // |scale| * log2(e), or 1 where that is not a normal number;
   uint32_t keep, flip;           // for these, q is taken as zero, or as its negative: masks of two fp16 numbers
   void *out;
@@ -776,8 +778,15 @@ __global__ __launch_bounds__(64 * prefix_waves(D), D == 256 ? 1 : 2) void prefix
       const int32_t len = min(max(a.lens[p.row0], 0), a.max_len);
       p.tokens = min(max(a.prefix[g], 0), len) >> a.tok_shift << a.tok_shift;   // whole pages
     }
-    p.units = p.tokens ? (p.tokens + tile_tokens(D) - 1) / tile_tokens(D) + kLead : 0;
-    p.row_tiles = p.units ? (int32_t)(((int64_t)rows * a.group + kRows - 1) / kRows) : 0;
+    const int32_t tiles = (p.tokens + tile_tokens(D) - 1) / tile_tokens(D);
+    p.row_tiles = (int32_t)(((int64_t)rows * a.group + kRows - 1) / kRows);
+    // Is it less to read the tokens for each row apart? 24 groups of 32 heads in 8, 1600 tokens: two rows of int8 take
+    // 35 us apart and 56 together, three 45 and 52 (fp32 out 66), four 56 and 54 (65); of fp16 52 and 46, 72 and 42.
+    if ((float)rows * a.tiles_per_kv * tiles <= a.apart * p.row_tiles * (tiles + kLead)) {
+      p.tokens = 0;
+      p.row_tiles = 0;
+    }
+    p.units = p.tokens ? tiles + kLead : 0;
     segs += (uint32_t)(p.row_tiles * a.kv_heads);
     units += (uint32_t)(p.row_tiles * a.kv_heads) * (uint32_t)p.units;
   }
@@ -809,7 +818,11 @@ __global__ __launch_bounds__(64 * prefix_waves(D), D == 256 ? 1 : 2) void prefix
     workers = (uint32_t)((float)gridDim.x * (x / (x + y)) + 0.5f);
     workers = min(max(workers, 1u), gridDim.x - (own ? 1u : 0u));
   }
-  const Split split{shared, workers, own, min((gridDim.x - workers) * W, a.own_most)};
+  // A wave a unit is soonest done, but the join then has a part of each: 48 parts of a segment, more where a
+  // wave gets four units. One row of two heads of 256 and 14394 tokens takes 11 and 41 us with 450 parts, 17 and 11 with
+  // 112; four rows of 32 heads and 830 tokens, 27 units a segment, 11 and 5, and 16 and 4 with four units a wave.
+  const uint32_t most_waves = min(a.own_most, max(own / 4, 48u * (uint32_t)(a.batch * a.head_tiles)));
+  const Split split{shared, workers, own, min((gridDim.x - workers) * W, most_waves)};
   if (blockIdx.x == gridDim.x - 1) {
     if (tid == 0) *a.split = split;
     uint32_t u = my_at;
@@ -943,7 +956,8 @@ int prefix_space(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t g
   if (units > 0x7FFFFFFF || batch * head_tiles * steps(max_len) > 0x7FFFFFFF) return QG_ERR_SHAPE;
   // what is past the prefix's last whole page is a row's own, too
   const int64_t tail = max_tail + pool->page_tokens < max_len ? max_tail + pool->page_tokens : max_len;
-  const int64_t own = batch * head_tiles * steps(tail), workers = units < kResident ? units : kResident;
+  // room for max_tail tokens of every row, and for one row that shares nothing
+  const int64_t own = std::max(batch * steps(tail), steps(max_len)) * head_tiles, workers = units < kResident ? units : kResident;
   s->own_waves = (int32_t)(own < kResident * waves ? own : kResident * waves);
   s->part_rows = (int32_t)(batch * group < rows ? batch * group : rows);
   s->own_rows = (int32_t)(group < kHeads ? group : kHeads);
@@ -1049,7 +1063,10 @@ int qg_prefix_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q
   a.own_most = (uint32_t)w.own_waves;
   // a tile of shared work takes 2.3 us, 1.3 times that with weights as pairs
   a.own_lead = own_lead(pool->head_dim, pool->kind == QG_KV_Q8);
-  a.shared_cost = (float)((out_f32 ? 3.0 : 2.3) / own_step_us(pool->head_dim, pool->kind == QG_KV_Q8));
+  const double tile_us = out_f32 ? 3.0 : 2.3;
+  a.shared_cost = (float)(tile_us / own_step_us(pool->head_dim, pool->kind == QG_KV_Q8));
+  // the tile's tokens as own work, on all of the card: decoding as above, fp16 at HBM's 6 TB/s, 23 KB a us for each
+  a.apart = (float)(tile_us / (pool->kind == QG_KV_Q8 ? 8192 * 2.125 / 30e3 : 8192 * 4.0 / 23e3));
   const float size = std::fabs(scale * kLog2e);
   a.scale_log2 = size < FLT_MIN ? 1.0f : size;
   a.keep = size < FLT_MIN ? 0 : 0xFFFFFFFFu;

@@ -505,17 +505,18 @@ int qg_kv_compact(const qg_kv_pool *pool, const int32_t *table, int64_t ld_table
  * prompt, many requests after one long instruction): the shared tokens are read and multiplied once for
  * all of them. Group g < groups is the rows starts[g] to starts[g + 1] - 1 of the batch (int32 [groups + 1] on the
  * device; rows before starts[0] and from starts[groups] on are in no group), and the first prefix[g] tokens
- * (int32 [groups] on the device) of each of its rows are the same: they are read through the table's
- * row starts[g] only, as far as they fill whole pages and that row has them (a prefix below 0 counts as 0,
- * past lens[starts[g]] as that). Further tokens, and all of a group of one row, are read through each
+ * (int32 [groups] on the device) of each of its rows are the same, in the same pages or in equal ones: as far as
+ * they fill whole pages and row starts[g] has them (a prefix below 0 counts as 0, past lens[starts[g]] as that), they
+ * are read once through that row's table entries, or, where a group's few rows make that more work, for each row
+ * through its own. Further tokens, and all of a group of one row, are read through each
  * row's own entries. A row that is shorter than the prefix sees its lens tokens.
  * Values of starts outside [0, batch] count as the nearest of these, one below an earlier one as that one.
  * The result is defined as qg_paged_attention's with window 0, with these bounds of the error: with fp32
  * out the same; with fp16 out the weights e^(s_j - max) of shared tokens meet V as one fp16 number, 2^-11 of
  * each weight, rounded to nearest, on top (the denominators add the unrounded weights).
  *
- * max_tail bounds the tokens that a row does not share and chooses the workspace and the shares of the work only: a
- * row with more of them is slower, no less right. Arguments, alignment, limits and errors otherwise as
+ * max_tail bounds the tokens that a row does not share and chooses the workspace and with it how far the work on them
+ * is spread: where rows have more of them it is slower, no less right. Arguments, alignment, limits and errors otherwise as
  * qg_paged_attention; groups is at most 1023 and at most batch, and the sizes are refused (QG_ERR_SHAPE) where the
  * work could pass 2^31 units. The workspace, at least qg_prefix_attention_bytes, is always needed; what is said of
  * qg_paged_attention's holds for it. */

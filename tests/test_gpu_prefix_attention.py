@@ -263,6 +263,32 @@ def test_many_groups():
         check(out, lse, paged.attention(c, 0, q, table, lens, max(lens), 0.125), max(lens), 64, c)
 
 
+@pytest.mark.parametrize("kind,sizes,prefixes,heads,kv_heads,dim,tokens", [
+    ("f16", [12, 30, 9], [16, 40, 130], 8, 4, 64, 16), ("q8", [24, 40], [16, 33], 8, 4, 128, 16), ("f16", [16, 2, 25], [32, 500, 16], 4, 1, 256, 16),
+    ("q8", [90], [128], 34, 2, 64, 32), ("q8", [4, 5, 3, 2], [1600, 1600, 1600, 1600], 4, 2, 128, 64), ("f16", [2, 3, 1], [1500, 900, 2000], 20, 1, 64, 16)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_groups_round_the_choice_to_share(kind, sizes, prefixes, heads, kv_heads, dim, tokens, f32):
+    """Many rows after less than a tile of shared tokens, few rows after many: read together, or for each row."""
+    lens = [prefixes[g] + (7 * b) % 19 for b, g in enumerate(g for g, n in enumerate(sizes) for _ in range(n))]
+    c, table = shared_cache(kind, sizes, prefixes, lens, kv_heads, dim, tokens, 21)
+    q = (np.random.default_rng(4).standard_normal((len(lens), heads, dim)) * 1.5).astype(np.float16)
+    out, lse = qg.prefix_attention(upload(c), dev(q, np.float16), dev(table), dev(lens), dev(starts_of(sizes)), dev(prefixes),
+                                   max_tail=20, out_f32=f32, return_lse=True)
+    check(out, lse, paged.attention(c, 0, q, table, lens, max(lens), dim ** -0.5), max(lens), dim, c)
+
+
+@pytest.mark.parametrize("kind,dim", [("q8", 64), ("f16", 256)])
+def test_long_rows_without_a_group(kind, dim):
+    """More own tokens than max_tail says: the workspace's room for partial results spreads them less."""
+    lens = [9000, 33, 5000]
+    c, table = shared_cache(kind, [1], [8000], lens, 2, dim, 16, 9)
+    q = (np.random.default_rng(4).standard_normal((3, 6, dim)) * 1.5).astype(np.float16)
+    want = paged.attention(c, 0, q, table, lens, max(lens), dim ** -0.5)
+    for max_tail in (0, 100, 9000):
+        out, lse = qg.prefix_attention(upload(c), dev(q, np.float16), dev(table), dev(lens), dev([0, 1]), dev([8000]), max_tail=max_tail, return_lse=True)
+        check(out, lse, want, max(lens), dim, c)
+
+
 def test_equal_inputs_give_equal_bits():
     lens = [1000 + i for i in range(30)]
     c, table = shared_cache("q8", [30], [1000], lens, 2, 128, 16, 8)
