@@ -761,6 +761,17 @@ def _head_rows(index, what: str, t, count: int, head_dim: int):
     return t.data_ptr(), t.stride(0), heads
 
 
+def _heads_out(index, what: str, out, t, count: int, heads: int, head_dim: int):
+    """(out, address, leading dimension) of an output for t, allocated dense if none is given."""
+    if out is None:
+        out = t.new_empty(t.shape)
+        return out, out.data_ptr(), heads * head_dim
+    at, ld, out_heads = _head_rows(index, what, out, count, head_dim)
+    if out_heads != heads:
+        raise ValueError(f"{what} must have its input's {heads} heads")
+    return out, at, ld
+
+
 def qk_rope(rotary, q, k, positions, q_out=None, k_out=None, stream=None):
     """Norm and rotate queries and keys: fp16 [count, heads * head_dim] (or [count, heads, head_dim]) with any
     row stride, row i at positions[i] (int32 on the device; below 0: the row of the output stays as it
@@ -778,14 +789,12 @@ def qk_rope(rotary, q, k, positions, q_out=None, k_out=None, stream=None):
     count, dim = q.shape[0], rotary.head_dim
     at, ld, heads = _head_rows(index, "q", q, count, dim)
     kat, ldk, kv_heads = (None, 0, 0) if k is None else _head_rows(index, "k", k, count, dim)
-    q_out = q.new_empty(q.shape) if q_out is None else q_out
-    to, ldo, out_heads = _head_rows(index, "q_out", q_out, count, dim)
-    kto, ldko, k_out_heads = None, 0, 0
+    q_out, to, ldo = _heads_out(index, "q_out", q_out, q, count, heads, dim)
+    kto, ldko = None, 0
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
     if k is not None:
-        k_out = k.new_empty(k.shape) if k_out is None else k_out
-        kto, ldko, k_out_heads = _head_rows(index, "k_out", k_out, count, dim)
-    if out_heads != heads or k_out_heads != kv_heads:
-        raise ValueError("outputs must have their inputs' heads")
+        k_out, kto, ldko = _heads_out(index, "k_out", k_out, k, count, kv_heads, dim)
     _check(_lib.qg_qk_rope(rotary._ref, dim, heads, kv_heads, at, ld, kat, ldk, _ints(where, "positions", positions, count), count,
                            to, ldo, kto, ldko, _stream_now(index)), "qg_qk_rope")
     return q_out, k_out
@@ -806,10 +815,7 @@ def kv_append_rope(pool, table, rotary, q, k, v, positions, seqs=None, q_out=Non
     at, ld, heads, to, ldo = None, 0, 0, None, 0
     if q is not None:
         at, ld, heads = _head_rows(pool._index, "q", q, count, dim)
-        q_out = q.new_empty(q.shape) if q_out is None else q_out
-        to, ldo, out_heads = _head_rows(pool._index, "q_out", q_out, count, dim)
-        if out_heads != heads:
-            raise ValueError("q_out must have q's heads")
+        q_out, to, ldo = _heads_out(pool._index, "q_out", q_out, q, count, heads, dim)
     _check(_lib.qg_kv_append_rope(pool._ref, layer, *_table(pool, table), rotary._ref, heads, at, ld,
                                   *_rows16(pool, "k", k, count), *_rows16(pool, "v", v, count),
                                   None if seqs is None else _ints(pool, "seqs", seqs, count),

@@ -311,3 +311,15 @@ def test_binding_refusals():
                 lambda: qg.kv_append_rope(pool, t, rotary, q, q, k, i), lambda: qg.kv_append_rope(pool, t, rotary, q, k, k, i, q_out=k)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_outputs_of_other_heads():
+    q, k, wide = (torch.zeros((2, n), dtype=torch.float16, device="cuda") for n in (128, 64, 192))
+    i = dev([0, 1])
+    rotary = qg.Rotary(64, qg.rope_freqs(64))
+    for bad in (lambda: qg.qk_rope(rotary, q, k, i, q_out=wide), lambda: qg.qk_rope(rotary, q, k, i, k_out=q), lambda: qg.qk_rope(rotary, q, None, i, k_out=k),
+                lambda: qg.qk_rope(rotary, q, k, i, q_out=q.view(2, 1, 128))):
+        with pytest.raises(ValueError):
+            bad()
+    out = qg.qk_rope(rotary, q, k, i, q_out=wide[:, 64:])
+    assert out[0].data_ptr() == wide.data_ptr() + 128 and out[1].shape == k.shape
