@@ -164,10 +164,13 @@ __device__ __forceinline__ Own own_of(const PrefixArgs &a, int32_t raw, int32_t 
 // ---- the shared tokens ---------------------------------------------------------------------------
 
 // What a tile is to a workgroup. K is fetched 16 bytes a thread and load, V in pieces of four tokens by four
-// elements, so that the 64 lanes of a load lie in one block of 16 tokens: its page is scalar. In LDS a row has 16
-// bytes more than it needs: 16 neighbouring lanes read the same place of neighbouring rows at once, which so lie
-// in different banks, and all places of a lane are constants away from one address. K is [T][D], V^T [D][T] with
-// each 16 bytes the eight tokens of a lane's operand (16 s + 4 h + {0..3, 8..11} for step s, lane half h: place 2 s + h).
+// elements, so that the 64 lanes of a load lie in one block of 16 tokens: its page is scalar. In LDS K is [T][D], V^T
+// [D][T] with each 16 bytes the eight tokens of a lane's operand (16 s + 4 h + {0..3, 8..11} for step s, lane half h:
+// place 2 s + h). 16 neighbouring lanes read the same place of neighbouring rows at once, which shall lie in different
+// banks, and all places of a lane are constants away from one address. So a row of K has 16 bytes more than
+// it needs; V^T, which a lane writes four rows apart from its neighbour, has rows of 4 places mod 16 and one more after
+// every four rows: both ways all 16 differ. (With one more place a row the writes met 4 to a bank: 128 rows after
+// 16384 int8 tokens took 76 us, now 72.)
 template <int D, bool Q8>
 struct Shape {
   static constexpr int NT = 64 * prefix_waves(D);
@@ -180,8 +183,9 @@ struct Shape {
   static constexpr int KL = T * KPer / NT;          // such loads a thread
   static constexpr int VPer = D / 4;                // pieces of four tokens' V
   static constexpr int VL = T / 4 * VPer / NT;      // pieces a thread
-  static constexpr uint32_t KRow = D / 8 + 1, VRow = T / 8 + 1;   // 16-byte places of a row in LDS
-  static constexpr uint32_t KTile = T * KRow, VTile = D * VRow;   // and of a tile
+  static constexpr uint32_t KRow = D / 8 + 1;       // 16-byte places of a row of K in LDS,
+  static constexpr uint32_t VRow = T / 8 == 4 ? 4 : T / 8 + 4, VFour = 4 * VRow + 1;   // of one of V^T, and of four
+  static constexpr uint32_t KTile = T * KRow, VTile = D / 4 * VFour;   // and of a tile
   static constexpr uint32_t kLds = 16 * 3 * (KTile + VTile);      // bytes of three tiles
 };
 
@@ -222,7 +226,7 @@ struct StagedV {
   u32x2 s[S::VL];
   __device__ __forceinline__ void write(u32x4 *lds) const {
     const uint32_t d0 = 4 * (threadIdx.x % S::VPer), run = threadIdx.x / S::VPer;   // of four tokens
-    const uint32_t at = d0 * S::VRow + 2 * (run >> 2) + (run & 1), half = (run >> 1) & 1;
+    const uint32_t at = d0 / 4 * S::VFour + 2 * (run >> 2) + (run & 1), half = (run >> 1) & 1;
 #pragma unroll
     for (int i = 0; i < S::VL; ++i) {
       u32x2 e[4];                                   // elements d0 .. d0 + 3, four tokens each
@@ -268,7 +272,7 @@ __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &pla
   constexpr int T = S::T, TB = S::TB, KS = S::KS, DB = S::DB, kBlocks = T / 16, kRows = S::NT / 2, NT = S::NT;
   const uint32_t tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), n = lane & 31, h = lane >> 5;
   u32x4 *const lds_k = tiles, *const lds_v = tiles + 3 * S::KTile;
-  const uint32_t k_at = n * S::KRow + h, v_at = n * S::VRow + h;   // a lane's places of K and V
+  const uint32_t k_at = n * S::KRow + h, v_at = n / 4 * S::VFour + n % 4 * S::VRow + h;   // a lane's places of K and V
   // a lane's part of an address of K and V, beside the wave's first rows
   const uint32_t k_lane = (lane / S::KPer) * S::KBytes + 16 * (lane % S::KPer);
   const uint32_t ks_lane = Q8 ? (lane / S::KPer) * (D / 16) + 2 * (lane % S::KPer / 2) : 0;
@@ -456,7 +460,7 @@ __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &pla
           // slots on, a part of the softmax. Past the last tile the scores are of what is there, and nobody reads them.
           const u32x4 *ks = lds_k + (tb + 1 < TB ? now : ahead) * S::KTile + k_at + 32 * ((tb + 1) % TB) * S::KRow;
           const u32x4 *vs = lds_v + (tb > 0 ? now : past) * S::VTile + v_at + 4 * ((tb + TB - 1) % TB);
-          auto read = [&](int i) { return i < KS ? ks[2 * i] : vs[2 * ((i - KS) / DB) + 32 * ((i - KS) % DB) * S::VRow]; };
+          auto read = [&](int i) { return i < KS ? ks[2 * i] : vs[2 * ((i - KS) / DB) + 8 * ((i - KS) % DB) * S::VFour]; };
           u32x4 ring[kRing];
           f32x16 next;
 #pragma unroll
@@ -525,7 +529,7 @@ __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &pla
       const u32x4 *vs = lds_v + past * S::VTile + v_at + 4 * (TB - 1);
 #pragma unroll
       for (int i = 0; i < 2 * DB; ++i) {
-        const half8_t x = __builtin_bit_cast(half8_t, vs[2 * (i / DB) + 32 * (i % DB) * S::VRow]);
+        const half8_t x = __builtin_bit_cast(half8_t, vs[2 * (i / DB) + 8 * (i % DB) * S::VFour]);
         o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, hi[i / DB], o[i % DB], 0, 0, 0);
         if constexpr (PAIRS) o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, lo[i / DB], o[i % DB], 0, 0, 0);
       }
@@ -1061,9 +1065,10 @@ int qg_prefix_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q
   a.part_rows = w.part_rows;
   a.own_rows = w.own_rows;
   a.own_most = (uint32_t)w.own_waves;
-  // a tile of shared work takes 2.3 us, 1.3 times that with weights as pairs
   a.own_lead = own_lead(pool->head_dim, pool->kind == QG_KV_Q8);
-  const double tile_us = out_f32 ? 3.0 : 2.3;
+  // A tile of shared work takes 2.2 to 2.3 us, 1.3 times that with weights as pairs; with heads of 256, half the rows,
+  // 2.1 (79 rows of 48 heads after 6127 tokens: 98 us with 2.3 here, 90 with 2.1; 128 of 32 heads of 128: 72 and 73).
+  const double tile_us = (out_f32 ? 3.0 : 2.3) * (pool->head_dim == 256 ? 0.92 : 1.0);
   a.shared_cost = (float)(tile_us / own_step_us(pool->head_dim, pool->kind == QG_KV_Q8));
   // the tile's tokens as own work, on all of the card: decoding as above, fp16 at HBM's 6 TB/s, 23 KB a us for each
   a.apart = (float)(tile_us / (pool->kind == QG_KV_Q8 ? 8192 * 2.125 / 30e3 : 8192 * 4.0 / 23e3));
