@@ -43,8 +43,8 @@ __host__ __device__ constexpr double own_step_us(int dim, bool q8) {
 }
 __host__ __device__ constexpr int32_t own_lead(int dim, bool q8) { return (int32_t)(3.0 / own_step_us(dim, q8) + 0.5); }
 struct GroupPlan {
-  int32_t row0, tokens, row_tiles, units;
-  uint32_t unit0, seg0;          // units and segments of the groups before
+  int32_t row0, rows, tokens, row_tiles, units;
+  uint32_t unit0;                // units of the groups before
 };
 // Of a row: its group (-1: it shares nothing), and its own tokens' place on the line of own work: for each head tile in
 // turn `units`, a lead and steps of 32 tokens, or none.
@@ -55,6 +55,13 @@ struct RowPlan {
 // Of the call: both lines, and their workers.
 struct Split {
   uint32_t shared, workers, own, waves;
+};
+
+// Partial results: query rows' sums, and their references and denominators. From one part to the next on a line the
+// worker or the segment goes up, or both: a worker's rows of a segment lie behind as many as a part has at most for each
+// worker before it, and the rows of all segments before (part_row, own_part).
+struct Parts {
+  float *o, *ml;                 // [rows][D], [rows][2]
 };
 
 struct PrefixArgs {
@@ -70,7 +77,7 @@ struct PrefixArgs {
   int32_t groups, batch, heads, group, kv_heads;   // group = heads / kv_heads
   int32_t tiles_per_kv, head_tiles;   // own work: head tiles of a KV head, and of all of them
   int32_t max_len;
-  int32_t part_rows, own_rows;   // query rows that a part of shared work, and of own work, has room for
+  int32_t part_rows, own_rows;   // the most query rows of a part of shared work, and of own work
   int32_t own_lead;              // of own work's segments
   uint32_t own_most;             // waves that own work may have: the parts' room
   float shared_cost, apart;      // of a tile of shared work for a workgroup, in steps of own work of a wave, and in its
@@ -84,11 +91,8 @@ struct PrefixArgs {
   Split *split;                  // workspace: what the join has to know,
   GroupPlan *plan;
   RowPlan *rows;
-  float *parts, *own_parts;      // and the partial results: part w + s is worker w's of segment s
+  Parts parts, own_parts;        // and the partial results
 };
-
-// A part: [rows][D] sums, then each row's reference and denominator.
-__host__ __device__ __forceinline__ int64_t part_floats(int32_t dim, int32_t rows) { return (int64_t)rows * dim + 2 * rows; }
 
 // ---- the plan ------------------------------------------------------------------------------------
 //
@@ -107,8 +111,8 @@ __device__ __forceinline__ uint32_t scan_max(uint32_t v) {
 struct Plan {
   int32_t lead[kMaxGroups + 1];  // the groups' first rows, made to ascend, and the last one's end
   GroupPlan g[kMaxGroups];
-  uint32_t red[2][8];
-  uint32_t found[3][8];
+  uint32_t red[8];
+  uint32_t found[2][8];
 
   // the group of row b, -1: none
   __device__ __forceinline__ int32_t group_of(int32_t b, int32_t groups) const {
@@ -121,29 +125,32 @@ struct Plan {
   }
 };
 
-// Sums over the threads before this one, and in all, of two values at once.
+// The sum over the threads before this one, and in all.
 template <int W>
-__device__ __forceinline__ void scan_two(uint32_t &x, uint32_t &y, uint32_t &all_x, uint32_t &all_y, Plan &p) {
-  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, sx = wave_scan(x), sy = wave_scan(y);
+__device__ __forceinline__ uint32_t scan_sum(uint32_t x, uint32_t &all, Plan &p) {
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, sum = wave_scan(x);
   __syncthreads();
-  if (lane == 63) {
-    p.red[0][wave] = sx;
-    p.red[1][wave] = sy;
-  }
+  if (lane == 63) p.red[wave] = sum;
   __syncthreads();
-  uint32_t bx = 0, by = 0, tx = 0, ty = 0;
+  uint32_t before = 0, total = 0;
 #pragma unroll
   for (int k = 0; k < W; ++k) {
-    const uint32_t rx = p.red[0][k], ry = p.red[1][k];
-    bx += k < (int)wave ? rx : 0;
-    by += k < (int)wave ? ry : 0;
-    tx += rx;
-    ty += ry;
+    const uint32_t r = p.red[k];
+    before += k < (int)wave ? r : 0;
+    total += r;
   }
-  x = bx + sx - x;
-  y = by + sy - y;
-  all_x = uniform(tx);
-  all_y = uniform(ty);
+  all = uniform(total);
+  return before + sum - x;
+}
+
+// Where worker w puts query row m of a KV head of a group.
+__device__ __forceinline__ int64_t part_row(const PrefixArgs &a, const GroupPlan &p, uint32_t w, int32_t kvh, int32_t m) {
+  return (int64_t)w * a.part_rows + (int64_t)p.row0 * a.heads + (int64_t)kvh * p.rows * a.group + m;
+}
+
+// And wave v the first row of its part of a head tile of row b.
+__device__ __forceinline__ int64_t own_part(const PrefixArgs &a, uint32_t v, int32_t b, int32_t ht) {
+  return ((int64_t)v + (int64_t)b * a.head_tiles + ht) * a.own_rows;
 }
 
 // What of a row's tokens is its own: [first, len), in steps of 32 from base = first rounded down, and the units
@@ -288,9 +295,9 @@ __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &pla
     g = lo - 1;
   }
   while (at < end) {
-    const GroupPlan p{uniform(plan.g[g].row0), uniform(plan.g[g].tokens), uniform(plan.g[g].row_tiles), uniform(plan.g[g].units),
-                      uniform(plan.g[g].unit0), uniform(plan.g[g].seg0)};
-    const int32_t rows = (uniform(plan.lead[g + 1]) - p.row0) * a.group;
+    const GroupPlan p{uniform(plan.g[g].row0), uniform(plan.g[g].rows), uniform(plan.g[g].tokens), uniform(plan.g[g].row_tiles),
+                      uniform(plan.g[g].units), uniform(plan.g[g].unit0)};
+    const int32_t rows = p.rows * a.group;
     const uint32_t segs = (uint32_t)(p.row_tiles * a.kv_heads);
     if (p.units == 0 || at - p.unit0 >= segs * (uint32_t)p.units) {
       ++g;
@@ -536,16 +543,15 @@ __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &pla
     }
     l += __shfl_xor(l, 32);
     if (m < rows) {
-      float *part = a.parts + (int64_t)(w + p.seg0 + seg) * part_floats(D, a.part_rows);
-      const int r = m - rt * kRows;
+      const int64_t r = part_row(a, p, w, kvh, m);
       if (bad && ref > -INFINITY) l = __builtin_nanf("");
 #pragma unroll
       for (int i = 0; i < DB; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<f32x4 *>(part + r * D + 32 * i + 8 * j + 4 * h) =
+          *reinterpret_cast<f32x4 *>(a.parts.o + r * D + 32 * i + 8 * j + 4 * h) =
               f32x4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
-      if (h == 0) *reinterpret_cast<f32x2 *>(part + a.part_rows * D + 2 * r) = f32x2{ref, l};
+      if (h == 0) *reinterpret_cast<f32x2 *>(a.parts.ml + 2 * r) = f32x2{ref, l};
     }
   }
 }
@@ -729,13 +735,13 @@ __device__ __forceinline__ void own_work(const PrefixArgs &a, const Plan &plan, 
     l += __shfl_xor(l, 32);
     if (bad && ref > -INFINITY) l = __builtin_nanf("");
     if (c < cur.rows) {
-      float *part = a.own_parts + (int64_t)(v + (uint32_t)(cur.b * a.head_tiles + cur.ht)) * part_floats(D, a.own_rows);
+      const int64_t r = own_part(a, v, cur.b, cur.ht) + c;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < VJ; j += 4)
-          *reinterpret_cast<f32x4 *>(part + c * D + VJ * (4 * g + i) + j) = f32x4{o[0][j][i], o[0][j + 1][i], o[0][j + 2][i], o[0][j + 3][i]};
-      if (g == 0) *reinterpret_cast<f32x2 *>(part + a.own_rows * D + 2 * c) = f32x2{ref, l};
+          *reinterpret_cast<f32x4 *>(a.own_parts.o + r * D + VJ * (4 * g + i) + j) = f32x4{o[0][j][i], o[0][j + 1][i], o[0][j + 2][i], o[0][j + 3][i]};
+      if (g == 0) *reinterpret_cast<f32x2 *>(a.own_parts.ml + 2 * r) = f32x2{ref, l};
     }
     cur = fetch;
   }
@@ -760,60 +766,58 @@ __global__ __launch_bounds__(64 * prefix_waves(D), D == 256 ? 1 : 2) void prefix
     lead[i] = most;
   }
   const uint32_t upto = scan_max(most);
-  if ((tid & 63) == 63) plan.red[0][wave] = upto;
+  if ((tid & 63) == 63) plan.red[wave] = upto;
   __syncthreads();
   const uint32_t left = (uint32_t)__shfl_up((int)upto, 1);
   uint32_t before = (tid & 63) ? left : 0;
-  for (int k = 0; k < wave; ++k) before = max(before, plan.red[0][k]);
+  for (int k = 0; k < wave; ++k) before = max(before, plan.red[k]);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) plan.lead[kPer * tid + i] = (int32_t)max(lead[i], before);
   __syncthreads();
-  uint32_t units = 0, segs = 0, shared, all_segs;
+  uint32_t units = 0, shared;
   GroupPlan mine[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int32_t g = kPer * tid + i;
-    mine[i] = GroupPlan{0, 0, 0, 0, units, segs};
+    mine[i] = GroupPlan{0, 0, 0, 0, 0, units};
     if (g >= a.groups) continue;
     GroupPlan &p = mine[i];
     p.row0 = plan.lead[g];
-    const int32_t rows = plan.lead[g + 1] - p.row0;
-    if (rows > 1) {
+    p.rows = plan.lead[g + 1] - p.row0;
+    if (p.rows > 1) {
       const int32_t len = min(max(a.lens[p.row0], 0), a.max_len);
       p.tokens = min(max(a.prefix[g], 0), len) >> a.tok_shift << a.tok_shift;   // whole pages
     }
     const int32_t tiles = (p.tokens + tile_tokens(D) - 1) / tile_tokens(D);
-    p.row_tiles = (int32_t)(((int64_t)rows * a.group + kRows - 1) / kRows);
+    p.row_tiles = (int32_t)(((int64_t)p.rows * a.group + kRows - 1) / kRows);
     // Is it less to read the tokens for each row apart? 24 groups of 32 heads in 8, 1600 tokens: two rows of int8 take
     // 35 us apart and 56 together, three 45 and 52 (fp32 out 66), four 56 and 54 (65); of fp16 52 and 46, 72 and 42.
-    if ((float)rows * a.tiles_per_kv * tiles <= a.apart * p.row_tiles * (tiles + kLead)) {
+    if ((float)p.rows * a.tiles_per_kv * tiles <= a.apart * p.row_tiles * (tiles + kLead)) {
       p.tokens = 0;
       p.row_tiles = 0;
     }
     p.units = p.tokens ? tiles + kLead : 0;
-    segs += (uint32_t)(p.row_tiles * a.kv_heads);
     units += (uint32_t)(p.row_tiles * a.kv_heads) * (uint32_t)p.units;
   }
-  scan_two<W>(units, segs, shared, all_segs, plan);
+  units = scan_sum<W>(units, shared, plan);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int32_t g = kPer * tid + i;
     if (g >= a.groups) continue;
     mine[i].unit0 += units;
-    mine[i].seg0 += segs;
     plan.g[g] = mine[i];
     if (blockIdx.x == 0) a.plan[g] = mine[i];
   }
   __syncthreads();
   // the rows' own tokens, a run of rows for each thread
   const int32_t per = (a.batch + NT - 1) / NT, my_b = tid * per;
-  uint32_t my_units = 0, unused = 0, own, none;
+  uint32_t my_units = 0, own;
   for (int32_t b = my_b; b < min(my_b + per, a.batch); ++b) {
     const int32_t g = plan.group_of(b, a.groups);
     my_units += own_of(a, a.lens[b], g < 0 ? 0 : plan.g[g].tokens).units * (uint32_t)a.head_tiles;
   }
   uint32_t my_at = my_units;
-  scan_two<W>(my_at, unused, own, none, plan);
+  my_at = scan_sum<W>(my_at, own, plan);
 
   // Both kinds of work get workgroups by their cost.
   uint32_t workers = 0;
@@ -890,12 +894,12 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(PrefixArgs a) {
     l = l * keep + y[1] * f;
     m = now;
   };
-  auto join = [&](const float *parts, uint32_t first, uint32_t last, int32_t rows, int32_t r) {
+  auto join = [&](const Parts &parts, uint32_t first, uint32_t last, int64_t r, int32_t step) {   // at r + w * step
 #pragma unroll 4
     for (uint32_t w = first + turn; w <= last; w += TEAMS) {
-      const float *part = parts + (int64_t)w * part_floats(D, rows);
-      const f32x4 x = *reinterpret_cast<const f32x4 *>(part + r * D + d);
-      const f32x2 y = *reinterpret_cast<const f32x2 *>(part + rows * D + 2 * r);
+      const int64_t at = r + (int64_t)w * step;
+      const f32x4 x = *reinterpret_cast<const f32x4 *>(parts.o + at * D + d);
+      const f32x2 y = *reinterpret_cast<const f32x2 *>(parts.ml + 2 * at);
       add(x, y);
     }
   };
@@ -905,13 +909,13 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(PrefixArgs a) {
     const Line line = make_line(split.shared, split.workers);
     const int32_t q = (b - p.row0) * a.group + hd - kvh * a.group, rt = q / kRows;
     const uint32_t seg = (uint32_t)(kvh * p.row_tiles + rt), u0 = p.unit0 + seg * (uint32_t)p.units;
-    join(a.parts, line.holder(u0 + kLead) + p.seg0 + seg, line.holder(u0 + (uint32_t)p.units - 1) + p.seg0 + seg, a.part_rows, q - rt * kRows);
+    join(a.parts, line.holder(u0 + kLead), line.holder(u0 + (uint32_t)p.units - 1), part_row(a, p, 0, kvh, q), a.part_rows);
   }
   if (rp.units) {
     const Line line = make_line(split.own, split.waves);
     const int32_t head = hd - kvh * a.group, ht = kvh * a.tiles_per_kv + head / kHeads;
-    const uint32_t u0 = rp.unit0 + (uint32_t)ht * rp.units, seg = (uint32_t)(b * a.head_tiles + ht);
-    join(a.own_parts, line.holder(u0) + seg, line.holder(u0 + rp.units - 1) + seg, a.own_rows, head % kHeads);
+    const uint32_t u0 = rp.unit0 + (uint32_t)ht * rp.units;
+    join(a.own_parts, line.holder(u0), line.holder(u0 + rp.units - 1), own_part(a, 0, b, ht) + head % kHeads, a.own_rows);
   }
   if constexpr (TEAMS > 1) {
     team_o[threadIdx.x] = o;
@@ -942,9 +946,9 @@ bool prefix_misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<ui
 constexpr int64_t kResident = 256;                 // workgroups that are resident at once
 
 // Where things lie in the workspace, in bytes, and the rows of the parts. A group's query rows of a KV head fill
-// all their tiles but one, so there are at most `segments` segments of shared work.
+// all their tiles but one, so there are at most `segments` segments of shared work. Their rows are batch * heads at most.
 struct PrefixSpace {
-  int64_t plan, rows, parts, own_parts, bytes;
+  int64_t plan, rows, parts, parts_ml, own_parts, own_ml, bytes;
   int32_t part_rows, own_rows, own_waves;
 };
 
@@ -969,8 +973,12 @@ int prefix_space(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t g
   s->plan = up(sizeof(Split));
   s->rows = s->plan + up(groups * (int64_t)sizeof(GroupPlan));
   s->parts = s->rows + up(batch * (int64_t)sizeof(RowPlan));
-  s->own_parts = s->parts + up(4 * part_floats((int32_t)dim, s->part_rows) * (workers ? workers + segments - 1 : 0));
-  s->bytes = s->own_parts + 4 * part_floats((int32_t)dim, s->own_rows) * (batch ? s->own_waves + batch * head_tiles - 1 : 0);
+  const int64_t all = workers ? workers * s->part_rows + batch * heads : 0;
+  const int64_t all_own = batch ? s->own_rows * (s->own_waves + batch * head_tiles) : 0;
+  s->parts_ml = s->parts + 4 * dim * all;
+  s->own_parts = s->parts_ml + up(8 * all);
+  s->own_ml = s->own_parts + 4 * dim * all_own;
+  s->bytes = s->own_ml + up(8 * all_own);
   return QG_OK;
 }
 
@@ -1083,8 +1091,8 @@ int qg_prefix_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q
   a.split = reinterpret_cast<Split *>(ws);
   a.plan = reinterpret_cast<GroupPlan *>(ws + w.plan);
   a.rows = reinterpret_cast<RowPlan *>(ws + w.rows);
-  a.parts = reinterpret_cast<float *>(ws + w.parts);
-  a.own_parts = reinterpret_cast<float *>(ws + w.own_parts);
+  a.parts = Parts{reinterpret_cast<float *>(ws + w.parts), reinterpret_cast<float *>(ws + w.parts_ml)};
+  a.own_parts = Parts{reinterpret_cast<float *>(ws + w.own_parts), reinterpret_cast<float *>(ws + w.own_ml)};
   const bool q8 = pool->kind == QG_KV_Q8;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   switch (pool->head_dim) {
