@@ -2,9 +2,17 @@
 //
 // A group's rows with the heads of a KV head are one block of queries against the shared tokens: unlike a single
 // sequence's few heads, enough of them to keep the matrix cores busy. One launch does both kinds of work, each on its
-// share of the workgroups: the shared tokens, once a group, as a flash attention of up to 256 query rows a workgroup
-// (bound by the matrix and vector instructions), and the tokens that a row has for itself, as paged_attn.hip does
-// them, a wave for up to 16 heads (bound by HBM). A second launch joins the parts.
+// share of the workgroups: the shared tokens, once a group, in one pass with a running reference, up to 256 query rows
+// a workgroup, and the tokens that a row has for itself, as paged_attn.hip does them, a wave for up to 16 heads. A
+// second launch joins the parts.
+//
+// Measured: 128 rows of 32 heads on 8 of 128 after 16384 shared int8 tokens, up to 1024 of their own, take 71 and 8 us; a
+// pass over the shared tokens for each row would read 4.6 GB, 670 us at HBM's rate. Shared work reaches 800 to 930
+// TFLOP/s on its workgroups; a large library product 1150 on all. Of a tile's 2.2 us the matrix instructions are
+// busy for 1.0, the vector instructions about as long, LDS for 0.9, and the two waves of a SIMD do not overlap
+// them all. Own work runs at 30 to 38 KB a us and workgroup: instruction issue for int8, loads in flight for
+// fp16. Short calls are latency: 3 us for the plan, 5 to the first scores (page, K, LDS), 2 to 3 to
+// store the parts, 4 to 9 for the join (8 rows after 1000 tokens: 11 and 4).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

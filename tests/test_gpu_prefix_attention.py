@@ -289,6 +289,20 @@ def test_long_rows_without_a_group(kind, dim):
         check(out, lse, want, max(lens), dim, c)
 
 
+def test_nothing_to_see():
+    """No sequences, no groups, no tokens at all, a table without entries."""
+    c, table = shared_cache("f16", [3], [16], [20] * 3, 1, 64, 16, 8)
+    pool, q, none = upload(c), torch.ones((3, 2, 64), dtype=torch.float16, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")
+    for args in ((dev(table), dev([0, 0, -3]), dev([0, 3]), dev([16])), (torch.zeros((3, 0), dtype=torch.int32, device="cuda"), dev([5, 5, 5]), dev([0, 3]), dev([16])),
+                 (dev(table), dev([0, 0, 0]), dev([0]), none)):
+        out, lse = qg.prefix_attention(pool, q, *args, return_lse=True)
+        assert torch.all(out == 0) and torch.all(lse == -float("inf"))
+    out, lse = qg.prefix_attention(pool, q[:0], dev(table)[:0], none, dev([0]), none, return_lse=True)
+    assert out.shape == (0, 2, 64) and lse.shape == (0, 2)
+    alone = qg.prefix_attention(pool, q, dev(table), dev([20] * 3), dev([0]), none, out_f32=True, return_lse=True)
+    check(*alone, paged.attention(c, 0, q.cpu().numpy(), table, [20] * 3, 32, 0.125), 20, 64, c)
+
+
 def test_equal_inputs_give_equal_bits():
     lens = [1000 + i for i in range(30)]
     c, table = shared_cache("q8", [30], [1000], lens, 2, 128, 16, 8)
