@@ -54,8 +54,11 @@ struct GroupPlan {
   int32_t row0, rows, tokens, row_tiles, units;
   uint32_t unit0;                // units of the groups before
 };
-// Of a row: its group (-1: it shares nothing), and its own tokens' place on the line of own work: for each head tile in
-// turn `units`, a lead and steps of 32 tokens, or none.
+// A group of few query rows goes to the line of own work instead (row_tiles 0), before its first row: 16 query rows are a
+// pack, and a KV head's packs have `units` each as if they were heads of a row.
+//
+// Of a row: its group (-1: it shares nothing), and its place on the line of own work: the packs that it is the first row
+// of, then for each head tile in turn `units`, a lead and steps of 32 tokens, or none.
 struct RowPlan {
   int32_t group;
   uint32_t unit0, units;
@@ -88,8 +91,8 @@ struct PrefixArgs {
   int32_t part_rows, own_rows;   // the most query rows of a part of shared work, and of own work
   int32_t own_lead;              // of own work's segments
   uint32_t own_most;             // waves that own work may have: the parts' room
-  float shared_cost, apart;      // of a tile of shared work for a workgroup, in steps of own work of a wave, and in its
-                                 // tokens' own work for a head tile of a row
+  float shared_cost, tile_steps; // of a tile of shared work for a workgroup, in steps of own work of a wave: of each of
+                                 // its waves, and of all where they all do such work
   float scale_log2;              // |scale| * log2(e), or 1 where that is not a normal number;
   uint32_t keep, flip;           // for these, q is taken as zero, or as its negative: masks of two fp16 numbers
   void *out;
@@ -99,7 +102,7 @@ struct PrefixArgs {
   Split *split;                  // workspace: what the join has to know,
   GroupPlan *plan;
   RowPlan *rows;
-  Parts parts, own_parts;        // and the partial results
+  Parts parts, packs, own_parts; // and the partial results
 };
 
 // ---- the plan ------------------------------------------------------------------------------------
@@ -154,6 +157,16 @@ __device__ __forceinline__ uint32_t scan_sum(uint32_t x, uint32_t &all, Plan &p)
 // Where worker w puts query row m of a KV head of a group.
 __device__ __forceinline__ int64_t part_row(const PrefixArgs &a, const GroupPlan &p, uint32_t w, int32_t kvh, int32_t m) {
   return (int64_t)w * a.part_rows + (int64_t)p.row0 * a.heads + (int64_t)kvh * p.rows * a.group + m;
+}
+
+// The same for a pack's and wave w.
+__device__ __forceinline__ int64_t pack_row(const PrefixArgs &a, const GroupPlan &p, uint32_t w, int32_t kvh, int32_t m) {
+  return (int64_t)w * kHeads + (int64_t)p.row0 * a.heads + (int64_t)kvh * p.rows * a.group + m;
+}
+__device__ __forceinline__ int32_t packs_of(const PrefixArgs &a, const GroupPlan &p) { return (p.rows * a.group + kHeads - 1) / kHeads; }
+// What the packs before row b's own tokens have on the line.
+__device__ __forceinline__ uint32_t pack_units(const PrefixArgs &a, const GroupPlan &p, int32_t b) {
+  return p.row0 == b && p.tokens && !p.row_tiles ? (uint32_t)(packs_of(a, p) * a.kv_heads) * (uint32_t)p.units : 0;
 }
 
 // And wave v the first row of its part of a head tile of row b.
@@ -566,37 +579,66 @@ __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &pla
 
 // ---- the rows' own tokens ------------------------------------------------------------------------
 
-// A wave's part of one head tile of one row's own tokens.
+// A wave's part of one head tile of one row's own tokens, or of a pack.
 struct OwnSegment {
-  uint32_t u0, u1;           // the head tile on the line
+  uint32_t row_at, u0;       // where row b, and the segment, begin on the line
   uint32_t at, end;          // the wave's part of it; at in the lead: a step before the first, all masked
-  int32_t b, ht;
+  int32_t b;
   Own seen;
-  int32_t h0, rows;          // its first head, heads
+  int32_t h0, rows;          // its first head, query rows
+  int32_t m0, per;           // query row i: row b + (m0 + i) / per, head h0 + (m0 + i) % per
+  bool pack;
+  int64_t part;              // its first row of wave 0's partial results
   const uint8_t *kv;         // its KV head's part of page 0
   const int32_t *row;        // the row's entries
 };
 
-// The segment at unit `at` < end, at or after row b, whose own tokens start at row_at on the line.
+// The segment at unit `at` < end, at or after row b, which starts at row_at on the line.
 __device__ __forceinline__ OwnSegment own_segment(const PrefixArgs &a, const Plan &plan, uint32_t at, uint32_t end, int32_t b,
                                                   uint32_t row_at) {
   OwnSegment s;
+  GroupPlan p;
+  uint32_t before;
   for (;;) {
     const int32_t g = uniform(plan.group_of(b, a.groups));
-    s.seen = own_of(a, scalar_load(a.lens + b), g < 0 ? 0 : uniform(plan.g[g].tokens));
-    if (at - row_at < s.seen.units * (uint32_t)a.head_tiles) break;
-    row_at += s.seen.units * (uint32_t)a.head_tiles;
+    p = GroupPlan{-1, 0, 0, 0, 0, 0};
+    if (g >= 0)
+      p = GroupPlan{uniform(plan.g[g].row0), uniform(plan.g[g].rows), uniform(plan.g[g].tokens), uniform(plan.g[g].row_tiles),
+                    uniform(plan.g[g].units), 0};
+    before = pack_units(a, p, b);
+    s.seen = own_of(a, scalar_load(a.lens + b), p.tokens);
+    const uint32_t n = before + s.seen.units * (uint32_t)a.head_tiles;
+    if (at - row_at < n) break;
+    row_at += n;
     ++b;
   }
   s.b = b;
-  s.ht = (int32_t)((at - row_at) / s.seen.units);
-  s.u0 = row_at + (uint32_t)s.ht * s.seen.units;
-  s.u1 = s.u0 + s.seen.units;
-  s.end = min(end, s.u1);
+  s.row_at = row_at;
+  s.pack = at - row_at < before;
+  int32_t kvh;
+  if (s.pack) {
+    s.seen = Own{0, p.tokens, 0, (uint32_t)p.units};
+    const int32_t i = (int32_t)((at - row_at) / s.seen.units), n = packs_of(a, p);
+    kvh = i / n;
+    s.u0 = row_at + (uint32_t)i * s.seen.units;
+    s.m0 = (i - kvh * n) * kHeads;
+    s.per = a.group;
+    s.h0 = kvh * a.group;
+    s.rows = min(kHeads, p.rows * a.group - s.m0);
+    s.part = pack_row(a, p, 0, kvh, s.m0);
+  } else {
+    const int32_t ht = (int32_t)((at - row_at - before) / s.seen.units);
+    s.u0 = row_at + before + (uint32_t)ht * s.seen.units;
+    kvh = ht / a.tiles_per_kv;
+    const int32_t first_head = (ht - kvh * a.tiles_per_kv) * kHeads;
+    s.m0 = 0;
+    s.per = kHeads;
+    s.h0 = kvh * a.group + first_head;
+    s.rows = min(kHeads, a.group - first_head);
+    s.part = own_part(a, 0, b, ht);
+  }
+  s.end = min(end, s.u0 + s.seen.units);
   s.at = at < s.u0 + a.own_lead && s.u0 + a.own_lead < s.end ? s.u0 + a.own_lead : at;
-  const int32_t kvh = s.ht / a.tiles_per_kv, first_head = (s.ht - kvh * a.tiles_per_kv) * kHeads;
-  s.h0 = kvh * a.group + first_head;
-  s.rows = min(kHeads, a.group - first_head);
   s.kv = a.pool + kvh * a.head_bytes;
   s.row = a.table + b * a.ld_table;
   return s;
@@ -633,12 +675,13 @@ __device__ __forceinline__ void own_work(const PrefixArgs &a, const Plan &plan, 
       blk[st].place = (uint32_t)token(st) & ((1u << a.tok_shift) - 1);
     }
   };
-  auto load_q = [&]() {                              // heads past the tile's read as zeros: their lanes' own offsets are out of range
-    const uint16_t *from = a.q + uniform(fetch.b) * a.ldq + (int64_t)uniform(fetch.h0) * D;
-    const rsrc_t r = make_rsrc(from, (uint32_t)uniform(fetch.rows) * D * 2);
+  int32_t limit = 0;                                 // the tokens that the lane's query row sees; of the segment in q
+  auto load_q = [&]() {                              // query rows past the segment's are its last: nobody reads their results
+    const int32_t m = fetch.m0 + min(c, fetch.rows - 1), down = m / fetch.per, b = fetch.b + down;
+    const uint16_t *from = a.q + b * a.ldq + (int64_t)(fetch.h0 + m - down * fetch.per) * D + 16 * g;
+    limit = a.lens[b];
 #pragma unroll
-    for (int i = 0; i < T::KD; ++i)
-      q[0][i] = __builtin_bit_cast(half8_t, bldx4<0>(r, c * (2 * D) + 32 * g, 128 * (i >> 1) + 16 * (i & 1)));
+    for (int i = 0; i < T::KD; ++i) q[0][i] = *reinterpret_cast<const half8_t *>(from + 64 * (i >> 1) + 8 * (i & 1));
   };
   look_up();
   locate();
@@ -655,22 +698,26 @@ __device__ __forceinline__ void own_work(const PrefixArgs &a, const Plan &plan, 
     for (int j = 0; j < VJ; ++j) o[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     float ref = -INFINITY, l = 0.f;
     bool inside = true, fresh = true, bad = false;   // the step in t is of segment cur, and its first; q is not finite
+    const bool even = !cur.pack || !__any(limit < cur.seen.len);   // all see the same tokens
+    const int32_t seen = limit;
     while (inside) {
       const int32_t t0 = token(0);
-      const bool full = t0 >= cur.seen.first && t0 + kTile <= cur.seen.len && page[0] >= 0 && page[1] >= 0;
-      uint32_t valid = 0xFF;                         // of the lane's eight tokens
+      const bool full = even && t0 >= cur.seen.first && t0 + kTile <= cur.seen.len && page[0] >= 0 && page[1] >= 0;
+      uint32_t valid = 0xFF, sees = 0xFF;            // of the lane's eight tokens: those that are there, those its query row sees
       if (!full) {
-        valid = 0;
+        valid = sees = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int32_t tok = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
           valid |= (uint32_t)(tok >= cur.seen.first && tok < cur.seen.len && page[i >> 2] >= 0) << i;
+          sees |= (uint32_t)(tok < seen) << i;
         }
+        sees &= valid;
       }
       more = fetch.at + 1 < end;
       if (++fetch.at == fetch.end) {
         inside = false;
-        if (more) fetch = own_segment(a, plan, fetch.at, end, fetch.b, fetch.u0 - fetch.seen.units * (uint32_t)fetch.ht);
+        if (more) fetch = own_segment(a, plan, fetch.at, end, fetch.b, fetch.row_at);
       }
       look_up();
       if (fresh) {                                   // a head that is not finite is taken as zeros, and marked
@@ -697,7 +744,7 @@ __device__ __forceinline__ void own_work(const PrefixArgs &a, const Plan &plan, 
       for (int i = 0; i < 8; ++i) y[i] = x[i >> 2][0][i & 3] * a.scale_log2;
       if (!full) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = (valid >> i & 1) ? y[i] : -INFINITY;
+        for (int i = 0; i < 8; ++i) y[i] = (sees >> i & 1) ? y[i] : -INFINITY;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = fmaxf(top, y[i]);
@@ -716,7 +763,7 @@ __device__ __forceinline__ void own_work(const PrefixArgs &a, const Plan &plan, 
       for (int i = 0; i < 8; ++i) y[i] = __builtin_amdgcn_exp2f(y[i] - ref);
       if (!full) {                                   // masked places may hold anything: zero times NaN is NaN
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = (valid >> i & 1) ? y[i] : 0.f;
+        for (int i = 0; i < 8; ++i) y[i] = (sees >> i & 1) ? y[i] : 0.f;
         if constexpr (Q8) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -743,13 +790,14 @@ __device__ __forceinline__ void own_work(const PrefixArgs &a, const Plan &plan, 
     l += __shfl_xor(l, 32);
     if (bad && ref > -INFINITY) l = __builtin_nanf("");
     if (c < cur.rows) {
-      const int64_t r = own_part(a, v, cur.b, cur.ht) + c;
+      const int64_t r = cur.part + (int64_t)v * (cur.pack ? kHeads : a.own_rows) + c;
+      const Parts &to = cur.pack ? a.packs : a.own_parts;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < VJ; j += 4)
-          *reinterpret_cast<f32x4 *>(a.own_parts.o + r * D + VJ * (4 * g + i) + j) = f32x4{o[0][j][i], o[0][j + 1][i], o[0][j + 2][i], o[0][j + 3][i]};
-      if (g == 0) *reinterpret_cast<f32x2 *>(a.own_parts.ml + 2 * r) = f32x2{ref, l};
+          *reinterpret_cast<f32x4 *>(to.o + r * D + VJ * (4 * g + i) + j) = f32x4{o[0][j][i], o[0][j + 1][i], o[0][j + 2][i], o[0][j + 3][i]};
+      if (g == 0) *reinterpret_cast<f32x2 *>(to.ml + 2 * r) = f32x2{ref, l};
     }
     cur = fetch;
   }
@@ -798,13 +846,25 @@ __global__ __launch_bounds__(64 * prefix_waves(D), D == 256 ? 1 : 2) void prefix
     }
     const int32_t tiles = (p.tokens + tile_tokens(D) - 1) / tile_tokens(D);
     p.row_tiles = (int32_t)(((int64_t)p.rows * a.group + kRows - 1) / kRows);
-    // Is it less to read the tokens for each row apart? 24 groups of 32 heads in 8, 1600 tokens: two rows of int8 take
-    // 35 us apart and 56 together, three 45 and 52 (fp32 out 66), four 56 and 54 (65); of fp16 52 and 46, 72 and 42.
-    if ((float)p.rows * a.tiles_per_kv * tiles <= a.apart * p.row_tiles * (tiles + kLead)) {
-      p.tokens = 0;
-      p.row_tiles = 0;
-    }
+    // Three ways, by what a KV head's tokens cost in steps of own work: once for up to 256 query rows, once for each
+    // pack, or for each row apart, behind whose own tokens they lie. us with 24 groups of 2, 4 and 8 rows of 32 heads on
+    // 8, 1600 tokens: together 56, 54, 56 (int8) and 46, 43, 49 (fp16), in packs 26, 28, 42 and 35, 38, 50, apart
+    // 35, 56 and 52, 95; with 43 groups of 128 heads on 8, whose packs are a row each, 353 tokens, 56 in packs and 44
+    // apart. With few tiles for each workgroup in all, latency counts, which is least together: 8 rows after 1000
+    // tokens 11, in packs 14.
+    const int32_t steps = (p.tokens + kTile - 1) / kTile;
+    const float together = a.tile_steps * p.row_tiles * (tiles + kLead), packs = (float)packs_of(a, p) * (steps + a.own_lead),
+                apart = (float)p.rows * a.tiles_per_kv * steps;
+    const bool few = (float)a.groups * a.kv_heads * (tiles + kLead) <= 2.5f * gridDim.x;
     p.units = p.tokens ? tiles + kLead : 0;
+    if (!few && apart <= min(packs, together)) {
+      p.tokens = 0;
+      p.units = 0;
+      p.row_tiles = 0;
+    } else if (!few && packs <= together) {
+      p.row_tiles = 0;
+      p.units = p.tokens ? steps + a.own_lead : 0;
+    }
     units += (uint32_t)(p.row_tiles * a.kv_heads) * (uint32_t)p.units;
   }
   units = scan_sum<W>(units, shared, plan);
@@ -817,12 +877,12 @@ __global__ __launch_bounds__(64 * prefix_waves(D), D == 256 ? 1 : 2) void prefix
     if (blockIdx.x == 0) a.plan[g] = mine[i];
   }
   __syncthreads();
-  // the rows' own tokens, a run of rows for each thread
+  // the packs and the rows' own tokens, a run of rows for each thread
   const int32_t per = (a.batch + NT - 1) / NT, my_b = tid * per;
   uint32_t my_units = 0, own;
   for (int32_t b = my_b; b < min(my_b + per, a.batch); ++b) {
     const int32_t g = plan.group_of(b, a.groups);
-    my_units += own_of(a, a.lens[b], g < 0 ? 0 : plan.g[g].tokens).units * (uint32_t)a.head_tiles;
+    my_units += own_of(a, a.lens[b], g < 0 ? 0 : plan.g[g].tokens).units * (uint32_t)a.head_tiles + (g < 0 ? 0 : pack_units(a, plan.g[g], b));
   }
   uint32_t my_at = my_units;
   my_at = scan_sum<W>(my_at, own, plan);
@@ -846,7 +906,7 @@ __global__ __launch_bounds__(64 * prefix_waves(D), D == 256 ? 1 : 2) void prefix
       const int32_t g = plan.group_of(b, a.groups);
       const uint32_t n = own_of(a, a.lens[b], g < 0 ? 0 : plan.g[g].tokens).units;
       a.rows[b] = RowPlan{g, u, n};
-      u += n * (uint32_t)a.head_tiles;
+      u += n * (uint32_t)a.head_tiles + (g < 0 ? 0 : pack_units(a, plan.g[g], b));
     }
   }
   if (blockIdx.x < workers) {
@@ -911,19 +971,26 @@ __global__ __launch_bounds__(256) void prefix_join_kernel(PrefixArgs a) {
       add(x, y);
     }
   };
+  const Line own = make_line(max(split.own, 1u), max(split.waves, 1u));
+  uint32_t own_at = rp.unit0;
   if (rp.group >= 0) {
     constexpr int32_t kRows = 32 * prefix_waves(D);
     const GroupPlan p = a.plan[rp.group];
-    const Line line = make_line(split.shared, split.workers);
-    const int32_t q = (b - p.row0) * a.group + hd - kvh * a.group, rt = q / kRows;
-    const uint32_t seg = (uint32_t)(kvh * p.row_tiles + rt), u0 = p.unit0 + seg * (uint32_t)p.units;
-    join(a.parts, line.holder(u0 + kLead), line.holder(u0 + (uint32_t)p.units - 1), part_row(a, p, 0, kvh, q), a.part_rows);
+    const int32_t q = (b - p.row0) * a.group + hd - kvh * a.group;
+    own_at += pack_units(a, p, b);
+    if (p.row_tiles) {
+      const Line line = make_line(split.shared, split.workers);
+      const uint32_t u0 = p.unit0 + (uint32_t)(kvh * p.row_tiles + q / kRows) * (uint32_t)p.units;
+      join(a.parts, line.holder(u0 + kLead), line.holder(u0 + (uint32_t)p.units - 1), part_row(a, p, 0, kvh, q), a.part_rows);
+    } else {
+      const uint32_t u0 = a.rows[p.row0].unit0 + (uint32_t)(kvh * packs_of(a, p) + q / kHeads) * (uint32_t)p.units;
+      join(a.packs, own.holder(u0), own.holder(u0 + (uint32_t)p.units - 1), pack_row(a, p, 0, kvh, q), kHeads);
+    }
   }
   if (rp.units) {
-    const Line line = make_line(split.own, split.waves);
     const int32_t head = hd - kvh * a.group, ht = kvh * a.tiles_per_kv + head / kHeads;
-    const uint32_t u0 = rp.unit0 + (uint32_t)ht * rp.units;
-    join(a.own_parts, line.holder(u0), line.holder(u0 + rp.units - 1), own_part(a, 0, b, ht) + head % kHeads, a.own_rows);
+    const uint32_t u0 = own_at + (uint32_t)ht * rp.units;
+    join(a.own_parts, own.holder(u0), own.holder(u0 + rp.units - 1), own_part(a, 0, b, ht) + head % kHeads, a.own_rows);
   }
   if constexpr (TEAMS > 1) {
     team_o[threadIdx.x] = o;
@@ -956,7 +1023,7 @@ constexpr int64_t kResident = 256;                 // workgroups that are reside
 // Where things lie in the workspace, in bytes, and the rows of the parts. A group's query rows of a KV head fill
 // all their tiles but one, so there are at most `segments` segments of shared work. Their rows are batch * heads at most.
 struct PrefixSpace {
-  int64_t plan, rows, parts, parts_ml, own_parts, own_ml, bytes;
+  int64_t plan, rows, parts, parts_ml, packs, packs_ml, own_parts, own_ml, bytes;
   int32_t part_rows, own_rows, own_waves;
 };
 
@@ -969,11 +1036,13 @@ int prefix_space(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t g
   const int64_t head_tiles = pool->kv_heads * ((group + kHeads - 1) / kHeads);
   const int64_t lead = own_lead((int)dim, pool->kind == QG_KV_Q8);
   const auto steps = [lead](int64_t n) { return (n + kTile - 1) / kTile + 1 + lead; };   // from the middle of one on: one more
-  if (units > 0x7FFFFFFF || batch * head_tiles * steps(max_len) > 0x7FFFFFFF) return QG_ERR_SHAPE;
+  const int64_t packs = pool->kv_heads * (batch * group / kHeads + (groups < batch / 2 ? groups : batch / 2));
+  const int64_t pack_units = groups ? packs * steps(max_len) : 0;
+  if (units > 0x7FFFFFFF || batch * head_tiles * steps(max_len) + pack_units > 0x7FFFFFFF) return QG_ERR_SHAPE;
   // what is past the prefix's last whole page is a row's own, too
   const int64_t tail = max_tail + pool->page_tokens < max_len ? max_tail + pool->page_tokens : max_len;
-  // room for max_tail tokens of every row, and for one row that shares nothing
-  const int64_t own = std::max(batch * steps(tail), steps(max_len)) * head_tiles, workers = units < kResident ? units : kResident;
+  // room for max_tail tokens of every row and for the packs, and for one row that shares nothing
+  const int64_t own = std::max(batch * steps(tail), steps(max_len)) * head_tiles + pack_units, workers = units < kResident ? units : kResident;
   s->own_waves = (int32_t)(own < kResident * waves ? own : kResident * waves);
   s->part_rows = (int32_t)(batch * group < rows ? batch * group : rows);
   s->own_rows = (int32_t)(group < kHeads ? group : kHeads);
@@ -984,7 +1053,10 @@ int prefix_space(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t g
   const int64_t all = workers ? workers * s->part_rows + batch * heads : 0;
   const int64_t all_own = batch ? s->own_rows * (s->own_waves + batch * head_tiles) : 0;
   s->parts_ml = s->parts + 4 * dim * all;
-  s->own_parts = s->parts_ml + up(8 * all);
+  const int64_t all_packs = groups ? (int64_t)s->own_waves * kHeads + batch * heads : 0;
+  s->packs = s->parts_ml + up(8 * all);
+  s->packs_ml = s->packs + 4 * dim * all_packs;
+  s->own_parts = s->packs_ml + up(8 * all_packs);
   s->own_ml = s->own_parts + 4 * dim * all_own;
   s->bytes = s->own_ml + up(8 * all_own);
   return QG_OK;
@@ -1086,8 +1158,8 @@ int qg_prefix_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q
   // 2.1 (79 rows of 48 heads after 6127 tokens: 98 us with 2.3 here, 90 with 2.1; 128 of 32 heads of 128: 72 and 73).
   const double tile_us = (out_f32 ? 3.0 : 2.3) * (pool->head_dim == 256 ? 0.92 : 1.0);
   a.shared_cost = (float)(tile_us / own_step_us(pool->head_dim, pool->kind == QG_KV_Q8));
-  // the tile's tokens as own work, on all of the card: decoding as above, fp16 at HBM's 6 TB/s, 23 KB a us for each
-  a.apart = (float)(tile_us / (pool->kind == QG_KV_Q8 ? 8192 * 2.125 / 30e3 : 8192 * 4.0 / 23e3));
+  // on all of the card: decoding as above, fp16 at HBM's 6 TB/s, 23 KB a us for each workgroup
+  a.tile_steps = (float)(tile_us / (32 * pool->head_dim * (pool->kind == QG_KV_Q8 ? 2.125 / 30e3 : 4.0 / 23e3)));
   const float size = std::fabs(scale * kLog2e);
   a.scale_log2 = size < FLT_MIN ? 1.0f : size;
   a.keep = size < FLT_MIN ? 0 : 0xFFFFFFFFu;
@@ -1100,6 +1172,7 @@ int qg_prefix_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q
   a.plan = reinterpret_cast<GroupPlan *>(ws + w.plan);
   a.rows = reinterpret_cast<RowPlan *>(ws + w.rows);
   a.parts = Parts{reinterpret_cast<float *>(ws + w.parts), reinterpret_cast<float *>(ws + w.parts_ml)};
+  a.packs = Parts{reinterpret_cast<float *>(ws + w.packs), reinterpret_cast<float *>(ws + w.packs_ml)};
   a.own_parts = Parts{reinterpret_cast<float *>(ws + w.own_parts), reinterpret_cast<float *>(ws + w.own_ml)};
   const bool q8 = pool->kind == QG_KV_Q8;
   const hipStream_t s = static_cast<hipStream_t>(stream);

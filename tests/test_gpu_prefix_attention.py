@@ -277,6 +277,37 @@ def test_groups_round_the_choice_to_share(kind, sizes, prefixes, heads, kv_heads
     check(out, lse, paged.attention(c, 0, q, table, lens, max(lens), dim ** -0.5), max(lens), dim, c)
 
 
+@pytest.mark.parametrize("kind,dim,heads,kv_heads,tokens", [
+    ("q8", 64, 32, 16, 16), ("f16", 64, 14, 14, 32), ("q8", 128, 60, 20, 16), ("f16", 128, 80, 16, 64), ("q8", 256, 16, 16, 16), ("f16", 256, 45, 15, 16),
+    ("q8", 64, 256, 16, 16), ("f16", 64, 272, 16, 16)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_many_groups_of_few_rows(kind, dim, heads, kv_heads, tokens, f32):
+    """Enough of them that their tokens are read once for 16 query rows (or, with 16 heads of a KV head, for each
+    row): rows shorter than their prefix, of no token, of equal and of different lengths, missing pages, queries that are
+    not finite."""
+    sizes, prefixes = [2, 3, 1, 5, 4, 2, 7, 2, 3, 2], [100, 64, 90, 33, 160, 47, 16, 96, 128, 70]
+    owner = [g for g, n in enumerate(sizes) for _ in range(n)]
+    lens = [prefixes[g] + (5 * b) % 23 for b, g in enumerate(owner)]
+    lens[1], lens[4], lens[8], lens[18], lens[22] = 40, 0, 1, 17, 128
+    c, table = shared_cache(kind, sizes, prefixes, lens, kv_heads, dim, tokens, 31)
+    for b in (11, 12, 13, 14):                            # the group that starts at row 11 misses a page in its prefix
+        table[b, 1] = -1
+    rng = np.random.default_rng(5)
+    q = (rng.standard_normal((len(lens), heads, dim)) * 1.5).astype(np.float16)
+    want = paged.attention(c, 0, q, table, lens, max(lens), dim ** -0.5)
+    args = [dev(table), dev(lens), dev(starts_of(sizes)), dev(prefixes)]
+    out, lse = qg.prefix_attention(upload(c), dev(q, np.float16), *args, max_tail=30, out_f32=f32, return_lse=True)
+    check(out, lse, want, max(lens), dim, c)
+    odd = q.copy()
+    odd[2, 1], odd[9, 0, 3], odd[20, heads - 1, dim - 1] = np.nan, np.inf, -np.inf
+    got, got_lse = qg.prefix_attention(upload(c), dev(odd, np.float16), *args, max_tail=30, out_f32=f32, return_lse=True)
+    bad = ~np.isfinite(odd).all(-1)
+    seen = bad & ~np.isneginf(want[1])
+    assert np.isnan(got.cpu().numpy()[seen]).all() and np.isnan(got_lse.cpu().numpy()[seen]).all()
+    rest = torch.from_numpy(~bad).cuda()
+    assert torch.equal(got[rest], out[rest]) and torch.equal(got_lse[rest], lse[rest])
+
+
 @pytest.mark.parametrize("kind,dim", [("q8", 64), ("f16", 256)])
 def test_long_rows_without_a_group(kind, dim):
     """More own tokens than max_tail says: the workspace's room for partial results spreads them less."""
