@@ -3,10 +3,11 @@
 // A group's rows with the heads of a KV head are one block of queries against the shared tokens: unlike a single
 // sequence's few heads, enough of them to keep the matrix cores busy. One launch does both kinds of work, each on its
 // share of the workgroups: the shared tokens, once a group, in one pass with a running reference, up to 256 query rows
-// a workgroup, and the tokens that a row has for itself, as paged_attn.hip does them, a wave for up to 16 heads. A
-// second launch joins the parts.
+// a workgroup, and the tokens that a row has for itself, as paged_attn.hip does them, a wave for up to 16 heads. The
+// second kind also takes groups of few rows, 16 query rows (rows by heads) in place of a row's heads, or
+// their rows one by one. A second launch joins the parts.
 //
-// Measured: 128 rows of 32 heads on 8 of 128 after 16384 shared int8 tokens, up to 1024 of their own, take 71 and 8 us; a
+// Measured: 128 rows of 32 heads on 8 of 128 after 16384 shared int8 tokens, up to 1024 of their own, take 72 and 8 us; a
 // pass over the shared tokens for each row would read 4.6 GB, 670 us at HBM's rate. Shared work reaches 800 to 930
 // TFLOP/s on its workgroups; a large library product 1150 on all. Of a tile's 2.2 us the matrix instructions are
 // busy for 1.0, the vector instructions about as long, LDS for 0.9, and the two waves of a SIMD do not overlap
@@ -38,10 +39,9 @@ __host__ __device__ constexpr int tile_tokens(int dim) { return 8192 / dim; }
 constexpr int kHeads = 16;
 constexpr int kMaxGroups = 1023;
 
-// What the workgroups find out of a group (of at least two rows). Its query rows are rows * (heads of a KV head), in
-// tiles a KV head; its tokens, whole pages, are tiles too, `units` with the lead. On the line of shared work its
-// segments (KV head, row tile) follow each other, `units` each: the lead, which stands for what the start of a segment
-// costs a worker that comes from another one, then the tiles.
+// Both kinds of work lie on a line each, segment after segment, and every worker (a workgroup of shared work, a wave of
+// own work) gets an equal part of its line. A segment's first units are a lead, which stands for what its start costs a
+// worker that comes from another one.
 constexpr int32_t kLead = 4;
 // The same for own work, about 3 us; a step takes what its bytes do, of which the waves of a workgroup together
 // get 38 KB a us, or 30 where they are decoded. (64 rows after 8192 fp16 tokens take 46 us at 30 and 44 at 36 to 42,
@@ -50,6 +50,9 @@ __host__ __device__ constexpr double own_step_us(int dim, bool q8) {
   return prefix_waves(dim) * 32 * dim * (q8 ? 2.125 / 30e3 : 4.0 / 38e3);
 }
 __host__ __device__ constexpr int32_t own_lead(int dim, bool q8) { return (int32_t)(3.0 / own_step_us(dim, q8) + 0.5); }
+// What the workgroups find out of a group (of at least two rows). Its query rows are rows * (heads of a KV head), in
+// tiles a KV head; its tokens, whole pages, are tiles too. On the line of shared work its segments (KV head, row tile)
+// follow each other, `units` each.
 struct GroupPlan {
   int32_t row0, rows, tokens, row_tiles, units;
   uint32_t unit0;                // units of the groups before
