@@ -11,9 +11,9 @@
 // pass over the shared tokens for each row would read 4.6 GB, 670 us at HBM's rate. Shared work reaches 800 to 930
 // TFLOP/s on its workgroups; a large library product 1150 on all. Of a tile's 2.2 us the matrix instructions are
 // busy for 1.0, the vector instructions about as long, LDS for 0.9, and the two waves of a SIMD do not overlap
-// them all. Own work runs at 30 to 38 KB a us and workgroup: instruction issue for int8, loads in flight for
+// them all. Own work runs at 28 to 38 KB a us and workgroup: instruction issue for int8, loads in flight for
 // fp16. Short calls are latency: 3 us for the plan, 5 to the first scores (page, K, LDS), 2 to 3 to
-// store the parts, 4 to 9 for the join (8 rows after 1000 tokens: 11 and 4).
+// store the parts, 4 to 9 for the join (8 rows after 1000 tokens: 12 and 4).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -44,10 +44,10 @@ constexpr int kMaxGroups = 1023;
 // worker that comes from another one.
 constexpr int32_t kLead = 4;
 // The same for own work, about 3 us; a step takes what its bytes do, of which the waves of a workgroup together
-// get 38 KB a us, or 30 where they are decoded. (64 rows after 8192 fp16 tokens take 46 us at 30 and 44 at 36 to 42,
+// get 38 KB a us, or 28 where they are decoded. (64 rows after 8192 fp16 tokens take 46 us at 30 and 44 at 36 to 42,
 // 128 after 16384 int8 ones 80 us at 24 and at 42 and 76 to 77 at 28 to 30.)
 __host__ __device__ constexpr double own_step_us(int dim, bool q8) {
-  return prefix_waves(dim) * 32 * dim * (q8 ? 2.125 / 30e3 : 4.0 / 38e3);
+  return prefix_waves(dim) * 32 * dim * (q8 ? 2.125 / 28e3 : 4.0 / 38e3);
 }
 __host__ __device__ constexpr int32_t own_lead(int dim, bool q8) { return (int32_t)(3.0 / own_step_us(dim, q8) + 0.5); }
 // What the workgroups find out of a group (of at least two rows). Its query rows are rows * (heads of a KV head), in
@@ -589,7 +589,7 @@ struct OwnSegment {
   int32_t b;
   Own seen;
   int32_t h0, rows;          // its first head, query rows
-  int32_t m0, per;           // query row i: row b + (m0 + i) / per, head h0 + (m0 + i) % per
+  int32_t m0;                // of a pack: its first query row
   bool pack;
   int64_t part;              // its first row of wave 0's partial results
   const uint8_t *kv;         // its KV head's part of page 0
@@ -625,7 +625,6 @@ __device__ __forceinline__ OwnSegment own_segment(const PrefixArgs &a, const Pla
     kvh = i / n;
     s.u0 = row_at + (uint32_t)i * s.seen.units;
     s.m0 = (i - kvh * n) * kHeads;
-    s.per = a.group;
     s.h0 = kvh * a.group;
     s.rows = min(kHeads, p.rows * a.group - s.m0);
     s.part = pack_row(a, p, 0, kvh, s.m0);
@@ -635,7 +634,6 @@ __device__ __forceinline__ OwnSegment own_segment(const PrefixArgs &a, const Pla
     kvh = ht / a.tiles_per_kv;
     const int32_t first_head = (ht - kvh * a.tiles_per_kv) * kHeads;
     s.m0 = 0;
-    s.per = kHeads;
     s.h0 = kvh * a.group + first_head;
     s.rows = min(kHeads, a.group - first_head);
     s.part = own_part(a, 0, b, ht);
@@ -680,8 +678,13 @@ __device__ __forceinline__ void own_work(const PrefixArgs &a, const Plan &plan, 
   };
   int32_t limit = 0;                                 // the tokens that the lane's query row sees; of the segment in q
   auto load_q = [&]() {                              // query rows past the segment's are its last: nobody reads their results
-    const int32_t m = fetch.m0 + min(c, fetch.rows - 1), down = m / fetch.per, b = fetch.b + down;
-    const uint16_t *from = a.q + b * a.ldq + (int64_t)(fetch.h0 + m - down * fetch.per) * D + 16 * g;
+    int32_t m = fetch.m0 + min(c, fetch.rows - 1), b = fetch.b;
+    if (fetch.pack) {
+      const int32_t down = m / a.group;
+      b += down;
+      m -= down * a.group;
+    }
+    const uint16_t *from = a.q + b * a.ldq + (int64_t)(fetch.h0 + m) * D + 16 * g;
     limit = a.lens[b];
 #pragma unroll
     for (int i = 0; i < T::KD; ++i) q[0][i] = *reinterpret_cast<const half8_t *>(from + 64 * (i >> 1) + 8 * (i & 1));
@@ -1161,7 +1164,7 @@ int qg_prefix_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q
   // 2.1 (79 rows of 48 heads after 6127 tokens: 98 us with 2.3 here, 90 with 2.1; 128 of 32 heads of 128: 72 and 73).
   const double tile_us = (out_f32 ? 3.0 : 2.3) * (pool->head_dim == 256 ? 0.92 : 1.0);
   a.shared_cost = (float)(tile_us / own_step_us(pool->head_dim, pool->kind == QG_KV_Q8));
-  // on all of the card: decoding as above, fp16 at HBM's 6 TB/s, 23 KB a us for each workgroup
+  // on all of the card: int8 at 30 KB a us for each workgroup, fp16 at HBM's 6 TB/s, which are 23
   a.tile_steps = (float)(tile_us / (32 * pool->head_dim * (pool->kind == QG_KV_Q8 ? 2.125 / 30e3 : 4.0 / 23e3)));
   const float size = std::fabs(scale * kLog2e);
   a.scale_log2 = size < FLT_MIN ? 1.0f : size;
