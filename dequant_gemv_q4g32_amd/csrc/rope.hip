@@ -4,8 +4,9 @@
 // A head x of D elements becomes y = x / sqrt(mean x^2 + eps) * w where it has weights (else y = x), and
 // the pair (y1, y2) with frequency f becomes factor * (y1 cos t - y2 sin t, y2 cos t + y1 sin t), t =
 // position * f. All of it in fp32 with one rounding to fp16 at the end, except the angle: a position
-// of 100000 times a frequency near 1 leaves fp32 an error of 0.004 radians, so position * f is fp64 and
-// so is its reduction to a part of a turn, which fp32 then holds to 2^-25.
+// of 100000 times a frequency near 1 leaves fp32 an error of 0.004 radians, so position * f is fp64, and so are its
+// reduction to a part of a turn, cosine and sine, once for all heads of a token. The fp32 instructions for these are
+// off by up to 2^-23, and an int8 code that the key's fp16 rounding decides would go with them.
 //
 // A lane takes 8 elements of a head (16 bytes), D / 8 lanes a head, so that a norm is a sum over 8 to 32
 // neighbouring lanes and a pair's other half is 8 elements of another lane of the same head.
@@ -79,8 +80,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
   if (pos < 0) return;
   if (tid < a.half) {
     const double t = (double)pos * a.freqs[tid] * 0.15915494309189533577;
-    const float r = (float)(t - __builtin_rint(t));
-    turn[tid] = float2_t{a.factor * __builtin_amdgcn_cosf(r), a.factor * __builtin_amdgcn_sinf(r)};
+    const double r = 2 * (t - __builtin_rint(t));
+    turn[tid] = float2_t{(float)(a.factor * cospi(r)), (float)(a.factor * sinpi(r))};
   }
   int32_t at = 0;
   uint8_t *page = nullptr;
@@ -116,7 +117,9 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
     for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(y[j], y[j], ss);
     ss = head_sum<D>(ss);
     if (weight) {
-      const float inv = __builtin_amdgcn_rsqf(ss * (1.0f / D) + a.eps);
+      const float mean = ss * (1.0f / D) + a.eps;
+      float inv = __builtin_amdgcn_rsqf(mean);       // to one step, and to half of one by
+      inv = __builtin_fmaf(0.5f * inv, __builtin_fmaf(-(mean * inv), inv, 1.0f), inv);
       float w[8];
       unpack8(*reinterpret_cast<const u32x4 *>(weight + e), w);
 #pragma unroll
