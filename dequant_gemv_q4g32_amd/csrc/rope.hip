@@ -3,10 +3,9 @@
 //
 // A head x of D elements becomes y = x / sqrt(mean x^2 + eps) * w where it has weights (else y = x), and
 // the pair (y1, y2) with frequency f becomes factor * (y1 cos t - y2 sin t, y2 cos t + y1 sin t), t =
-// position * f. All of it in fp32 with one rounding to fp16 at the end, except the angle: a position
-// of 100000 times a frequency near 1 leaves fp32 an error of 0.004 radians, so position * f is fp64, and so are its
-// reduction to a part of a turn, cosine and sine, once for all heads of a token. The fp32 instructions for these are
-// off by up to 2^-23, and an int8 code that the key's fp16 rounding decides would go with them.
+// position * f. All of it in fp32 with one rounding to fp16 at the end, but in fp64 for int8 keys and the angle: a position
+// of 100000 times a frequency near 1 leaves fp32 an error of 0.004 radians. Its reduction to a part of a turn, cosine
+// and sine are made once for all heads of a token.
 //
 // A lane takes 8 elements of a head (16 bytes), D / 8 lanes a head, so that a norm is a sum over 8 to 32
 // neighbouring lanes and a pair's other half is 8 elements of another lane of the same head.
@@ -31,6 +30,7 @@
 namespace qg {
 
 typedef float float2_t __attribute__((ext_vector_type(2)));
+typedef double double2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kRopeThreads = 256;
 
@@ -69,11 +69,53 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
+// A key on its way to int8, in fp64: its largest element of 32 decides the codes of all of them, and where that is
+// rounded to fp16 the other way, or a code lies near a tie, a code changes, by up to a hundredth of the largest. In fp32
+// one key element in 10000 is rounded the other way. A decode step takes 0.5 us more for it; for fp16 results, where it
+// would be half a step in one of 10000, it would take 82 us in place of 67 (8192 tokens).
+template <int D>
+__device__ __forceinline__ void key_head(float *y, const float *z, const uint16_t *weight, int away, float eps, const double2_t *turn,
+                                         bool rotated, bool interleaved, bool second, int e, int half) {
+  double yd[8], zd[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    yd[j] = y[j];
+    zd[j] = z[j];
+  }
+  if (weight) {
+    double ss = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss += yd[j] * yd[j];
+#pragma unroll
+    for (int o = 1; o < D / 8; o <<= 1) ss += __shfl_xor(ss, o);
+    const double inv = 1.0 / sqrt(ss * (1.0 / D) + (double)eps);
+    float w[8], v[8];
+    unpack8(*reinterpret_cast<const u32x4 *>(weight), w);
+    unpack8(*reinterpret_cast<const u32x4 *>(weight + away), v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      yd[j] *= inv * w[j];
+      zd[j] *= inv * v[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    double r = yd[j];
+    if (rotated) {
+      const double2_t cs = turn[interleaved ? (e + j) / 2 : second ? e - half + j : e + j];
+      const double o = (interleaved ? yd[j ^ 1] : zd[j]) * cs[1];
+      r = yd[j] * cs[0] + ((interleaved ? (j & 1) == 0 : !second) ? -o : o);
+    }
+    y[j] = (float)r;
+  }
+}
+
 // Workgroup (token, y): the token's heads, its K and its V, 2048 / D of them a step.
 template <int D, int TO>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
   constexpr int L = D / 8, kUnits = kRopeThreads / L;
-  __shared__ float2_t turn[D / 2];                    // factor * (cos, sin) of the pairs
+  __shared__ float2_t turn[D / 2];                    // factor * (cos, sin) of the pairs; the same
+  __shared__ double2_t turn_k[TO == kPagesQ8 ? D / 2 : 1];   // for keys that become int8
   const uint32_t row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, l = tid % L, e = 8 * l;
   const int32_t pos = a.rows.positions[row];
@@ -81,7 +123,9 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
   if (tid < a.half) {
     const double t = (double)pos * a.freqs[tid] * 0.15915494309189533577;
     const double r = 2 * (t - __builtin_rint(t));
-    turn[tid] = float2_t{(float)(a.factor * cospi(r)), (float)(a.factor * sinpi(r))};
+    const double2_t cs = double2_t{a.factor * cospi(r), a.factor * sinpi(r)};
+    turn[tid] = float2_t{(float)cs[0], (float)cs[1]};
+    if constexpr (TO == kPagesQ8) turn_k[tid] = cs;
   }
   int32_t at = 0;
   uint8_t *page = nullptr;
@@ -116,7 +160,9 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(y[j], y[j], ss);
     ss = head_sum<D>(ss);
-    if (weight) {
+    if (TO == kPagesQ8 && kind == 1) {
+      key_head<D>(y, z, weight ? weight + e : nullptr, 8 * (other - lane), a.eps, turn_k, rotated, a.interleaved, second, e, a.half);
+    } else if (weight) {
       const float mean = ss * (1.0f / D) + a.eps;
       float inv = __builtin_amdgcn_rsqf(mean);       // to one step, and to half of one by
       inv = __builtin_fmaf(0.5f * inv, __builtin_fmaf(-(mean * inv), inv, 1.0f), inv);
@@ -128,7 +174,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[j] = z[j] * inv * w[j];
     }
-    if (rotated && kind < 2) {
+    if (rotated && kind < (TO == kPagesQ8 ? 1 : 2)) {
       float r[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {

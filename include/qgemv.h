@@ -610,7 +610,8 @@ int qg_qk_rope(const qg_rotary *rotary, int64_t head_dim, int64_t heads, int64_t
                uint16_t *k_out, int64_t ld_k_out, void *stream);
 
 /* qg_qk_rope and qg_kv_append in one pass: the queries into q_out, the keys (rounded to fp16) and the values v into
- * `layer` of the pool, the same bytes as by the two calls. A row with a position below 0 is skipped, one whose
+ * `layer` of the pool: for fp16 pages the same bytes as by the two calls; for int8 pages keys are computed in fp64
+ * before their rounding to fp16, which is the other way than qg_qk_rope's in one of some 10000 elements. A row with a position below 0 is skipped, one whose
  * place is no page (see qg_kv_append) gives its queries only. What is cached, rotated keys among it, is finite.
  * heads may be 0. q_out may be q as above, and overlaps nothing else that the call reads. Sizes and alignment of
  * qg_qk_rope for q and q_out, of qg_kv_append for k and v; errors of both. */

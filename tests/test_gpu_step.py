@@ -251,7 +251,8 @@ def test_qk_rope_many_tokens():
     (128, 128, False, 32, 8, 9, True), (64, 32, True, 6, 3, 20, False), (256, 64, True, 8, 1, 5, True), (64, 64, False, 0, 12, 4, True),
     (128, 48, False, 5, 5, 1, False), (128, 128, False, 4, 1, 1500, False)])
 def test_append_rope(kind, dim, rot, inter, heads, kv_heads, count, norm):
-    """The same bytes as qk_rope and kv_append one after the other; rows without a place, and skipped ones."""
+    """The same bytes as qk_rope and kv_append one after the other, for int8 pages with the keys as fp64 rounds them; rows
+    without a place, and skipped ones."""
     rng = np.random.default_rng(dim + count)
     tokens, layers, rows = 16, 2, 7
     width = -(-count // (tokens * rows)) + 2
@@ -271,7 +272,12 @@ def test_append_rope(kind, dim, rot, inter, heads, kv_heads, count, norm):
     rotary = qg.Rotary(dim, qg.rope_freqs(rot, 10000.0, "linear", 2.0), inter, *w)
     before = torch.full((count, heads * dim), 3.0, dtype=torch.float16, device="cuda")
     got = qg.kv_append_rope(pool, dev(table), rotary, q if heads else None, k, v, dev(pos), dev(seqs), q_out=before.clone() if heads else None, layer=1)
+    keys = k.cpu().numpy().reshape(count, kv_heads, dim)   # k itself is the output where it is dense
     want_q, want_k = qg.qk_rope(rotary, q, k, dev(pos), q_out=before.clone(), k_out=k.contiguous())
+    if kind == "q8":
+        freqs, weight = qg.rope_freqs(rot, 10000.0, "linear", 2.0), None if w[1] is None else w[1].cpu().numpy()
+        exact = np.stack([[step.rotate(x, p, freqs, inter, weight, float(np.float32(1e-6))) for x in heads_] for heads_, p in zip(keys, pos)])
+        want_k = dev(exact.astype(np.float32).reshape(count, -1), np.float16)
     qg.kv_append(other, dev(table), want_k, v, dev(pos), dev(seqs), layer=1)
     torch.cuda.synchronize()
     assert torch.equal(got, want_q) if heads else got is None
