@@ -10,10 +10,10 @@
 // A lane takes 8 elements of a head (16 bytes), D / 8 lanes a head, so that a norm is a sum over 8 to 32
 // neighbouring lanes and a pair's other half is 8 elements of another lane of the same head.
 //
-// HBM bounds it: 8192 tokens of 64 and 8 heads of 128 into fp16 pages, 336 MB read and written, take 66 us, 5.1 TB/s
+// HBM bounds it: 8192 tokens of 64 and 8 heads of 128 into fp16 pages, 336 MB read and written, take 67 us, 5.0 TB/s
 // (torch's copy of 2 GiB: 4.9), 4099 of 16 and 4 heads of 256, normed, 84 MB, 19 us. A workgroup takes a token, so that
 // cosines and sines are made once for all its heads; with fewer than 1024 tokens its heads are shared over several, as a
-// single token's would otherwise wait for each other. One token takes 4.0 us and 64 take 4.8: a chain of
+// single token's would otherwise wait for each other. One token into int8 pages takes 5.0 us and 64 take 5.5: a chain of
 // position, frequency and table entry behind a launch.
 #include <hip/hip_runtime.h>
 
