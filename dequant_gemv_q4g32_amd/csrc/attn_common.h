@@ -20,6 +20,10 @@ constexpr int kTile = 32;                          // tokens of a wave's step, t
 // fp16's 65504 and small ones lose nothing above 2^-31 of the largest, while most steps find ref good
 // as it is. The difference itself is compared, as the weights use it: ref + 15 rounds up to ref + 16
 // for scores of 2^24 to 2^28.
+// A weight below 2^-14 is a subnormal fp16 number (as a pair: its remainder is), off by up to 2^-25, which is 2^-31 of the
+// weights' sum at most: that is 2^6 or more while s - 7 is good to one, below scores of 2^24. Larger scores
+// differ by multiples of 2^k, 2^(k + 24) being their size, so that what of a weight is lost is at most 2^-25, 2^-26, 2^-28 and 2^-32
+// for k = 0, 1, 2 and from 3 on, while the sum is at least 2^6, 2^5, 2^4 and 1.
 constexpr float kLow = 7.0f, kHigh = 15.0f;
 
 template <typename T>

@@ -38,6 +38,10 @@ __host__ __device__ constexpr int tile_tokens(int dim) { return 8192 / dim; }
 // Heads of a KV head that a wave takes against a row's own tokens.
 constexpr int kHeads = 16;
 constexpr int kMaxGroups = 1023;
+// Scores (s times the scale, units of log2) from which on a weight takes its exponent from the rounded product, as own
+// work's do and as the reference is placed; below, from s by one fused operation. The two differ by half a
+// last place of the score: here 2^-13 at most, but 16 for a score of 2^28, which would carry weights out of fp16.
+constexpr float kFused = 4096.0f;
 
 // Both kinds of work lie on a line each, segment after segment, and every worker (a workgroup of shared work, a wave of
 // own work) gets an equal part of its line. A segment's first units are a lead, which stands for what its start costs a
@@ -420,6 +424,7 @@ __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &pla
 #pragma unroll
       for (int j = 0; j < 16; ++j) o[i][j] = 0.f;
     float ref = -INFINITY, l = 0.f;
+    bool rounded = false;                            // whether a reference of the wave is past kFused
 
     __syncthreads();                                 // the segment before is done with LDS
     kt.write(lds_k);
@@ -487,6 +492,12 @@ __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &pla
             l *= keep;
           }
           const float off = ref == -INFINITY ? 0.f : -ref;   // no token so far: all weights are 2^-inf
+          if (moves) rounded = __any(fabsf(off) >= kFused);
+          if (rounded) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[j] *= a.scale_log2;
+          }
+          const float times = rounded ? 1.0f : a.scale_log2;
           // One step in slots, in the order written: a matrix instruction, the read of the operand of the one four
           // slots on, a part of the softmax. Past the last tile the scores are of what is there, and nobody reads them.
           const u32x4 *ks = lds_k + (tb + 1 < TB ? now : ahead) * S::KTile + k_at + 32 * ((tb + 1) % TB) * S::KRow;
@@ -514,7 +525,7 @@ __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &pla
             if (i + kRing < kSlots) ring[i % kRing] = read(i + kRing);
 #pragma unroll
             for (int j = 16 * i / kSlots; j < 16 * (i + 1) / kSlots; ++j) {
-              float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], a.scale_log2, off));
+              float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j], times, off));
               asm volatile("" : "+v"(y));            // here and not where it is used
               l += y;
               asm volatile("" : "+v"(l));

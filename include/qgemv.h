@@ -512,7 +512,7 @@ int qg_kv_compact(const qg_kv_pool *pool, const int32_t *table, int64_t ld_table
  * row's own entries. A row that is shorter than the prefix sees its lens tokens.
  * Values of starts outside [0, batch] count as the nearest of these, one below an earlier one as that one.
  * The result is defined as qg_paged_attention's with window 0, with these bounds of the error: with fp32
- * out the same, and 2^-32 sum |V_j| for weights below fp16's normal range; with fp16 out the weights e^(s_j - max) of
+ * out the same, and 2^-31 sum |V_j| for weights below fp16's normal range; with fp16 out the weights e^(s_j - max) of
  * shared tokens meet V as one fp16 number, 2^-11 of each weight, rounded to nearest, on top (the denominators add the
  * unrounded weights).
  *
