@@ -560,8 +560,7 @@ def prefix_attention(pool, q, table, lens, starts, prefix, max_len: Optional[int
     starts[g] to starts[g + 1] - 1 (int32 [groups + 1], ascending); the first prefix[g] tokens (int32 [groups]) of its
     rows are the same, by pages that they share or by equal ones. Rows in no group, and what follows a prefix, are read as by
     paged_attention. max_tail bounds the tokens that a row does not share (default: max_len); more of them are slower,
-    no less right. The other arguments and the results are paged_attention's, without a window; fp16 results
-    carry one more rounding of the shared tokens' weights to fp16."""
+    no less right. The other arguments and the results are paged_attention's, without a window."""
     if stream is not None or _device_now() != pool._index:
         with _on(pool, stream):
             return prefix_attention(pool, q, table, lens, starts, prefix, max_len, max_tail, scale, out, out_f32, lse, return_lse,

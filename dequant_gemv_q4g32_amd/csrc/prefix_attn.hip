@@ -7,11 +7,11 @@
 // second kind also takes groups of few rows, 16 query rows (rows by heads) in place of a row's heads, or
 // their rows one by one. A second launch joins the parts.
 //
-// Measured: 128 rows of 32 heads on 8 of 128 after 16384 shared int8 tokens, up to 1024 of their own, take 72 and 8 us; a
-// pass over the shared tokens for each row would read 4.6 GB, 670 us at HBM's rate. Shared work reaches 800 to 930
-// TFLOP/s on its workgroups; a large library product 1150 on all. Of a tile's 2.2 us the matrix instructions are
-// busy for 1.0, the vector instructions about as long, LDS for 0.9, and the two waves of a SIMD do not overlap
-// them all. Own work runs at 28 to 38 KB a us and workgroup: instruction issue for int8, loads in flight for
+// Measured: 128 rows of 32 heads on 8 of 128 after 16384 shared int8 tokens, up to 1024 of their own, take 93 and 8 us; a
+// pass over the shared tokens for each row would read 4.6 GB, 670 us at HBM's rate. Shared work reaches 530 to 650
+// TFLOP/s on its workgroups, the weights' second halves not counted; a large library product 1150 on all. Of a tile's 3.3 us
+// the matrix instructions are busy for 1.5, the vector instructions about as long, LDS for 0.9, and the two waves of a SIMD do
+// not overlap them all. Own work runs at 28 to 38 KB a us and workgroup: instruction issue for int8, loads in flight for
 // fp16. Short calls are latency: 3 us for the plan, 5 to the first scores (page, K, LDS), 2 to 3 to
 // store the parts, 4 to 9 for the join (8 rows after 1000 tokens: 12 and 4).
 #include <hip/hip_runtime.h>
@@ -48,8 +48,8 @@ constexpr float kFused = 4096.0f;
 // worker that comes from another one.
 constexpr int32_t kLead = 4;
 // The same for own work, about 3 us; a step takes what its bytes do, of which the waves of a workgroup together
-// get 38 KB a us, or 28 where they are decoded. (64 rows after 8192 fp16 tokens take 46 us at 30 and 44 at 36 to 42,
-// 128 after 16384 int8 ones 80 us at 24 and at 42 and 76 to 77 at 28 to 30.)
+// get 38 KB a us, or 28 where they are decoded. (64 rows after 8192 fp16 tokens take 62 us at 30 and 38 and 64 at 46, 128
+// after 16384 int8 ones 102 at 28 and 103 at 24 and 36, 48 rows of 16 heads of 256 41 at 24 and 28 and 43 at 36.)
 __host__ __device__ constexpr double own_step_us(int dim, bool q8) {
   return prefix_waves(dim) * 32 * dim * (q8 ? 2.125 / 28e3 : 4.0 / 38e3);
 }
@@ -204,8 +204,8 @@ __device__ __forceinline__ Own own_of(const PrefixArgs &a, int32_t raw, int32_t 
 // place 2 s + h). 16 neighbouring lanes read the same place of neighbouring rows at once, which shall lie in different
 // banks, and all places of a lane are constants away from one address. So a row of K has 16 bytes more than
 // it needs; V^T, which a lane writes four rows apart from its neighbour, has rows of 4 places mod 16 and one more after
-// every four rows: both ways all 16 differ. (With one more place a row the writes met 4 to a bank: 128 rows after
-// 16384 int8 tokens took 76 us, now 72.)
+// every four rows: both ways all 16 differ. (With one more place a row the writes met 4 to a bank: 4 us more for 128 rows
+// after 16384 int8 tokens.)
 template <int D, bool Q8>
 struct Shape {
   static constexpr int NT = 64 * prefix_waves(D);
@@ -290,9 +290,10 @@ struct StagedV {
   }
 };
 
-// A worker's part [at, end) of the line of shared work, segment by segment. PAIRS: weights as hi + lo fp16 pairs (22
-// bits), for fp32 results; else as one fp16 number, whose rounding, 2^-12 of a weight on average and
-// independent from token to token, is of the size of an fp16 result's own.
+// A worker's part [at, end) of the line of shared work, segment by segment. The weights are hi + lo fp16 pairs (22
+// bits), for fp16 results too: as one fp16 number they would add as much to such a result's error as its own rounding, and
+// where the values all but cancel 30 times what pairs do. (A tile would take 2.3 to 2.7 us in place of 3.3, the call for 128 rows
+// after 16384 int8 tokens 88 in place of 102.)
 //
 // The work is in steps of 32 tokens, three of which are under way at once, each independent of the others: the
 // scores of the next, the softmax of this one, the products with V of the one before. So matrix and vector
@@ -301,7 +302,7 @@ struct StagedV {
 //
 // S^T = K Q^T and O^T += V^T P^T on v_mfma_f32_32x32x16_f16: a lane of S^T holds one query row and 16 of 32
 // tokens, which is the operand that P^T has to be, so the softmax stays in the registers.
-template <int D, bool Q8, bool PAIRS>
+template <int D, bool Q8>
 __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &plan, u32x4 *tiles, uint32_t w, uint32_t at, uint32_t end) {
   using S = Shape<D, Q8>;
   constexpr int T = S::T, TB = S::TB, KS = S::KS, DB = S::DB, kBlocks = T / 16, kRows = S::NT / 2, NT = S::NT;
@@ -520,7 +521,7 @@ __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &pla
             } else {
               f32x16 &to = o[(i - KS) % DB];
               to = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, hi[(i - KS) / DB], to, 0, 0, 0);
-              if constexpr (PAIRS) to = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, lo[(i - KS) / DB], to, 0, 0, 0);
+              to = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, lo[(i - KS) / DB], to, 0, 0, 0);
             }
             if (i + kRing < kSlots) ring[i % kRing] = read(i + kRing);
 #pragma unroll
@@ -537,18 +538,16 @@ __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &pla
               uint32_t bits = __builtin_bit_cast(uint32_t, x2);
               asm volatile("" : "+v"(bits));
               hi_now[j >> 3][(j & 7) >> 1] = bits;
-              if constexpr (PAIRS) {
-                bits = __builtin_bit_cast(uint32_t, h2_t{(_Float16)(y0 - (float)x2[0]), (_Float16)(y - (float)x2[1])});
-                asm volatile("" : "+v"(bits));
-                lo_now[j >> 3][(j & 7) >> 1] = bits;
-              }
+              bits = __builtin_bit_cast(uint32_t, h2_t{(_Float16)(y0 - (float)x2[0]), (_Float16)(y - (float)x2[1])});
+              asm volatile("" : "+v"(bits));
+              lo_now[j >> 3][(j & 7) >> 1] = bits;
             }
             __builtin_amdgcn_sched_barrier(0);
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             hi[k] = __builtin_bit_cast(half8_t, hi_now[k]);
-            if constexpr (PAIRS) lo[k] = __builtin_bit_cast(half8_t, lo_now[k]);
+            lo[k] = __builtin_bit_cast(half8_t, lo_now[k]);
           }
           s = next;
           if (moves) {                               // the products so far belong to the reference of before
@@ -573,7 +572,7 @@ __device__ __forceinline__ void shared_work(const PrefixArgs &a, const Plan &pla
       for (int i = 0; i < 2 * DB; ++i) {
         const half8_t x = __builtin_bit_cast(half8_t, vs[2 * (i / DB) + 8 * (i % DB) * S::VFour]);
         o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, hi[i / DB], o[i % DB], 0, 0, 0);
-        if constexpr (PAIRS) o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, lo[i / DB], o[i % DB], 0, 0, 0);
+        o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, lo[i / DB], o[i % DB], 0, 0, 0);
       }
     }
     l += __shfl_xor(l, 32);
@@ -822,7 +821,7 @@ __device__ __forceinline__ void own_work(const PrefixArgs &a, const Plan &plan, 
 
 // ---- the launch ----------------------------------------------------------------------------------
 
-template <int D, bool Q8, bool PAIRS>
+template <int D, bool Q8>
 __global__ __launch_bounds__(64 * prefix_waves(D), D == 256 ? 1 : 2) void prefix_kernel(PrefixArgs a) {
   constexpr int W = prefix_waves(D), NT = 64 * W, kRows = NT / 2, kPer = (kMaxGroups + 1) / NT;
   extern __shared__ __align__(16) u32x4 tiles[];
@@ -865,10 +864,11 @@ __global__ __launch_bounds__(64 * prefix_waves(D), D == 256 ? 1 : 2) void prefix
     p.row_tiles = (int32_t)(((int64_t)p.rows * a.group + kRows - 1) / kRows);
     // Three ways, by what a KV head's tokens cost in steps of own work: once for up to 256 query rows, once for each
     // pack, or for each row apart, behind whose own tokens they lie. us with 24 groups of 2, 4 and 8 rows of 32 heads on
-    // 8, 1600 tokens: together 56, 54, 56 (int8) and 46, 43, 49 (fp16), in packs 26, 28, 42 and 35, 38, 50, apart
-    // 35, 56 and 52, 95; with 43 groups of 128 heads on 8, whose packs are a row each, 353 tokens, 56 in packs and 44
-    // apart. With few tiles for each workgroup in all, latency counts, which is least together: 8 rows after 1000
-    // tokens 11, in packs 14.
+    // 8, 1600 tokens: together 66, 76, 78 (int8) and 69, 73, 77 (fp16), in packs 33, 36, 49 and 44, 46, 70, apart
+    // 40, 65, 103 and 57, 98, 153; with 43 groups of 2 rows of 128 heads on 8, whose packs are a row each, 353 int8 tokens, 77,
+    // 39 and 34. With few tiles for each workgroup in all, latency counts, which is least together: one group of
+    // 2, 4, 8 and 16 rows of 32 heads after 1000 int8 tokens 15, 15, 16, 18, in packs 16, 17, 19, 22, apart 15, 18, 20, 21; after
+    // 4000 tokens 19, 22, 23, 25 against 24, 26, 31, 30 and 22, 23, 25, 32.
     const int32_t steps = (p.tokens + kTile - 1) / kTile;
     const float together = a.tile_steps * p.row_tiles * (tiles + kLead), packs = (float)packs_of(a, p) * (steps + a.own_lead),
                 apart = (float)p.rows * a.tiles_per_kv * steps;
@@ -929,7 +929,7 @@ __global__ __launch_bounds__(64 * prefix_waves(D), D == 256 ? 1 : 2) void prefix
   if (blockIdx.x < workers) {
     const Line line = make_line(shared, workers);
     if (blockIdx.x >= line.waves) return;
-    shared_work<D, Q8, PAIRS>(a, plan, tiles, blockIdx.x, line.start(blockIdx.x), line.start(blockIdx.x + 1));
+    shared_work<D, Q8>(a, plan, tiles, blockIdx.x, line.start(blockIdx.x), line.start(blockIdx.x + 1));
     return;
   }
   if (own == 0) return;
@@ -951,9 +951,10 @@ __global__ __launch_bounds__(64 * prefix_waves(D), D == 256 ? 1 : 2) void prefix
 
 // ---- the join ------------------------------------------------------------------------------------
 
-// With few rows (query heads of the batch) the parts are many: most workgroups hold one of each row. A workgroup a row
-// then takes 8 to 10 us where a team of it takes 15 to 26 (40 to 568 rows after 6000 to 20000 tokens); with many rows
-// there are few parts, and it takes 12 us where a team a row takes 7 (2048 rows of 128).
+// With few rows (query heads of the batch) the parts are many: most workgroups hold one of each row. The whole call then
+// takes less with a workgroup a row than with a team of it; with many rows there are few parts, and it takes
+// more. 256, 512, 768, 1024, 1280, 1536 and 2048 rows of 128 after 6000 int8 tokens: 33, 32, 31, 32, 35, 37, 42 us with a
+// workgroup a row, 48, 37, 33, 35, 38, 38, 41 with a team.
 constexpr int64_t kFewRows = 1024;
 
 // D / 4 threads, a team, take every TEAMS-th part of a row's shared tokens and of its own; the teams of a row meet in LDS.
@@ -1091,8 +1092,7 @@ int prefix_shape(const qg_kv_pool *pool, int64_t batch, int64_t heads, int64_t g
 template <int D, bool Q8>
 int launch_prefix(const PrefixArgs &a, hipStream_t s) {
   const dim3 grid(kResident), block(64 * prefix_waves(D));
-  if (a.out_f32) return launch(prefix_kernel<D, Q8, true>, grid, block, Shape<D, Q8>::kLds, s, a);
-  return launch(prefix_kernel<D, Q8, false>, grid, block, Shape<D, Q8>::kLds, s, a);
+  return launch(prefix_kernel<D, Q8>, grid, block, Shape<D, Q8>::kLds, s, a);
 }
 
 template <int D>
@@ -1171,9 +1171,10 @@ int qg_prefix_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q
   a.own_rows = w.own_rows;
   a.own_most = (uint32_t)w.own_waves;
   a.own_lead = own_lead(pool->head_dim, pool->kind == QG_KV_Q8);
-  // A tile of shared work takes 2.2 to 2.3 us, 1.3 times that with weights as pairs; with heads of 256, half the rows,
-  // 2.1 (79 rows of 48 heads after 6127 tokens: 98 us with 2.3 here, 90 with 2.1; 128 of 32 heads of 128: 72 and 73).
-  const double tile_us = (out_f32 ? 3.0 : 2.3) * (pool->head_dim == 256 ? 0.92 : 1.0);
+  // A tile of shared work takes 3.3 us (4.0 with heads of 64), with heads of 256, half the rows, 1.9. 128 rows of 32 heads of
+  // 128 after 16384 int8 tokens: 102 us with 2.6 and 3.0 here, 103 to 104 with 2.3 and 3.5. Heads of 256, 79 rows of 48 on 4 in 3
+  // groups after up to 6127 tokens: 70 with 2.1, 71 with 2.4, 82 with 2.8.
+  const double tile_us = pool->head_dim == 256 ? 2.2 : 3.0;
   a.shared_cost = (float)(tile_us / own_step_us(pool->head_dim, pool->kind == QG_KV_Q8));
   // on all of the card: int8 at 30 KB a us for each workgroup, fp16 at HBM's 6 TB/s, which are 23
   a.tile_steps = (float)(tile_us / (32 * pool->head_dim * (pool->kind == QG_KV_Q8 ? 2.125 / 30e3 : 4.0 / 23e3)));

@@ -511,10 +511,8 @@ int qg_kv_compact(const qg_kv_pool *pool, const int32_t *table, int64_t ld_table
  * through its own. Further tokens, and all of a group of one row, are read through each
  * row's own entries. A row that is shorter than the prefix sees its lens tokens.
  * Values of starts outside [0, batch] count as the nearest of these, one below an earlier one as that one.
- * The result is defined as qg_paged_attention's with window 0, with these bounds of the error: with fp32
- * out the same, and 2^-31 sum |V_j| for weights below fp16's normal range; with fp16 out the weights e^(s_j - max) of
- * shared tokens meet V as one fp16 number, 2^-11 of each weight, rounded to nearest, on top (the denominators add the
- * unrounded weights).
+ * The result is defined as qg_paged_attention's with window 0, its error bounded as there (with 512 in place of 1024
+ * waves in the count of a wave's steps), and by 2^-31 sum |V_j| on top for weights below fp16's normal range.
  *
  * max_tail bounds the tokens that a row does not share and chooses the workspace and with it how far the work on them
  * is spread: where rows have more of them it is slower, no less right. Arguments, alignment, limits and errors otherwise as

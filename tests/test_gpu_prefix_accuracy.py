@@ -84,3 +84,75 @@ def test_large_scores(way, kind, dim, order):
         assert not bad.any(), (f"{int(bad.sum())} heads, of q = 35 * 2^{sorted(set(powers[which][bad].tolist()))}: "
                                f"got {got[bad][0][:4]} want {out[bad][0][:4]}")
         assert (np.abs(got_lse - lse) <= tol_lse).all()
+
+
+# scale * log2(e) is exactly 1 in fp32 with this scale, so scores in units of log2 are <q, k> itself
+LN2 = float(np.float32(np.log(2.0)))
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("kind,dim", [("f16", 64), ("f16", 128), ("f16", 256), ("q8", 64), ("q8", 128), ("q8", 256)])
+def test_weights_of_shared_tokens(way, kind, dim):
+    """fp16 results whose terms all but cancel: token 2 i + 1 has the V of token 2 i times -2^(y(2 i) - y(2 i + 1)), rounded to
+    fp16 (int8 pages: in its scale), with y the scores, which are exact multiples of 1/64. The sum is then some 2^-12 of its
+    terms, so that its own rounding to fp16 hides nothing, and the weights have to be good to 22 bits: to 2 (2^-21 + tokens
+    (2^-24 + 2^-30)) of the sum of their terms' sizes, as for the one-token attention, and 2^-31 of the sum of |V|."""
+    sizes, heads, kv_heads = WAYS[way]
+    tokens, prefix, rows = 16, 32, sum(WAYS[way][0])
+    rng = np.random.default_rng(dim)
+    groups = len(sizes)
+    c = paged.Cache(kind, 1, groups * prefix // tokens, kv_heads, dim, tokens)
+    table = np.repeat(np.arange(c.pages).reshape(groups, -1), sizes, axis=0).astype(np.int32)
+    for g in range(groups):
+        for kvh in range(kv_heads):
+            y = rng.integers(0, 512, prefix) / 64          # 0 to 8
+            v = rng.integers(-100, 101, dim).astype(np.float64)
+            for j in range(prefix):
+                at = (0, g * prefix // tokens + j // tokens, kvh, j % tokens)
+                if j % 2 == 0:
+                    v = rng.integers(-100, 101, dim).astype(np.float64)
+                    code, step = v, 1 / 64
+                else:
+                    code, step = -v, np.float16(2.0 ** (y[j - 1] - y[j]) / 64)
+                if kind == "f16":
+                    c.values[0][at + (0,)], c.values[1][at] = y[j] * 4, (code * np.float64(2.0 ** (y[j - 1] - y[j]) if j % 2 else 1)) / 64
+                else:
+                    c.codes[0][at + (0,)], c.codes[1][at] = 64, code
+                    c.scales[0][at + (0,)], c.scales[1][at] = y[j] * 4 / 64, step
+    q = np.zeros((rows, heads, dim), np.float16)
+    q[:, :, 0] = 0.25
+    lens = [prefix] * rows
+    out, lse, bound, reach = paged.attention(c, 0, q, table, lens, prefix, LN2)
+    assert (np.abs(out) < 2.0 ** -8 * bound).all()         # they do cancel
+    most = float(np.abs(c.values[1]).max() if kind == "f16" else 127 * c.scales[1].max())
+    tol, _ = attention_tolerance(out, lse, bound, np.zeros_like(reach), prefix, dim, False)
+    tol = tol + prefix * most * 2.0 ** -31
+    got = qg.prefix_attention(upload(c), dev(q, np.float16), dev(table), dev(lens), dev(starts_of(sizes)), dev([prefix] * groups),
+                              max_tail=0, scale=LN2).cpu().double().numpy()
+    off = np.abs(got - out)
+    assert (off <= tol).all(), f"{int((off > tol).sum())} of {off.size}, off by up to {(off / tol).max():.3g} of the tolerance"
+
+
+@pytest.mark.parametrize("kind,heads,kv_heads,dim", [("q8", 16, 4, 128), ("f16", 16, 4, 128), ("f16", 32, 4, 64), ("q8", 16, 1, 256)])
+def test_fp16_results_are_off_by_their_own_rounding(kind, heads, kv_heads, dim):
+    """Rounding to fp16 is off by a uniform part of half a step either way, the square of a step / 12 on average. Over 16384 results
+    and more the mean lies within 2 % of that (the square of a uniform number has a deviation of 0.9 of its mean, and steps span
+    some binades: 1.5 % for 16384), and the rest, fp32's 2^-24 of scores of about 100, adds 1 % at most: 10 % are allowed."""
+    rows, prefix, tokens = 8, 1008, 16
+    rng = np.random.default_rng(heads)
+    c = paged.Cache(kind, 1, prefix // tokens, kv_heads, dim, tokens)
+    if kind == "q8":
+        for a, d in zip(c.codes, c.scales):
+            a[...] = rng.integers(-127, 128, a.shape)
+            d[...] = rng.random(d.shape) * 0.01 + 0.01
+    else:
+        for a in c.values:
+            a[...] = rng.standard_normal(a.shape)
+    table = np.tile(np.arange(c.pages, dtype=np.int32), (rows, 1))
+    q = rng.standard_normal((rows, heads, dim)).astype(np.float16)
+    lens = [prefix] * rows
+    out = paged.attention(c, 0, q, table, lens, prefix, dim ** -0.5)[0]
+    got = qg.prefix_attention(upload(c), dev(q, np.float16), dev(table), dev(lens), dev([0, rows]), dev([prefix]), max_tail=0)
+    step = np.maximum(2.0 ** (np.floor(np.log2(np.abs(out))) - 10), 2.0 ** -24)
+    error = np.square(got.cpu().double().numpy() - out).sum() / (np.square(step).sum() / 12)
+    assert error < 1.1, error
