@@ -165,7 +165,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
     } else if (weight) {
       const float mean = ss * (1.0f / D) + a.eps;
       float inv = __builtin_amdgcn_rsqf(mean);       // to one step, and to half of one by
-      inv = __builtin_fmaf(0.5f * inv, __builtin_fmaf(-(mean * inv), inv, 1.0f), inv);
+      const float rest = __builtin_fmaf(-(mean * inv), inv, 1.0f);
+      inv = mean < INFINITY ? __builtin_fmaf(0.5f * inv, rest, inv) : inv;   // of an infinite head, zero as it is
       float w[8];
       unpack8(*reinterpret_cast<const u32x4 *>(weight + e), w);
 #pragma unroll
