@@ -655,7 +655,8 @@ def kv_extend(pool, table, lens, refs, add, slots: int, granted=None, starts=Non
     the tokens that each row got (add[r], or 0), and the slot map of `slots` places that kv_append
     takes, row after row with the tokens asked for; the places of a row that got none hold -1, as do
     those past the last row's. table, lens and refs are updated in place. A row gets none when the slots,
-    its table entries or the free pages (the rows before it come first) do not suffice, or when other rows hold the
+    its table entries or the free pages (the rows before it come first, those that the free pages did not suffice for among
+    them: one request that is too large leaves no page for the rows behind it) do not suffice, or when other rows hold the
     partly filled page that its tokens would go to. starts, int32 [rows + 1], receives each row's first slot
     if given; what else is not given is allocated as views of one buffer when none of it is."""
     if stream is not None or _device_now() != pool._index:

@@ -56,7 +56,7 @@ constexpr int32_t kSamples = 4096;                  // entries of a sum that a s
 struct ExtendArgs {
   int32_t *table;
   int64_t ld;
-  int32_t rows, pages, tok_shift;
+  int32_t rows, tok_shift;
   int64_t capacity;              // tokens of a row
   int32_t *lens, *refs;
   int32_t num_pages, blocks;
@@ -299,7 +299,6 @@ int qg_kv_extend(const qg_kv_pool *pool, int32_t *table, int64_t ld_table, int64
   a.table = table;
   a.ld = ld_table;
   a.rows = (int32_t)table_rows;
-  a.pages = (int32_t)table_pages;
   a.tok_shift = __builtin_ctz(pool->page_tokens);
   a.capacity = row_capacity(pool, table_pages);
   a.lens = lens;

@@ -535,8 +535,11 @@ int qg_prefix_attention(const qg_kv_pool *pool, int64_t layer, const uint16_t *q
  *   N_r exceeds slots, or lens[r] + add[r] the row's table_pages * T tokens, or
  *   its last page is partly filled and not held by this row alone (refs 1): appending would write into
  *     another row's tokens (qg_kv_fork copies such a page), or
- *   it lacks pages and these, with those lacked by the rows before it that none of this refuses, are more
- *     than there are free pages (refs 0 or less).
+ *   it lacks pages and these, with those lacked by the rows before it that neither of the two refuses, are more
+ *     than there are free pages (refs 0 or less). A row that this refuses counts for the rows behind it, too: after one
+ *     request for more pages than are free, no later row that lacks a page is served, though pages are left (3 free
+ *     pages of 16 tokens, empty rows that ask for 80 and 32: both get none). A caller that wants later rows served asks for
+ *     no more than there is, or for such requests behind the others.
  * A served row's new entries name free pages, in ascending order over all rows, whose refs become 1; lens[r] grows
  * by add[r], granted[r] (int32 [table_rows]) is add[r], and slot i of its tokens holds seqs r and
  * positions the token's place in the row: what qg_kv_append takes. A row that is not served stays as it was,
