@@ -728,6 +728,7 @@ int qg_rope_freqs(int kind, int64_t rotary_dim, double base, double scale, doubl
   if (bands && !(std::isfinite(context) && context > 0 && std::isfinite(high) && low > 0 && low < high)) return QG_ERR_RANGE;
   const double r = (double)rotary_dim, turn = 2 * 3.14159265358979323846;
   if (kind == QG_ROPE_BASE) base *= std::pow(scale, r / (r - 2));
+  if (!(std::isfinite(base) && base > 0)) return QG_ERR_RANGE;
   // the pair, as a real number, that makes t turns in the context
   const auto pair = [&](double t) { return r * std::log(context / (t * turn)) / (2 * std::log(base)); };
   const double a = bands ? std::max(std::floor(pair(high)), 0.0) : 0, b = bands ? std::min(std::ceil(pair(low)), r - 1) : 0;
@@ -739,6 +740,7 @@ int qg_rope_freqs(int kind, int64_t rotary_dim, double base, double scale, doubl
     if (kind == QG_ROPE_PARTS) g = 1 - ((double)j - a) / std::max(b - a, 0.001);
     g = std::min(std::max(g, 0.0), 1.0);
     freqs[j] = g == 1 ? f : f * (g + (1 - g) / scale);
+    if (!std::isfinite(freqs[j])) return QG_ERR_RANGE;
   }
   return QG_OK;
 }

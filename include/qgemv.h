@@ -594,7 +594,7 @@ typedef struct qg_rotary {
  *   QG_ROPE_PARTS   the same with 1 - g = clamp((j - a) / (b - a), 0, 1), a and b the pairs (as real numbers, rounded
  *                   down and up, at least 0 and at most rotary_dim - 1) that make `high` and `low` turns; b - a at least 0.001
  * scale is read by all but QG_ROPE_PLAIN, context, low and high by the last two; base > 1, scale > 0, context > 0 and
- * 0 < low < high, all finite, else QG_ERR_RANGE. rotary_dim is a positive even number, above 2 for QG_ROPE_BASE.
+ * 0 < low < high, all finite, as are the raised base and the frequencies, else QG_ERR_RANGE. rotary_dim is a positive even number, above 2 for QG_ROPE_BASE.
  * Errors: QG_ERR_NULL, QG_ERR_FORMAT (kind), QG_ERR_SHAPE, QG_ERR_RANGE. */
 typedef enum qg_rope_kind { QG_ROPE_PLAIN = 0, QG_ROPE_LINEAR = 1, QG_ROPE_BASE = 2, QG_ROPE_TURNS = 3, QG_ROPE_PARTS = 4 } qg_rope_kind;
 int qg_rope_freqs(int kind, int64_t rotary_dim, double base, double scale, double context, double low, double high,
