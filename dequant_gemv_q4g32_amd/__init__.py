@@ -816,6 +816,8 @@ def kv_append_rope(pool, table, rotary, q, k, v, positions, seqs=None, q_out=Non
     if q is not None:
         at, ld, heads = _head_rows(pool._index, "q", q, count, dim)
         q_out, to, ldo = _heads_out(pool._index, "q_out", q_out, q, count, heads, dim)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
     _check(_lib.qg_kv_append_rope(pool._ref, layer, *_table(pool, table), rotary._ref, heads, at, ld,
                                   *_rows16(pool, "k", k, count), *_rows16(pool, "v", v, count),
                                   None if seqs is None else _ints(pool, "seqs", seqs, count),
