@@ -3,9 +3,9 @@
 //
 // A head x of D elements becomes y = x / sqrt(mean x^2 + eps) * w where it has weights (else y = x), and
 // the pair (y1, y2) with frequency f becomes factor * (y1 cos t - y2 sin t, y2 cos t + y1 sin t), t =
-// position * f. All of it in fp32 with one rounding to fp16 at the end, but in fp64 for int8 keys and the angle: a position
-// of 100000 times a frequency near 1 leaves fp32 an error of 0.004 radians. Its reduction to a part of a turn, cosine
-// and sine are made once for all heads of a token.
+// position * f. All of it in fp32 with one rounding to fp16 at the end, but in fp64 for int8 keys, the angle, and its cosine and
+// sine: a position of 100000 times a frequency near 1 leaves fp32 an error of 0.004 radians. These are made once for all
+// heads of a token.
 //
 // A lane takes 8 elements of a head (16 bytes), D / 8 lanes a head, so that a norm is a sum over 8 to 32
 // neighbouring lanes and a pair's other half is 8 elements of another lane of the same head.
@@ -69,10 +69,11 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// A key on its way to int8, in fp64: its largest element of 32 decides the codes of all of them, and where that is
-// rounded to fp16 the other way, or a code lies near a tie, a code changes, by up to a hundredth of the largest. In fp32
-// one key element in 10000 is rounded the other way. A decode step takes 0.5 us more for it; for fp16 results, where it
-// would be half a step in one of 10000, it would take 82 us in place of 67 (8192 tokens).
+// A key on its way to int8, in fp64, then rounded to fp32 and to fp16: its largest element of 32 decides the codes of all of
+// them, and where that is rounded to fp16 the other way, or a code lies near a tie, a code changes, by up to a hundredth
+// of the largest. The rounding to fp32 does that to one element of 2^14, and one code of 200000; in fp32 throughout it would be
+// another element in 10000, and which ones would follow from the order of the sums. A decode step takes 0.5 us more for it; for
+// fp16 results, where it would be half a step in one of 10000, it would take 82 us in place of 67 (8192 tokens).
 template <int D>
 __device__ __forceinline__ void key_head(float *y, const float *z, const uint16_t *weight, int away, float eps, const double2_t *turn,
                                          bool rotated, bool interleaved, bool second, int e, int half) {

@@ -569,8 +569,8 @@ int qg_kv_trim(const qg_kv_pool *pool, int32_t *table, int64_t ld_table, int64_t
  * for the pairs j < rotary_dim / 2: (i, k) = (j, j + rotary_dim / 2), or (2 j, 2 j + 1) with interleaved
  * != 0. Elements from rotary_dim on are not rotated. freqs, fp64 [rotary_dim / 2] on the device (8-byte
  * aligned), are radians a token: qg_rope_freqs makes them, scaled for long contexts if need be, and factor (1 where
- * nothing is to be changed) is the factor of the attention's logits that goes with some scalings. The angle
- * is fp64 and right at any position, the rest fp32 with one rounding to fp16. rotary_dim is a multiple of 16,
+ * nothing is to be changed) is the factor of the attention's logits that goes with some scalings. The angle, its
+ * cosine and sine are fp64 and right at any position, the rest is fp32 with one rounding to fp16. rotary_dim is a multiple of 16,
  * at most head_dim; head_dim is 64, 128 or 256; eps is at least the smallest normal fp32 (read where there is
  * a weight), factor finite, else QG_ERR_RANGE. */
 typedef struct qg_rotary {
@@ -611,8 +611,9 @@ int qg_qk_rope(const qg_rotary *rotary, int64_t head_dim, int64_t heads, int64_t
                uint16_t *k_out, int64_t ld_k_out, void *stream);
 
 /* qg_qk_rope and qg_kv_append in one pass: the queries into q_out, the keys (rounded to fp16) and the values v into
- * `layer` of the pool: for fp16 pages the same bytes as by the two calls; for int8 pages keys are computed in fp64
- * before their rounding to fp16, which is the other way than qg_qk_rope's in one of some 10000 elements. A row with a position below 0 is skipped, one whose
+ * `layer` of the pool: for fp16 pages the same bytes as by the two calls; for int8 pages keys are computed in fp64 and
+ * rounded to fp32, then to fp16, which in one of some 10000 elements is the other way than qg_qk_rope's, and in one of 16384
+ * than one rounding. A row with a position below 0 is skipped, one whose
  * place is no page (see qg_kv_append) gives its queries only. What is cached, rotated keys among it, is finite.
  * heads may be 0. q_out may be q as above, and overlaps nothing else that the call reads. Sizes and alignment of
  * qg_qk_rope for q and q_out, of qg_kv_append for k and v; errors of both. */
