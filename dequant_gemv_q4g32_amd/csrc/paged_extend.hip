@@ -3,7 +3,7 @@
 //
 // Little is moved here; every launch is a chain of dependent loads (lengths, the last page's entry and
 // its count, the counts of all pages) and prefix sums. extend reads refs once and writes what changes. So the time is
-// latency: trim 3 us, extend's launches 4.2 and 7 us with 64 rows and 4096 pages, 4.6 and 9 with 1000 and 262144.
+// latency: trim 3 us, extend's launches 4.4 and 7.4 us with 64 rows and 4096 pages, 4.8 and 9 with 1000 and 262144.
 #include <hip/hip_runtime.h>
 
 #include "../../include/qgemv.h"

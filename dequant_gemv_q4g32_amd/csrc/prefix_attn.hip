@@ -7,7 +7,7 @@
 // second kind also takes groups of few rows, 16 query rows (rows by heads) in place of a row's heads, or
 // their rows one by one. A second launch joins the parts.
 //
-// Measured: 128 rows of 32 heads on 8 of 128 after 16384 shared int8 tokens, up to 1024 of their own, take 93 and 8 us; a
+// Measured: 128 rows of 32 heads on 8 of 128 after 16384 shared int8 tokens, up to 1024 of their own, take 90 and 8 us; a
 // pass over the shared tokens for each row would read 4.6 GB, 670 us at HBM's rate. Shared work reaches 530 to 650
 // TFLOP/s on its workgroups, the weights' second halves not counted; a large library product 1150 on all. Of a tile's 3.3 us
 // the matrix instructions are busy for 1.5, the vector instructions about as long, LDS for 0.9, and the two waves of a SIMD do
