@@ -512,7 +512,8 @@ int qg_kv_compact(const qg_kv_pool *pool, const int32_t *table, int64_t ld_table
  * row's own entries. A row that is shorter than the prefix sees its lens tokens.
  * Values of starts outside [0, batch] count as the nearest of these, one below an earlier one as that one.
  * The result is defined as qg_paged_attention's with window 0, its error bounded as there (with 512 in place of 1024
- * waves in the count of a wave's steps), and by 2^-31 sum |V_j| on top for weights below fp16's normal range.
+ * waves in the count of a wave's steps, fewer where max_tail does not hold), and by 2^-31 sum |V_j| on top for weights
+ * below fp16's normal range.
  *
  * max_tail bounds the tokens that a row does not share and chooses the workspace and with it how far the work on them
  * is spread: where rows have more of them it is slower, no less right. Arguments, alignment, limits and errors otherwise as
